@@ -552,6 +552,122 @@ q8_status q8_selftest_wait_timeout(q8_gemm_kernel kernel, const int8_t* qa, cons
                                    int64_t M, int64_t N, int64_t K, int32_t* acc,
                                    int64_t wait_cycles, q8_stream_t stream);
 
+/*
+ * Float8 operands with a scale for each block of 128, and layers of routed experts.
+ *
+ * A float8 tensor is a byte matrix of e4m3 codes (largest value 448) with fp32 scales: activations
+ * qa[M, K] have one scale for each row and block of 128 along K, sa[M, KB] with KB = ceil(K / 128);
+ * weights qw[N, K] one for each 128 x 128 block, sw[ceil(N / 128), KB]. The last block of a dimension may be
+ * short. K is a multiple of 16. What a code stands for is its value times its block's scale.
+ *
+ * Unlike the int8 quantizers, these define what happens to NaN and infinities (below): a broken
+ * value is passed on, never turned into a finite one.
+ */
+
+/* Type of float tensors read or written by these operators. */
+typedef enum q8_float_type { Q8_F32 = 0, Q8_BF16 = 1, Q8_F16 = 2 } q8_float_type;
+
+/* Scores of a router: softmax over the experts, or a sigmoid of each. */
+typedef enum q8_score { Q8_SOFTMAX = 0, Q8_SIGMOID = 1 } q8_score;
+
+/*
+ * Dynamic activation quantization to float8. For each row and block of 128 along K:
+ *   a = max(max |x|, 1e-30),  s = a / 448,  q = e4m3(x * (448 / a)),
+ * each operation rounded to nearest even in fp32, the code rounded once to e4m3. A block with a NaN or
+ * an infinity stands for NaN throughout (its scale is NaN or inf).
+ *
+ * x     : [M, K] of `type`, rows ldx elements apart (ldx >= K, rows 16-byte aligned).
+ * slots : NULL, or int32 [M, top_k]: row m is written to the rows slots[m, j] of q and s instead of row
+ *         m (the tokens of a routed layer, in expert order; q8_moe_plan). Slots outside
+ *         [0, rows_out) are skipped. The valid ones have to differ.
+ * top_k, rows_out : the slots of a row (1..32) and the rows of q and s; 0 and M when slots is NULL.
+ * q, s  : e4m3 codes [rows_out, K] and fp32 scales [rows_out, KB], written.
+ * Errors: Q8_ERR_UNSUPPORTED for K % 16 != 0, a row pitch that is not a multiple of 16 bytes, more than
+ * 32 slots a row, sizes of 2^31 and more, or 2^31 and more blocks.
+ */
+q8_status q8_quantize_fp8(const void* x, q8_float_type type, int64_t M, int64_t K, int64_t ldx,
+                          const int32_t* slots, int64_t top_k, int64_t rows_out, uint8_t* q, float* s,
+                          q8_stream_t stream);
+
+/*
+ * Gated activation and quantization in one pass, between the two products of a gated layer:
+ *   x[m, i] = h[m, I + i] * g / (1 + exp(-g)),  g = h[m, i],   then q and s of x as q8_quantize_fp8.
+ * The activation is computed in fp32, off by a few units of its last place.
+ * h    : [M, 2 I] of `type` (gates, then the values they gate), rows ldh elements apart. I % 16 == 0.
+ * q, s : [M, I] and [M, ceil(I / 128)], written. Errors as q8_quantize_fp8.
+ */
+q8_status q8_swiglu_quantize_fp8(const void* h, q8_float_type type, int64_t M, int64_t I, int64_t ldh, uint8_t* q,
+                                 float* s, q8_stream_t stream);
+
+/*
+ * Weight quantization (offline): the rule of q8_quantize_fp8 over 128 x 128 blocks of each of E
+ * matrices [N, K] (E = 1: one layer). w dense, of `type`; qw [E, N, K], sw [E, ceil(N / 128), KB].
+ */
+q8_status q8_quantize_weight_fp8(const void* w, q8_float_type type, int64_t E, int64_t N, int64_t K, uint8_t* qw,
+                                 float* sw, q8_stream_t stream);
+
+/*
+ * Product of float8 matrices with block scales:
+ *   y[m, n] = sum_b sa[m, b] sw[n / 128, b] sum_{k in block b} qa[m, k] qw[n, k].
+ * The inner sums are the tensor core's, in fp32; the sum over blocks is one fp32 multiply-add a block;
+ * y is rounded once, to `type`. The order of every sum depends on the sizes alone, so that the same
+ * call gives the same bits. y : [M, N], dense. K = 0 gives zeros.
+ * Errors: Q8_ERR_UNSUPPORTED for K % 16 != 0 or sizes of 2^31 and more.
+ */
+q8_status q8_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw, int64_t M, int64_t N,
+                      int64_t K, void* y, q8_float_type type, q8_stream_t stream);
+
+/*
+ * The same product for routed experts: rows offsets[e] .. offsets[e + 1] - 1 of qa, sa and y belong to
+ * expert e and use qw[e], sw[e] of qw[E, N, K], sw[E, ceil(N / 128), KB]. The offsets are read on the
+ * device (no synchronisation; the call can be captured in a graph); an expert may have no row.
+ * offsets : int32 [E + 1], not falling, offsets[0] >= 0. Values past `rows` are cut to it; rows before
+ *           offsets[0] or from offsets[E] on are not written. Overlapping ranges are not defined.
+ * rows    : the rows of qa, sa and y. E <= 512, K >= 16 (else Q8_ERR_UNSUPPORTED).
+ */
+q8_status q8_gemm_fp8_grouped(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
+                              const int32_t* offsets, int64_t rows, int64_t E, int64_t N, int64_t K, void* y,
+                              q8_float_type type, q8_stream_t stream);
+
+/*
+ * Routing to experts. For each token, from its logits l[E]: the scores are p = softmax(l) or
+ * sigmoid(l); top_k experts are chosen and written in falling order, ties to the lowest index.
+ *  - Without a bias experts are ordered by l, with one by p + bias (compared as 64 bits give it); the bias
+ *    takes part in the choice only.
+ *  - n_group > 1: the experts form n_group groups of E / n_group neighbours, and only those of the
+ *    topk_group best groups can be chosen. A group is ranked by its best expert, or, with a bias, by the sum
+ *    of its two best.
+ *  - weights = p of the chosen, divided by their sum if renorm (0 where that is 0), times scale.
+ *  - An expert whose logit is -inf or NaN is masked: its score is 0 and it is never chosen. A token
+ *    that has too few experts left gets idx -1 and weight 0 in the places that remain. A logit of +inf
+ *    counts as the largest fp32 value.
+ *
+ * logits  : [T, E] of `type`, rows ldl elements apart. bias : fp32 [E] or NULL.
+ * idx     : int32 [T, top_k], weights : fp32 [T, top_k], written.
+ * Limits  : E <= 512, top_k <= 32, n_group <= 32, else Q8_ERR_UNSUPPORTED.
+ */
+q8_status q8_moe_route(const void* logits, q8_float_type type, int64_t T, int64_t E, int64_t ldl, int64_t top_k,
+                       q8_score score, const float* bias, int64_t n_group, int64_t topk_group, int renorm,
+                       float scale, int32_t* idx, float* weights, q8_stream_t stream);
+
+/*
+ * The rows of each expert: a stable sort of the T * top_k choices by expert.
+ * idx     : int32 [T, top_k]; values outside [0, E) are nobody's.
+ * offsets : int32 [E + 1], written: expert e has rows offsets[e] .. offsets[e + 1] - 1.
+ * slots   : int32 [T, top_k], written: the row of each choice, in the order of (expert, token, place); -1
+ *           for nobody's. E <= 512, top_k <= 32, T * top_k < 2^31.
+ */
+q8_status q8_moe_plan(const int32_t* idx, int64_t T, int64_t top_k, int64_t E, int32_t* offsets, int32_t* slots,
+                      q8_stream_t stream);
+
+/*
+ * The weighted sum of the experts' answers: y[t] = sum_j weights[t, j] h[slots[t, j]] in fp32, in the
+ * order of j, rounded once. Slots outside [0, rows) add nothing; a token without any gets zeros.
+ * h : [rows, N], y : [T, N], dense, of `type`; N * its size a multiple of 16 bytes. top_k <= 32.
+ */
+q8_status q8_moe_combine(const void* h, q8_float_type type, int64_t rows, int64_t N, const int32_t* slots,
+                         const float* weights, int64_t T, int64_t top_k, void* y, q8_stream_t stream);
+
 /* The kernel q8_gemm_dequant would run for this shape (never Q8_GEMM_AUTO). */
 q8_gemm_kernel q8_gemm_pick(int64_t M, int64_t N, int64_t K);
 
@@ -564,7 +680,7 @@ const char* q8_status_string(q8_status status);
  * gave up: one byte per kernel family (bits 0..7: the single-CTA tcgen05 kernel,
  * and bit 7 the fused RMSNorm quantizer's wait for a row copy; bits 8..15: the
  * tcgen05 decode kernel; bits 16..23: the warp-MMA decode kernels; bits 24..31:
- * the CTA-pair kernel), within a byte one bit per role (1 TMA producer,
+ * the CTA-pair kernel and the float8 products), within a byte one bit per role (1 TMA producer,
  * 2 converters / compute warps waiting for loaded data, 4 converters waiting
  * for a free stage, 8 MMA issuer waiting for converted data, 16 MMA issuer
  * waiting for a free accumulator, 32 accumulator drain, 64 the odd CTA's relay).

@@ -15,6 +15,17 @@ CPU fallback; if the library is missing or a call fails, an exception says so.
   q8_quantize_weight_mx(w, group) -> qw, sf;  q8_gemm_mx(qa, s_a, qw, sf, group, ...)   (block-scaled weights)
   q8_linear(a, qw, s_w, colsum)                       -> y   (quantize A, then GEMM)
   q8_linear_host(a_host, qw, s_w, colsum, y_host)      (host buffers; copies overlapped with the device work)
+
+Float8 (e4m3) operands with a scale for each block of 128, and layers of routed experts:
+
+  q8_quantize_fp8(x, slots=None)          -> qa, sa    (or each row to the slots of its experts)
+  q8_swiglu_quantize_fp8(h)               -> qa, sa    (gated activation + quantize)
+  q8_quantize_weight_fp8(w)               -> qw, sw    ([N, K] or [E, N, K])
+  q8_gemm_fp8(qa, sa, qw, sw)             -> y
+  q8_gemm_fp8_grouped(qa, sa, qw, sw, offsets) -> y    (row ranges of experts)
+  q8_moe_route(logits, top_k, ...)        -> idx, weights
+  q8_moe_plan(idx, n_experts)             -> offsets, slots
+  q8_moe_combine(h, slots, weights)       -> y
 """
 from __future__ import annotations
 
@@ -29,7 +40,8 @@ __all__ = [
     "Q8Error", "load", "q8_quantize_act", "q8_rmsnorm_quantize_act", "q8_quantize_weight", "q8_colsum", "q8_gemm_dequant",
     "q8_gemm_epilogue", "q8_gemm_s32", "q8_linear", "q8_quantize_weight_int4", "q8_colsum_int4", "q8_gemm_w4a8",
     "q8_gemm_w4a8_s32", "q8_quantize_weight_mx", "q8_gemm_mx", "q8_quantize_act_f16", "q8_quantize_act_dual", "q8_gemm_f16a", "q8_gemm_f16a_s32", "q8_linear_host", "q8_linear_host_workspace", "q8_gemm_workspace", "q8_gemm_pick", "q8_launch_count", "q8_device_error",
-    "q8_selftest_wait_timeout", "KERNELS",
+    "q8_selftest_wait_timeout", "KERNELS", "q8_quantize_fp8", "q8_swiglu_quantize_fp8", "q8_quantize_weight_fp8",
+    "q8_gemm_fp8", "q8_gemm_fp8_grouped", "q8_moe_route", "q8_moe_plan", "q8_moe_combine",
 ]
 
 LIB_PATH = _build.LIB
@@ -95,7 +107,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.q8_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     lib.q8_launch_count.argtypes = []
     lib.q8_launch_count.restype = ctypes.c_uint64
-    for name in ("q8_quantize_act", "q8_rmsnorm_quantize_act", "q8_quantize_weight", "q8_colsum", "q8_gemm_dequant",
+    lib.q8_quantize_fp8.argtypes = [p, i32, i64, i64, i64, p, i64, i64, p, p, p]
+    lib.q8_swiglu_quantize_fp8.argtypes = [p, i32, i64, i64, i64, p, p, p]
+    lib.q8_quantize_weight_fp8.argtypes = [p, i32, i64, i64, i64, p, p, p]
+    lib.q8_gemm_fp8.argtypes = [p, p, p, p, i64, i64, i64, p, i32, p]
+    lib.q8_gemm_fp8_grouped.argtypes = [p, p, p, p, p, i64, i64, i64, i64, p, i32, p]
+    lib.q8_moe_route.argtypes = [p, i32, i64, i64, i64, i64, i32, p, i64, i64, i32, ctypes.c_float, p, p, p]
+    lib.q8_moe_plan.argtypes = [p, i64, i64, i64, p, p, p]
+    lib.q8_moe_combine.argtypes = [p, i32, i64, i64, p, p, i64, i64, p, p]
+    for name in ("q8_quantize_fp8", "q8_swiglu_quantize_fp8", "q8_quantize_weight_fp8", "q8_gemm_fp8",
+                 "q8_gemm_fp8_grouped", "q8_moe_route", "q8_moe_plan", "q8_moe_combine",
+                 "q8_quantize_act", "q8_rmsnorm_quantize_act", "q8_quantize_weight", "q8_colsum", "q8_gemm_dequant",
                  "q8_gemm_dequant_ex", "q8_gemm_dequant_ws", "q8_gemm_epilogue_ex", "q8_gemm_s32_ex", "q8_quantize_weight_int4",
                  "q8_colsum_int4", "q8_gemm_w4a8_ex", "q8_gemm_w4a8_s32_ex", "q8_quantize_weight_mx", "q8_gemm_mx_ex",
                  "q8_gemm_w4a8_ws", "q8_gemm_mx_ws", "q8_linear_ws", "q8_quantize_act_dual",
@@ -600,4 +622,211 @@ def q8_gemm_mx(qa, s_a, qw, sf, group: int = 32, bias=None, out_dtype=torch.floa
     _check(load().q8_gemm_mx_ex(_ptr(qa), _ptr(s_a), ga, _ptr(qw), _ptr(sf), group, _ptr(bias), M, N, K,
                                 OUT_TYPES[out_dtype], _ptr(out), ctypes.c_float(out_scale or 0.0), KERNELS[kernel],
                                 _stream(stream)), "q8_gemm_mx")
+    return out
+
+
+# ------------------------------------------------------------- float8 operands, routed experts
+
+FLOAT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+FP8_BLOCK = 128
+
+
+def _cdiv(a: int, b: int) -> int:
+    return -(-a // b)
+
+
+def _same_device(first: torch.Tensor, **others):
+    """Every tensor on the device of the first, which has to be the current one (the calls go to its stream)."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """The row pitch of a 2-D tensor of floats with unit column stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in FLOAT_TYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.stride(0)
+
+
+def _shaped(t: torch.Tensor, dtype, shape, name: str):
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _fp8_out(rows: int, K: int, q, s, device):
+    KB = _cdiv(K, FP8_BLOCK)
+    q = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device) if q is None else q
+    s = torch.empty((rows, KB), dtype=torch.float32, device=device) if s is None else s
+    _shaped(q, torch.float8_e4m3fn, (rows, K), "q")
+    _shaped(s, torch.float32, (rows, KB), "s")
+    return q, s
+
+
+def q8_quantize_fp8(x: torch.Tensor, slots=None, rows: int | None = None, q=None, s=None, stream=None):
+    """Float8 codes and scales (one for each row and block of 128) of x[M, K] (fp32, bf16 or fp16; rows may be
+    strided). slots int32 [M, k]: row m goes to the rows slots[m] of the result instead (skipped where
+    outside), which has `rows` rows (default M * k). Returns (q float8_e4m3fn [rows, K], s fp32 [rows, ceil(K / 128)])."""
+    ldx = _rows(x, "x")
+    M, K = x.shape
+    top_k = 0
+    if slots is not None:
+        _need(slots, torch.int32, "slots", 2)
+        if slots.shape[0] != M:
+            raise ValueError("slots must have a row for each row of x")
+        top_k = slots.shape[1]
+        rows = M * top_k if rows is None else rows
+    elif rows is not None and rows != M:
+        raise ValueError("rows goes with slots")
+    else:
+        rows = M
+    q, s = _fp8_out(rows, K, q, s, x.device)
+    _same_device(x, slots=slots, q=q, s=s)
+    _check(load().q8_quantize_fp8(_ptr(x), FLOAT_TYPES[x.dtype], M, K, ldx, _ptr(slots), top_k, rows, _ptr(q), _ptr(s),
+                                  _stream(stream)), "q8_quantize_fp8")
+    return q, s
+
+
+def q8_swiglu_quantize_fp8(h: torch.Tensor, q=None, s=None, stream=None):
+    """Codes and scales of silu(h[:, :I]) * h[:, I:], h[M, 2 I] (rows may be strided)."""
+    ldh = _rows(h, "h")
+    M = h.shape[0]
+    if h.shape[1] % 2:
+        raise ValueError("h must have an even number of columns")
+    I = h.shape[1] // 2
+    q, s = _fp8_out(M, I, q, s, h.device)
+    _same_device(h, q=q, s=s)
+    _check(load().q8_swiglu_quantize_fp8(_ptr(h), FLOAT_TYPES[h.dtype], M, I, ldh, _ptr(q), _ptr(s), _stream(stream)),
+           "q8_swiglu_quantize_fp8")
+    return q, s
+
+
+def q8_quantize_weight_fp8(w: torch.Tensor, qw=None, sw=None, stream=None):
+    """Codes and 128 x 128 block scales of w[N, K] or of the matrices w[E, N, K] (offline)."""
+    if not isinstance(w, torch.Tensor) or w.dtype not in FLOAT_TYPES:
+        raise TypeError("w must be a float32, bfloat16 or float16 tensor")
+    _need(w, w.dtype, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    N, K = w.shape[-2:]
+    E = w.shape[0] if w.dim() == 3 else 1
+    scales = (*w.shape[:-2], _cdiv(N, FP8_BLOCK), _cdiv(K, FP8_BLOCK))
+    qw = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device) if qw is None else qw
+    sw = torch.empty(scales, dtype=torch.float32, device=w.device) if sw is None else sw
+    _shaped(qw, torch.float8_e4m3fn, w.shape, "qw")
+    _shaped(sw, torch.float32, scales, "sw")
+    _same_device(w, qw=qw, sw=sw)
+    _check(load().q8_quantize_weight_fp8(_ptr(w), FLOAT_TYPES[w.dtype], E, N, K, _ptr(qw), _ptr(sw), _stream(stream)),
+           "q8_quantize_weight_fp8")
+    return qw, sw
+
+
+def _fp8_operands(qa, sa, qw, sw, ndim, out_dtype, out):
+    _need(qa, torch.float8_e4m3fn, "qa", 2)
+    _need(qw, torch.float8_e4m3fn, "qw", ndim)
+    M, K = qa.shape
+    N = qw.shape[-2]
+    if qw.shape[-1] != K:
+        raise ValueError("qa and qw disagree on K")
+    _shaped(sa, torch.float32, (M, _cdiv(K, FP8_BLOCK)), "sa")
+    _shaped(sw, torch.float32, (*qw.shape[:-2], _cdiv(N, FP8_BLOCK), _cdiv(K, FP8_BLOCK)), "sw")
+    if out_dtype not in FLOAT_TYPES:
+        raise TypeError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
+    out = torch.empty((M, N), dtype=out_dtype, device=qa.device) if out is None else out
+    _shaped(out, out_dtype, (M, N), "out")
+    return M, N, K, out
+
+
+def q8_gemm_fp8(qa, sa, qw, sw, out_dtype=torch.bfloat16, out=None, stream=None):
+    """y[m, n] = sum over blocks b of sa[m, b] sw[n / 128, b] (qa . qw over block b), as out_dtype [M, N]."""
+    M, N, K, out = _fp8_operands(qa, sa, qw, sw, 2, out_dtype, out)
+    _same_device(qa, sa=sa, qw=qw, sw=sw, out=out)
+    _check(load().q8_gemm_fp8(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), M, N, K, _ptr(out), FLOAT_TYPES[out_dtype],
+                              _stream(stream)), "q8_gemm_fp8")
+    return out
+
+
+def q8_gemm_fp8_grouped(qa, sa, qw, sw, offsets, out_dtype=torch.bfloat16, out=None, stream=None):
+    """The product of q8_gemm_fp8 with qw[e] (of qw[E, N, K]) for the rows offsets[e] .. offsets[e + 1] - 1 of each
+    expert; offsets int32 [E + 1] stay on the device. Rows of no expert are not written."""
+    M, N, K, out = _fp8_operands(qa, sa, qw, sw, 3, out_dtype, out)
+    E = qw.shape[0]
+    _shaped(offsets, torch.int32, (E + 1,), "offsets")
+    _same_device(qa, sa=sa, qw=qw, sw=sw, offsets=offsets, out=out)
+    _check(load().q8_gemm_fp8_grouped(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(offsets), M, E, N, K, _ptr(out),
+                                      FLOAT_TYPES[out_dtype], _stream(stream)), "q8_gemm_fp8_grouped")
+    return out
+
+
+def q8_moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=None, n_group: int = 1,
+                 topk_group: int = 1, renorm: bool = True, scale: float = 1.0, idx=None, weights=None, stream=None):
+    """The top_k experts of each token and their weights from logits[T, E] (fp32, bf16 or fp16; rows may be strided):
+    (idx int32 [T, top_k], weights fp32 [T, top_k]). score: "softmax" or "sigmoid"; bias fp32 [E] takes part in
+    the choice only; with n_group groups only experts of the topk_group best groups are chosen. Masked experts
+    (logit -inf or NaN) are not chosen; places that stay empty have idx -1 and weight 0."""
+    ldl = _rows(logits, "logits")
+    T, E = logits.shape
+    if score not in SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if top_k < 1:
+        raise ValueError("top_k must be positive")
+    if bias is not None:
+        _shaped(bias, torch.float32, (E,), "bias")
+    idx = torch.empty((T, top_k), dtype=torch.int32, device=logits.device) if idx is None else idx
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device) if weights is None else weights
+    _shaped(idx, torch.int32, (T, top_k), "idx")
+    _shaped(weights, torch.float32, (T, top_k), "weights")
+    _same_device(logits, bias=bias, idx=idx, weights=weights)
+    _check(load().q8_moe_route(_ptr(logits), FLOAT_TYPES[logits.dtype], T, E, ldl, top_k, SCORES[score], _ptr(bias),
+                               n_group, topk_group, int(renorm), ctypes.c_float(scale), _ptr(idx), _ptr(weights),
+                               _stream(stream)), "q8_moe_route")
+    return idx, weights
+
+
+def q8_moe_plan(idx: torch.Tensor, n_experts: int, offsets=None, slots=None, stream=None):
+    """The choices idx int32 [T, k] sorted by expert (stable): (offsets int32 [n_experts + 1], slots int32 [T, k]),
+    the first row of each expert and the row of each choice (-1 where idx is outside [0, n_experts))."""
+    _need(idx, torch.int32, "idx", 2)
+    T, k = idx.shape
+    if n_experts < 1:
+        raise ValueError("n_experts must be positive")
+    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=idx.device) if offsets is None else offsets
+    slots = torch.empty((T, k), dtype=torch.int32, device=idx.device) if slots is None else slots
+    _shaped(offsets, torch.int32, (n_experts + 1,), "offsets")
+    _shaped(slots, torch.int32, (T, k), "slots")
+    _same_device(idx, offsets=offsets, slots=slots)
+    _check(load().q8_moe_plan(_ptr(idx), T, k, n_experts, _ptr(offsets), _ptr(slots), _stream(stream)), "q8_moe_plan")
+    return offsets, slots
+
+
+def q8_moe_combine(h: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, out=None, stream=None):
+    """y[t] = sum_j weights[t, j] h[slots[t, j]] (fp32 sums), h[rows, N] and y[T, N] of one float type. Slots outside
+    [0, rows) add nothing."""
+    if _rows(h, "h") != h.shape[1] or not h.is_contiguous():
+        raise ValueError("h must be contiguous")
+    rows, N = h.shape
+    _need(slots, torch.int32, "slots", 2)
+    T, k = slots.shape
+    _shaped(weights, torch.float32, (T, k), "weights")
+    out = torch.empty((T, N), dtype=h.dtype, device=h.device) if out is None else out
+    _shaped(out, h.dtype, (T, N), "out")
+    _same_device(h, slots=slots, weights=weights, out=out)
+    _check(load().q8_moe_combine(_ptr(h), FLOAT_TYPES[h.dtype], rows, N, _ptr(slots), _ptr(weights), T, k, _ptr(out),
+                                 _stream(stream)), "q8_moe_combine")
     return out

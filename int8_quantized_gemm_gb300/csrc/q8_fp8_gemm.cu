@@ -1,0 +1,476 @@
+// Products of float8 (e4m3) matrices with a scale for each row and 128 K of the activations and each
+// 128 x 128 block of the weights, for one weight matrix or one for each group of rows (experts).
+//
+//   y[m, n] = sum_b sa[m, b] sw[n / 128, b] sum_{k in block b} qa[m, k] qw[n, k]
+//
+// The tensor core (tcgen05 kind::f8f6f4) sums one block of 128 K at a time in fp32 in tensor memory;
+// drain warps read each partial sum and add it, times its scale, to fp32 registers. The MMA of the
+// next block runs meanwhile, on another of the accumulator's buffers.
+#include <cuda.h>
+#include <string.h>
+
+#include "q8_fp8.h"
+#include "q8_internal.h"
+#include "q8_tc_ptx.cuh"
+
+namespace q8 {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned int g_fp8_error = 0;
+
+constexpr int BK = kFp8Block;          // K of a stage: one scale block, 128 bytes a row
+constexpr int TW = 128;                // weight rows of a tile: one scale block, the MMA's M side
+constexpr int kTileW = TW * BK;        // 16 KB
+constexpr uint32_t kIdescW = idesc_f16(TW, 0);   // fp32 D, e4m3 A and B, both K-major, M = 128
+
+// -------------------------------------------------------------------------- weights on the MMA's M side
+// A tile is 128 weight rows x up to TN token rows (16 .. 256), for few tokens (a whole weight block
+// is then read once, whatever the tokens) and for groups of few rows.
+//   warp 0     TMA: weights [128 x 128] and tokens [n x 128] of each K block, 128-byte swizzle
+//   warp 1     MMA issuer (N = n rounded up to 16), TMEM
+//   warps 2, 3 scales of the block's tokens, sa sw, into the buffer's scale row
+//   warps 4-11 drain: two warps for each quarter of the TMEM lanes (weight rows), each takes every
+//              other chunk of 32 tokens
+// With few tiles, a cluster of S CTAs splits a tile's K blocks; each CTA sends the partial sums of the
+// tokens it does not own to the CTA that does (st.async), which adds them in the order of the ranks:
+// the same bits every time, no workspace and no second launch.
+constexpr int kSwapThreads = 384;
+constexpr int kDrainThreads = 256;
+constexpr int kRegsLow = 88, kRegsHigh = 208;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kSwapThreads * 168, "above the launch's registers");
+constexpr int kMaxStages = 8;
+constexpr int kScaleBytes = 2 * 256 * 4;
+constexpr int kReduceBytes = 32 * 1024;
+constexpr int kTailBytes = 8 * (2 * kMaxStages + 4 + 2) + 32 + 4 * (kMaxExperts + 2);
+constexpr int kSmemMax = 227 * 1024;
+
+struct SwapArgs {
+    const float* sa;
+    const float* sw;
+    const int32_t* offsets;   // nullptr: one group of all rows
+    int rows, E;
+    int N, K;
+    int tn, box, stages;      // token rows of a tile, of a TMA box; stages of the ring
+    int split;                // CTAs of a cluster, sharing a tile's K blocks
+    void* y;
+    q8_float_type type;
+};
+
+// Token tiles before each group, and the rows of a group, from the offsets. Ranges are cut to
+// [0, rows], so that no offset, whatever its value, leads outside of qa and y.
+struct Groups {
+    const int32_t* offsets;
+    const int* cum;   // shared: tiles before group e
+    int rows, E, tn;
+    __device__ __forceinline__ void range(int e, int& lo, int& hi) const {
+        if (!offsets) {
+            lo = 0;
+            hi = rows;
+        } else {
+            lo = min(max(__ldg(offsets + e), 0), rows);
+            hi = min(max(__ldg(offsets + e + 1), lo), rows);
+        }
+    }
+    // token tile t -> its group, first row and rows
+    __device__ __forceinline__ void tile(int t, int& e, int& row, int& n) const {
+        int a = 0, b = E;
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (cum[mid] <= t) a = mid;
+            else b = mid;
+        }
+        e = a;
+        int lo, hi;
+        range(e, lo, hi);
+        row = lo + (t - cum[e]) * tn;
+        n = min(tn, hi - row);
+    }
+    // one warp: the prefix sums
+    __device__ __forceinline__ void scan(int* out, int lane) const {
+        int run = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            int c = 0;
+            if (e0 + lane < E) {
+                int lo, hi;
+                range(e0 + lane, lo, hi);
+                c = (hi - lo + tn - 1) / tn;
+            }
+            int s = c;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, s, d);
+                if (lane >= d) s += o;
+            }
+            if (e0 + lane < E) out[e0 + lane] = run + s - c;
+            run += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) out[E] = run;
+    }
+};
+
+__device__ __forceinline__ void store_one(void* y, q8_float_type t, int64_t at, float v) {
+    if (t == Q8_BF16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
+    else if (t == Q8_F16) static_cast<__half*>(y)[at] = __float2half_rn(v);
+    else static_cast<float*>(y)[at] = v;
+}
+
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+    const uint4 u = lds128(addr);
+    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+}
+
+template <int CH>   // chunks of 32 tokens of a drain warp: tn <= 64 CH
+__global__ void __launch_bounds__(kSwapThreads, 1)
+    gemm_fp8_swap_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                         SwapArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t sraw = smem_u32(smem_raw);
+    const uint32_t sbase = (sraw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (sbase - sraw);
+    const uint32_t stage_bytes = kTileW + p.tn * BK;
+    const uint32_t off_scale = p.stages * stage_bytes;
+    const uint32_t off_reduce = off_scale + kScaleBytes;
+    const uint32_t off_bar = off_reduce + (p.split > 1 ? kReduceBytes : 0);
+    const uint32_t bar_full = sbase + off_bar;
+    const uint32_t bar_empty = bar_full + 8 * kMaxStages;
+    const uint32_t bar_accfull = bar_empty + 8 * kMaxStages;
+    const uint32_t bar_accempty = bar_accfull + 16;
+    const uint32_t bar_got = bar_accempty + 16;     // split: the partial sums of this CTA's tokens
+    const uint32_t bar_free = bar_got + 8;          // split: the other CTAs have read what this one sent
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + off_bar + 8 * (2 * kMaxStages + 6));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* cum = reinterpret_cast<int*>(tmem_slot + 2);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+    const int acc_cols = CH * 64 < 32 ? 32 : CH * 64;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_accfull + 8 * b, 3);    // the MMA's commit and the two scale warps
+            mbar_init(bar_accempty + 8 * b, kDrainThreads / 32);
+        }
+        mbar_init(bar_got, 1);
+        mbar_init(bar_free, p.split > 1 ? (p.split - 1) * (kDrainThreads / 32) : 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+    }
+    const Groups groups{p.offsets, cum, p.rows, p.E, p.tn};
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 2 * acc_cols);
+    if (warp == 2) groups.scan(cum, lane);
+    tc_fence_before();
+    if (p.split > 1) cluster_sync();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int NT = (p.N + TW - 1) / TW, KB = (p.K + BK - 1) / BK;
+    const int64_t units = (int64_t)cum[p.E] * NT;
+    const int64_t first = blockIdx.x / p.split, step = gridDim.x / p.split;
+    const int kb0 = (int)((int64_t)KB * rank / p.split), kb1 = (int)((int64_t)KB * (rank + 1) / p.split);
+
+    if (warp < 4) {
+        if constexpr (CH > 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsLow));
+        if (warp == 0) {
+            // ------------------------------------------------------------------------ TMA
+            if (lane == 0) {
+                uint32_t s = 0, phase = 1;
+                bool ok = true;
+                for (int64_t u = first; u < units && ok; u += step) {
+                    int e, row, n;
+                    groups.tile((int)(u / NT), e, row, n);
+                    const int nt = (int)(u % NT), boxes = (n + p.box - 1) / p.box;
+                    const int wrow = e * p.N + nt * TW;
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t dst = sbase + s * stage_bytes, bar = bar_full + 8 * s;
+                        mbar_expect_tx(bar, kTileW + boxes * p.box * BK);
+                        tma_load_2d(dst, &tmap_w, kb * BK, wrow, bar);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(dst + kTileW + b * p.box * BK, &tmap_a, kb * BK, row + b * p.box, bar);
+                        if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------------------ MMA
+            if (lane == 0) {
+                uint32_t s = 0, phase = 0, c = 0;
+                bool ok = true;
+                for (int64_t u = first; u < units && ok; u += step) {
+                    int e, row, n;
+                    groups.tile((int)(u / NT), e, row, n);
+                    const uint32_t idesc = kIdescW + ((uint32_t)((n + 15) >> 4) << 18);   // N = n rounded up to 16
+                    for (int kb = kb0; kb < kb1; ++kb, ++c) {
+                        const uint32_t buf = c & 1;
+                        if (!mbar_wait(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrMmaAcc,
+                                       &g_fp8_error) ||
+                            !mbar_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t w = smem_desc_sw128(sbase + s * stage_bytes);
+                        const uint64_t a = smem_desc_sw128(sbase + s * stage_bytes + kTileW);
+                        const uint32_t d = tmem_base + buf * acc_cols;
+#pragma unroll
+                        for (int kk = 0; kk < BK / 32; ++kk)
+                            mma_fp8(d, w + 2 * kk, a + 2 * kk, idesc, kk ? 1u : 0u);
+                        mma_commit(bar_empty + 8 * s);
+                        mma_commit(bar_accfull + 8 * buf);
+                        if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
+                    }
+                }
+            }
+        } else {
+            // --------------------------------------------------------------------- scales
+            // Four blocks' scales are loaded ahead of the four being handed out.
+            constexpr int kAhead = 4, kCols = (CH + 1) / 2;   // token columns of a lane: 64 CH / 64, at least 1
+            uint32_t c = 0;
+            bool ok = true;
+            for (int64_t u = first; u < units && ok; u += step) {
+                int e, row, n;
+                groups.tile((int)(u / NT), e, row, n);
+                const int nt = (int)(u % NT);
+                const float* sw = p.sw + ((int64_t)e * NT + nt) * KB;
+                float a[2][kAhead][2 * kCols], w[2][kAhead];
+                auto load = [&](int kb, float (&av)[kAhead][2 * kCols], float (&wv)[kAhead]) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        const bool in = kb + i < kb1;
+                        wv[i] = in ? __ldg(sw + kb + i) : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 2 * kCols; ++j) {
+                            const int col = (warp - 2) * 32 + lane + 64 * j;
+                            av[i][j] = in && col < n ? __ldg(p.sa + (int64_t)(row + col) * KB + kb + i) : 0.0f;
+                        }
+                    }
+                };
+                load(kb0, a[0], w[0]);
+                for (int kb = kb0; kb < kb1 && ok; kb += kAhead) {
+                    load(kb + kAhead, a[1], w[1]);
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        if (kb + i >= kb1) break;
+                        const uint32_t buf = c & 1;
+                        if (!mbar_wait(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrConvEmpty,
+                                       &g_fp8_error)) {
+                            ok = false;
+                            break;
+                        }
+                        float* out = reinterpret_cast<float*>(smem + off_scale) + buf * 256 + (warp - 2) * 32 + lane;
+#pragma unroll
+                        for (int j = 0; j < 2 * kCols; ++j)
+                            if (j < CH) out[64 * j] = a[0][i][j] * w[0][i];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_accfull + 8 * buf);
+                        ++c;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        w[0][i] = w[1][i];
+#pragma unroll
+                        for (int j = 0; j < 2 * kCols; ++j) a[0][i][j] = a[1][i][j];
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------------------- drain
+        if constexpr (CH > 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsHigh));
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        uint32_t c = 0, done = 0;
+        bool ok = true;
+        for (int64_t u = first; u < units && ok; u += step, ++done) {
+            int e, row, n;
+            groups.tile((int)(u / NT), e, row, n);
+            const int col = (int)(u % NT) * TW + quarter * 32 + lane;   // this thread's weight row
+            float acc[CH][32];
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[i][j] = 0.0f;
+            for (int kb = kb0; kb < kb1; ++kb, ++c) {
+                const uint32_t buf = c & 1;
+                if (!mbar_wait(bar_accfull + 8 * buf, (c >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sc = sbase + off_scale + buf * 1024;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int t0 = (2 * i + half) * 32;
+                    if (t0 < n) {
+                        uint32_t v[32];
+                        tmem_ld32(tlane + buf * acc_cols + t0, v);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 f = lds_f4(sc + (t0 + j) * 4);
+                            acc[i][j] = __fmaf_rn(__uint_as_float(v[j]), f.x, acc[i][j]);
+                            acc[i][j + 1] = __fmaf_rn(__uint_as_float(v[j + 1]), f.y, acc[i][j + 1]);
+                            acc[i][j + 2] = __fmaf_rn(__uint_as_float(v[j + 2]), f.z, acc[i][j + 2]);
+                            acc[i][j + 3] = __fmaf_rn(__uint_as_float(v[j + 3]), f.w, acc[i][j + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_accempty + 8 * buf);
+            }
+            if (!ok) break;
+            int own_shift = 0;   // tokens in groups of four: group g is added up by CTA g % split
+            if (CH == 1 && p.split > 1) {
+                own_shift = 1;
+                const int S = p.split, groups4 = (n + 3) / 4;
+                const int per = (groups4 + S - 1) / S;          // slots of groups in the receive buffer
+                const int here = (groups4 - rank + S - 1) / S;  // groups that this CTA owns (may be 0)
+                const uint32_t buffer = sbase + off_reduce, lane16 = (quarter * 32 + lane) * 16;
+                if (done && !mbar_wait_cluster(bar_free, (done - 1) & 1, abort_flag, kErrRelay, &g_fp8_error)) break;
+                if (warp == 4 && lane == 0) mbar_expect_tx(bar_got, (S - 1) * max(here, 0) * TW * 16);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int g = half * 8 + q, owner = g % S;
+                    if (g < groups4 && owner != rank) {
+                        const int slot = (rank < owner ? rank : rank - 1) * per + g / S;
+                        st_async16(mapa_shared(buffer + slot * (TW * 16) + lane16, owner),
+                                   make_uint4(__float_as_uint(acc[0][4 * q]), __float_as_uint(acc[0][4 * q + 1]),
+                                              __float_as_uint(acc[0][4 * q + 2]), __float_as_uint(acc[0][4 * q + 3])),
+                                   mapa_shared(bar_got, owner));
+                    }
+                }
+                if (!mbar_wait_cluster(bar_got, done & 1, abort_flag, kErrRelay, &g_fp8_error)) break;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int g = half * 8 + q;
+                    if (g < groups4 && g % S == rank) {
+                        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int r = 0; r < S; ++r) {
+                            float4 f = make_float4(acc[0][4 * q], acc[0][4 * q + 1], acc[0][4 * q + 2], acc[0][4 * q + 3]);
+                            if (r != rank)
+                                f = lds_f4(buffer + ((r < rank ? r : r - 1) * per + g / S) * (TW * 16) + lane16);
+                            t.x += f.x; t.y += f.y; t.z += f.z; t.w += f.w;
+                        }
+                        acc[0][4 * q] = t.x; acc[0][4 * q + 1] = t.y; acc[0][4 * q + 2] = t.z; acc[0][4 * q + 3] = t.w;
+                    }
+                }
+                __syncwarp();
+                if (lane < S && lane != rank) mbar_arrive_remote(mapa_shared(bar_free, lane));
+            }
+            if (col < p.N) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int t = (2 * i + half) * 32 + j;
+                        if (t < n && (!own_shift || (t / 4) % p.split == rank))
+                            store_one(p.y, p.type, (int64_t)(row + t) * p.N + col, acc[i][j]);
+                    }
+            }
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1LL << 22)) __nanosleep(1000);
+    }
+    tc_fence_before();
+    // no CTA of a cluster leaves while another may still send to it
+    if (p.split > 1) cluster_sync();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, 2 * acc_cols);
+}
+
+template <int CH>
+cudaError_t launch_swap(const CUtensorMap& ma, const CUtensorMap& mw, SwapArgs p, int64_t max_tiles,
+                        cudaStream_t stream) {
+    const int stage = kTileW + p.tn * BK;
+    const int room = kSmemMax - 1024 - kTailBytes - kScaleBytes - (p.split > 1 ? kReduceBytes : 0);
+    p.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
+    const int smem = 1024 + p.stages * stage + kScaleBytes + (p.split > 1 ? kReduceBytes : 0) + kTailBytes;
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_swap_kernel<CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kSwapThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)p.split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int64_t clusters = device_sm_count() / p.split;
+    if (p.split > 1) {
+        cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
+        int fit = 0;
+        e = cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_swap_kernel<CH>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (fit > 0 && fit < clusters) clusters = fit;
+    }
+    const int64_t units = max_tiles * ((p.N + TW - 1) / TW);
+    if (units < clusters) clusters = units;
+    cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
+    e = cudaLaunchKernelEx(&cfg, gemm_fp8_swap_kernel<CH>, ma, mw, p);
+    note_launch();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
+                            const int32_t* offsets, int64_t rows, int E, int64_t N, int64_t K, void* y,
+                            q8_float_type t, cudaStream_t stream) {
+    // Token rows of a tile: the rows of a group (on average), up to 256.
+    const int64_t per = (rows + E - 1) / E;
+    const int tn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
+    const int64_t max_tiles = offsets ? rows / tn + (E < rows ? E : rows) : (rows + tn - 1) / tn;
+    const int64_t NT = (N + TW - 1) / TW, KB = (K + BK - 1) / BK;
+    if (max_tiles * NT >= (1LL << 40)) return cudaErrorNotSupported;
+    SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, tn, tn < 32 ? tn : 32, 0, 1, y, t};
+    if (tn <= 64) {
+        // the split that ends first: rounds of units over the clusters, a part of K each
+        const int sms = device_sm_count();
+        const int64_t units = max_tiles * NT;
+        double best = 1e30;
+        for (int S = 1; S <= 8 && S * 2 <= KB; S *= 2) {
+            const int64_t rounds = (units + sms / S - 1) / (sms / S);
+            const double cost = (double)rounds * ((KB + S - 1) / S + 4.0);
+            if (cost < best * 0.98) { best = cost; p.split = S; }
+        }
+    }
+    CUtensorMap ma, mw;
+    if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), rows, K, p.box, BK, true) ||
+        !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)E * N, K, TW, BK, true))
+        return cudaErrorInvalidValue;
+    if (tn <= 64) return launch_swap<1>(ma, mw, p, max_tiles, stream);
+    if (tn <= 128) return launch_swap<2>(ma, mw, p, max_tiles, stream);
+    return launch_swap<4>(ma, mw, p, max_tiles, stream);
+}
+
+cudaError_t read_and_clear_gemm_fp8_error(uint32_t* code) {
+    unsigned int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_fp8_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    *code = v;
+    if (v) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_fp8_error, &zero, sizeof(zero));
+    }
+    return e;
+}
+
+}  // namespace q8

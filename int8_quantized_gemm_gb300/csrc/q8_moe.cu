@@ -1,0 +1,413 @@
+// Routing to experts: choice of the experts and their weights, the rows of each expert, and the
+// weighted sum of the experts' answers.
+#include <cooperative_groups.h>
+
+#include "q8_fp8.h"
+#include "q8_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace q8 {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kFloatMax = 3.402823466e38f;
+
+// ------------------------------------------------------------------------------------- route
+// One warp for a token. With n_group groups of `per` experts, lpg = 32 / n_group lanes hold a group's
+// experts, lane r of them the VPL experts from r * VPL on: a lane never mixes groups, and lower
+// lanes hold lower experts, so that "the lowest lane that has the maximum" is the lowest index.
+//
+// Without a bias the order is that of the logits (both scores grow with the logit), which is exact.
+// With a bias the order is that of score + bias in 64 bits: keys are computed in fp32, and where two
+// that decide something are nearer than the fp32 keys' error bound, the warp does the token again in
+// fp64 (about one token in a thousand on Gaussian logits). The scores of the weights stay fp32.
+template <class K>
+__device__ __forceinline__ K masked_key();
+template <>
+__device__ __forceinline__ float masked_key<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ double masked_key<double>() { return -(double)INFINITY; }
+
+// Ascending order of the floats as unsigned values; -inf (masked) is 0x007fffff.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// Warp maximum and the lowest lane that has it.
+__device__ __forceinline__ float warp_best(float v, int& who) {
+    const uint32_t u = ordered(v), m = __reduce_max_sync(kFull, u);
+    who = __ffs(__ballot_sync(kFull, u == m)) - 1;
+    return unordered(m);
+}
+__device__ __forceinline__ double warp_best(double v, int& who) {
+    double m = v;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, d));
+    who = __ffs(__ballot_sync(kFull, v == m)) - 1;
+    return m;
+}
+
+struct Place {      // where a lane's experts are
+    int base, have; // first expert, how many (<= VPL, may be 0)
+    int group, first, lpg;
+};
+
+// Group choice and top-k over a lane's keys. Returns the chosen expert of lane j in `mine` (-1: none)
+// for j < k. eps >= 0 asks for a report of decisions closer than eps + rel |key| (group sums: twice).
+template <int VPL, class K>
+__device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, float eps,
+                                       float rel, int lane, int& mine) {
+    bool close = false;
+    if (a.n_group > 1) {
+        K m1 = masked_key<K>(), m2 = masked_key<K>();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const K v = key[i];
+            m2 = fmax(m2, fmin(m1, v));
+            m1 = fmax(m1, v);
+        }
+        const K l1 = m1, l2 = m2;
+        for (int d = 1; d < pl.lpg; ++d) {
+            int src = lane - pl.first + d;
+            src = pl.first + (src >= pl.lpg ? src - pl.lpg : src);
+            const K o1 = __shfl_sync(kFull, l1, src & 31), o2 = __shfl_sync(kFull, l2, src & 31);
+            m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+            m1 = fmax(m1, o1);
+        }
+        const K none = masked_key<K>();
+        const K score = sum2 && m2 > none ? m1 + m2 : m1;
+        int rank = 0;
+        for (int g = 0; g < a.n_group; ++g) {
+            const K o = __shfl_sync(kFull, score, g * pl.lpg);
+            rank += (o > score || (o == score && g < pl.group)) ? 1 : 0;
+            if (eps >= 0.0f && g != pl.group && pl.group < a.n_group)
+                close |= fabs((double)o - (double)score) <= 2.0 * (eps + rel * fabs((double)score));
+        }
+        if (rank >= a.topk_group) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) key[i] = none;
+        }
+    }
+    K best = masked_key<K>(), last = K(0);
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (key[i] > best) { best = key[i]; at = i; }
+    const int rounds = a.k + (eps >= 0.0f ? 1 : 0);
+    mine = -1;
+    for (int j = 0; j < rounds; ++j) {
+        int who;
+        const K top = warp_best(best, who);
+        if (!(top > masked_key<K>())) break;
+        if (eps >= 0.0f && j) close |= (float)last - (float)top <= eps + rel * fabsf((float)top);
+        last = top;
+        if (j == a.k) break;
+        const int e = __shfl_sync(kFull, pl.base + at, who);
+        if (lane == j) mine = e;
+        if (lane == who) {
+            best = masked_key<K>();
+            int next = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (i == at) key[i] = masked_key<K>();
+                if (key[i] > best) { best = key[i]; next = i; }
+            }
+            at = next;
+        }
+    }
+    return close;
+}
+
+template <class T>
+__device__ __forceinline__ float load_logit(const T* p) {
+    const float l = to_float(*p);
+    return l != l ? -INFINITY : fminf(l, kFloatMax) + 0.0f;   // + 0: -0 and 0 are one value
+}
+
+template <int VPL, class T>
+__device__ __noinline__ int route_exact(const T* row, const Place pl, const RouteArgs a, int lane) {
+    double key[VPL];
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < pl.have; ++i) m = fmaxf(m, load_logit(row + pl.base + i));
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const double l = i < pl.have ? (double)load_logit(row + pl.base + i) : -(double)INFINITY;
+        double p = 0.0;
+        if (l > -(double)INFINITY) p = a.softmax ? exp(l - (double)m) : 1.0 / (1.0 + exp(-l));
+        key[i] = l > -(double)INFINITY ? p : -1.0;
+        z += p;
+    }
+    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        key[i] = key[i] < 0.0 ? masked_key<double>()
+                              : (a.softmax ? key[i] / z : key[i]) + (double)__ldg(a.bias + pl.base + i);
+    int mine;
+    choose<VPL, double>(key, pl, a, true, -1.0f, 0.0f, lane, mine);
+    return mine;
+}
+
+template <int VPL, class T>
+__global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    if (t >= a.T) return;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
+    const int per = a.E / a.n_group;
+    Place pl;
+    pl.lpg = 32 / a.n_group;
+    pl.group = lane / pl.lpg;
+    pl.first = pl.group * pl.lpg;
+    const int r = lane - pl.first;
+    pl.base = pl.group * per + r * VPL;
+    pl.have = pl.group < a.n_group ? max(0, min(VPL, per - r * VPL)) : 0;
+    float key[VPL];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        key[i] = i < pl.have ? load_logit(row + pl.base + i) : -INFINITY;
+        m = fmaxf(m, key[i]);
+    }
+    int mine, who;
+    float inv_z = 1.0f;
+    if (a.softmax) {
+        m = warp_best(m, who);
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) z += key[i] > -INFINITY ? expf(key[i] - m) : 0.0f;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
+        inv_z = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
+    }
+    if (a.bias) {
+        // The fp32 key's error: the score's (sigmoid: exp, add and divide, under 2^-21; softmax: the
+        // rounding of l - m, exp, and a sum of up to 512 terms, under 2^-20 of the largest score)
+        // and the sum's, half a step of |key|. Two of them, and twice that for safety.
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > -INFINITY)
+                key[i] = (a.softmax ? expf(key[i] - m) * inv_z : __fdiv_rn(1.0f, 1.0f + expf(-key[i]))) +
+                         __ldg(a.bias + pl.base + i) + 0.0f;
+        const float eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-19f;
+        const bool close = choose<VPL, float>(key, pl, a, true, eps, 0x1p-22f, lane, mine);
+        if (__any_sync(kFull, close)) mine = route_exact<VPL, T>(row, pl, a, lane);
+    } else {
+        choose<VPL, float>(key, pl, a, false, -1.0f, 0.0f, lane, mine);
+    }
+    float p = 0.0f;
+    if (mine >= 0) {
+        const float l = load_logit(row + mine);
+        p = a.softmax ? expf(l - m) * inv_z : __fdiv_rn(1.0f, 1.0f + expf(-l));
+    }
+    if (a.renorm) {
+        float sum = p;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+        p = sum > 0.0f ? __fdiv_rn(p, sum) : 0.0f;
+    }
+    if (lane < a.k) {
+        a.idx[t * a.k + lane] = mine;
+        a.w[t * a.k + lane] = p * a.scale;
+    }
+}
+
+template <class T>
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+    const int per = a.E / a.n_group, lpg = 32 / a.n_group, vpl = (per + lpg - 1) / lpg;
+    const int64_t ctas = (a.T + 3) / 4;
+    if (ctas >= (1LL << 31)) return cudaErrorNotSupported;
+    const unsigned grid = (unsigned)ctas;
+    if (vpl <= 1) moe_route_kernel<1, T><<<grid, 128, 0, stream>>>(a);
+    else if (vpl <= 2) moe_route_kernel<2, T><<<grid, 128, 0, stream>>>(a);
+    else if (vpl <= 4) moe_route_kernel<4, T><<<grid, 128, 0, stream>>>(a);
+    else if (vpl <= 8) moe_route_kernel<8, T><<<grid, 128, 0, stream>>>(a);
+    else if (vpl <= 16) moe_route_kernel<16, T><<<grid, 128, 0, stream>>>(a);
+    else if (vpl <= 32) moe_route_kernel<32, T><<<grid, 128, 0, stream>>>(a);
+    else return cudaErrorNotSupported;
+    note_launch();
+    return cudaGetLastError();
+}
+
+// -------------------------------------------------------------------------------------- plan
+// A stable counting sort of the expert indices in one launch: a cluster of CTAs, each with a
+// contiguous share of the entries, each warp with a contiguous share of its CTA's. Sweep 1 counts
+// the entries of each (warp, expert); prefix sums over warps, then CTAs (distributed shared memory),
+// then experts give each warp its first slot of each expert; sweep 2 hands the slots out in order.
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+
+__global__ void __launch_bounds__(kPlanThreads)
+    moe_plan_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int32_t* __restrict__ offsets,
+                    int32_t* __restrict__ slots) {
+    extern __shared__ int32_t plan_smem[];
+    int32_t* count = plan_smem;                       // [warps][E]
+    int32_t* total = plan_smem + kPlanWarps * E;      // [E] of this CTA
+    __shared__ int32_t scan[kPlanWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) count[i] = 0;
+    __syncthreads();
+    // shares in whole warps of entries
+    const int64_t share = (n + (int64_t)ctas * kPlanThreads - 1) / ((int64_t)ctas * kPlanThreads) * 32;
+    const int64_t lo = min(n, ((int64_t)rank * kPlanWarps + warp) * share), hi = min(n, lo + share);
+    int32_t* mine = count + warp * E;
+    for (int64_t i = lo; i < hi; i += 32) {
+        int e = i + lane < hi ? __ldg(idx + i + lane) : -1;
+        if (e < 0 || e >= E) e = E;
+        const unsigned same = __match_any_sync(kFull, e);
+        if (e < E && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    if (threadIdx.x < E) {
+        int run = 0;
+#pragma unroll 8
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int c = count[w * E + threadIdx.x];
+            count[w * E + threadIdx.x] = run;
+            run += c;
+        }
+        total[threadIdx.x] = run;
+    }
+    cluster.sync();
+    int before = 0, all = 0;
+    if (threadIdx.x < E)
+        for (int c = 0; c < ctas; ++c) {
+            const int v = cluster.map_shared_rank(total, c)[threadIdx.x];
+            all += v;
+            if (c < rank) before += v;
+        }
+    int incl = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    cluster.sync();   // also: nobody reads this CTA's totals any more
+    int start = incl - all;
+    for (int w = 0; w < warp; ++w) start += scan[w];
+    if (threadIdx.x < E) {
+        total[threadIdx.x] = start + before;
+        if (rank == 0) {
+            if (threadIdx.x == 0) offsets[0] = 0;
+            offsets[threadIdx.x + 1] = start + all;
+        }
+    }
+    __syncthreads();
+    for (int64_t i = lo; i < hi; i += 32) {
+        const bool live = i + lane < hi;
+        int e = live ? __ldg(idx + i + lane) : -1;
+        if (e < 0 || e >= E) e = E;
+        const unsigned same = __match_any_sync(kFull, e);
+        int slot = -1;
+        if (e < E) slot = total[e] + mine[e] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (e < E && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+        if (live) slots[i + lane] = slot;
+    }
+}
+
+// ----------------------------------------------------------------------------------- combine
+// 16 bytes of a token's output for each thread, its k rows' loads in flight four at a time; the sum in
+// fp32 in the order of the choices. Reads k rows and writes one for each token: memory bound.
+template <class T>
+__global__ void __launch_bounds__(256)
+    moe_combine_kernel(const T* __restrict__ h, int64_t rows, uint32_t chunks, const int32_t* __restrict__ slots,
+                       const float* __restrict__ w, uint64_t total, int k, T* __restrict__ y) {
+    constexpr int n = Vec16<T>::n, kAhead = 4;
+    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const uint64_t t = i / chunks;
+    const uint32_t c = (uint32_t)(i - t * chunks);
+    float acc[n];
+#pragma unroll
+    for (int j = 0; j < n; ++j) acc[j] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += kAhead) {
+        Vec16<T> v[kAhead];
+        float wt[kAhead];
+        bool in[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t d = j0 + j < k ? (int64_t)__ldg(slots + t * k + j0 + j) : -1;
+            in[j] = d >= 0 && d < rows;
+            wt[j] = in[j] ? __ldg(w + t * k + j0 + j) : 0.0f;
+            v[j].u = make_uint4(0, 0, 0, 0);
+            if (in[j]) v[j].u = __ldcs(reinterpret_cast<const uint4*>(h) + (uint64_t)d * chunks + c);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (in[j])
+#pragma unroll
+                for (int q = 0; q < n; ++q) acc[q] = __fmaf_rn(wt[j], to_float(v[j].t[q]), acc[q]);
+    }
+    Vec16<T> o;
+#pragma unroll
+    for (int q = 0; q < n; ++q) o.t[q] = from_float<T>(acc[q]);
+    reinterpret_cast<uint4*>(y)[i] = o.u;
+}
+
+template <class T>
+cudaError_t launch_combine(const void* h, int64_t rows, int64_t N, const int32_t* slots, const float* w, int64_t T_,
+                           int k, void* y, cudaStream_t stream) {
+    const uint64_t chunks = (uint64_t)N / Vec16<T>::n, total = (uint64_t)T_ * chunks;
+    const uint64_t ctas = (total + 255) / 256;
+    if (chunks >= (1ULL << 32) || ctas >= (1ULL << 31)) return cudaErrorNotSupported;
+    moe_combine_kernel<T><<<(unsigned)ctas, 256, 0, stream>>>(static_cast<const T*>(h), rows, (uint32_t)chunks, slots, w,
+                                                             total, k, static_cast<T*>(y));
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const RouteArgs& a, q8_float_type t, cudaStream_t stream) {
+    switch (t) {
+        case Q8_F32: return launch_route<float>(a, stream);
+        case Q8_BF16: return launch_route<__nv_bfloat16>(a, stream);
+        default: return launch_route<__half>(a, stream);
+    }
+}
+
+cudaError_t launch_moe_plan(const int32_t* idx, int64_t n, int E, int32_t* offsets, int32_t* slots,
+                            cudaStream_t stream) {
+    const size_t smem = (size_t)(kPlanWarps + 1) * E * 4;
+    cudaError_t e = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    // A CTA for each 2048 entries, up to the portable cluster of 8.
+    int ctas = 1;
+    while (ctas < 8 && (int64_t)ctas * 2048 < n) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(kPlanThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, moe_plan_kernel, idx, n, E, offsets, slots);
+    note_launch();
+    return e;
+}
+
+cudaError_t launch_moe_combine(const void* h, q8_float_type t, int64_t rows, int64_t N, const int32_t* slots,
+                               const float* w, int64_t T, int k, void* y, cudaStream_t stream) {
+    switch (t) {
+        case Q8_F32: return launch_combine<float>(h, rows, N, slots, w, T, k, y, stream);
+        case Q8_BF16: return launch_combine<__nv_bfloat16>(h, rows, N, slots, w, T, k, y, stream);
+        default: return launch_combine<__half>(h, rows, N, slots, w, T, k, y, stream);
+    }
+}
+
+}  // namespace q8
