@@ -630,89 +630,94 @@ def q8_gemm_mx(qa, s_a, qw, sf, group: int = 32, bias=None, out_dtype=torch.floa
 FLOAT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
 FP8_BLOCK = 128
+_FP8 = torch.float8_e4m3fn
+# A decode step makes many of these calls, so the marshalling is kept short: raw integers for the pointers,
+# the stream's handle without a Stream object, each tensor looked at once.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _cdiv(a: int, b: int) -> int:
     return -(-a // b)
 
 
-def _same_device(first: torch.Tensor, **others):
-    """Every tensor on the device of the first, which has to be the current one (the calls go to its stream)."""
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
-
-
-def _rows(t: torch.Tensor, name: str) -> int:
-    """The row pitch of a 2-D tensor of floats with unit column stride."""
+def _float_rows(t: torch.Tensor, name: str):
+    """(rows, columns, row pitch, type) of a 2-D CUDA tensor of floats with unit stride along its rows."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in FLOAT_TYPES:
+    kind = FLOAT_TYPES.get(t.dtype)
+    if kind is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    pitch, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its rows")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
+    if rows <= 1:
+        pitch = cols
+    elif pitch < cols:
         raise ValueError(f"the rows of {name} overlap")
-    return t.stride(0)
+    return rows, cols, pitch, kind
 
 
-def _shaped(t: torch.Tensor, dtype, shape, name: str):
-    _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+def _dense(t: torch.Tensor, dtype, shape, device: int, name: str) -> int:
+    """The address of a contiguous tensor of this type and shape on the device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+        _need(t, dtype, name)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _fp8_out(rows: int, K: int, q, s, device):
-    KB = _cdiv(K, FP8_BLOCK)
-    q = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device) if q is None else q
-    s = torch.empty((rows, KB), dtype=torch.float32, device=device) if s is None else s
-    _shaped(q, torch.float8_e4m3fn, (rows, K), "q")
-    _shaped(s, torch.float32, (rows, KB), "s")
-    return q, s
+def _handle(device: int, stream) -> int:
+    """The stream to launch on: of the tensors' device, which has to be the current one."""
+    if torch._C._cuda_getDevice() != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def q8_quantize_fp8(x: torch.Tensor, slots=None, rows: int | None = None, q=None, s=None, stream=None):
     """Float8 codes and scales (one for each row and block of 128) of x[M, K] (fp32, bf16 or fp16; rows may be
     strided). slots int32 [M, k]: row m goes to the rows slots[m] of the result instead (skipped where
     outside), which has `rows` rows (default M * k). Returns (q float8_e4m3fn [rows, K], s fp32 [rows, ceil(K / 128)])."""
-    ldx = _rows(x, "x")
-    M, K = x.shape
-    top_k = 0
+    M, K, ldx, kind = _float_rows(x, "x")
+    dev = x.get_device()
+    top_k, to = 0, None
     if slots is not None:
         _need(slots, torch.int32, "slots", 2)
-        if slots.shape[0] != M:
-            raise ValueError("slots must have a row for each row of x")
         top_k = slots.shape[1]
+        to = _dense(slots, torch.int32, (M, top_k), dev, "slots")
         rows = M * top_k if rows is None else rows
     elif rows is not None and rows != M:
         raise ValueError("rows goes with slots")
     else:
         rows = M
-    q, s = _fp8_out(rows, K, q, s, x.device)
-    _same_device(x, slots=slots, q=q, s=s)
-    _check(load().q8_quantize_fp8(_ptr(x), FLOAT_TYPES[x.dtype], M, K, ldx, _ptr(slots), top_k, rows, _ptr(q), _ptr(s),
-                                  _stream(stream)), "q8_quantize_fp8")
+    KB = _cdiv(K, FP8_BLOCK)
+    q = _new((rows, K), _FP8, x) if q is None else q
+    s = _new((rows, KB), torch.float32, x) if s is None else s
+    _check(load().q8_quantize_fp8(x.data_ptr(), kind, M, K, ldx, to, top_k, rows, _dense(q, _FP8, (rows, K), dev, "q"),
+                                  _dense(s, torch.float32, (rows, KB), dev, "s"), _handle(dev, stream)),
+           "q8_quantize_fp8")
     return q, s
 
 
 def q8_swiglu_quantize_fp8(h: torch.Tensor, q=None, s=None, stream=None):
     """Codes and scales of silu(h[:, :I]) * h[:, I:], h[M, 2 I] (rows may be strided)."""
-    ldh = _rows(h, "h")
-    M = h.shape[0]
-    if h.shape[1] % 2:
+    M, cols, ldh, kind = _float_rows(h, "h")
+    if cols % 2:
         raise ValueError("h must have an even number of columns")
-    I = h.shape[1] // 2
-    q, s = _fp8_out(M, I, q, s, h.device)
-    _same_device(h, q=q, s=s)
-    _check(load().q8_swiglu_quantize_fp8(_ptr(h), FLOAT_TYPES[h.dtype], M, I, ldh, _ptr(q), _ptr(s), _stream(stream)),
+    I, KB, dev = cols // 2, _cdiv(cols // 2, FP8_BLOCK), h.get_device()
+    q = _new((M, I), _FP8, h) if q is None else q
+    s = _new((M, KB), torch.float32, h) if s is None else s
+    _check(load().q8_swiglu_quantize_fp8(h.data_ptr(), kind, M, I, ldh, _dense(q, _FP8, (M, I), dev, "q"),
+                                         _dense(s, torch.float32, (M, KB), dev, "s"), _handle(dev, stream)),
            "q8_swiglu_quantize_fp8")
     return q, s
 
@@ -726,51 +731,49 @@ def q8_quantize_weight_fp8(w: torch.Tensor, qw=None, sw=None, stream=None):
         raise ValueError("w must be [N, K] or [E, N, K]")
     N, K = w.shape[-2:]
     E = w.shape[0] if w.dim() == 3 else 1
+    dev = w.get_device()
     scales = (*w.shape[:-2], _cdiv(N, FP8_BLOCK), _cdiv(K, FP8_BLOCK))
-    qw = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device) if qw is None else qw
-    sw = torch.empty(scales, dtype=torch.float32, device=w.device) if sw is None else sw
-    _shaped(qw, torch.float8_e4m3fn, w.shape, "qw")
-    _shaped(sw, torch.float32, scales, "sw")
-    _same_device(w, qw=qw, sw=sw)
-    _check(load().q8_quantize_weight_fp8(_ptr(w), FLOAT_TYPES[w.dtype], E, N, K, _ptr(qw), _ptr(sw), _stream(stream)),
+    qw = _new(w.shape, _FP8, w) if qw is None else qw
+    sw = _new(scales, torch.float32, w) if sw is None else sw
+    _check(load().q8_quantize_weight_fp8(w.data_ptr(), FLOAT_TYPES[w.dtype], E, N, K, _dense(qw, _FP8, w.shape, dev, "qw"),
+                                         _dense(sw, torch.float32, scales, dev, "sw"), _handle(dev, stream)),
            "q8_quantize_weight_fp8")
     return qw, sw
 
 
 def _fp8_operands(qa, sa, qw, sw, ndim, out_dtype, out):
-    _need(qa, torch.float8_e4m3fn, "qa", 2)
-    _need(qw, torch.float8_e4m3fn, "qw", ndim)
+    """Addresses and sizes of a product: (device, M, N, K, pointers of qa, sa, qw, sw and out, type, out)."""
+    _need(qa, _FP8, "qa", 2)
+    _need(qw, _FP8, "qw", ndim)
     M, K = qa.shape
-    N = qw.shape[-2]
-    if qw.shape[-1] != K:
+    shape = qw.shape
+    N = shape[-2]
+    if shape[-1] != K:
         raise ValueError("qa and qw disagree on K")
-    _shaped(sa, torch.float32, (M, _cdiv(K, FP8_BLOCK)), "sa")
-    _shaped(sw, torch.float32, (*qw.shape[:-2], _cdiv(N, FP8_BLOCK), _cdiv(K, FP8_BLOCK)), "sw")
-    if out_dtype not in FLOAT_TYPES:
+    kind = FLOAT_TYPES.get(out_dtype)
+    if kind is None:
         raise TypeError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
-    out = torch.empty((M, N), dtype=out_dtype, device=qa.device) if out is None else out
-    _shaped(out, out_dtype, (M, N), "out")
-    return M, N, K, out
+    dev, KB = qa.get_device(), _cdiv(K, FP8_BLOCK)
+    out = _new((M, N), out_dtype, qa) if out is None else out
+    return (dev, M, N, K, qa.data_ptr(), _dense(sa, torch.float32, (M, KB), dev, "sa"), _dense(qw, _FP8, shape, dev, "qw"),
+            _dense(sw, torch.float32, (*shape[:-2], _cdiv(N, FP8_BLOCK), KB), dev, "sw"),
+            _dense(out, out_dtype, (M, N), dev, "out"), kind, out)
 
 
 def q8_gemm_fp8(qa, sa, qw, sw, out_dtype=torch.bfloat16, out=None, stream=None):
     """y[m, n] = sum over blocks b of sa[m, b] sw[n / 128, b] (qa . qw over block b), as out_dtype [M, N]."""
-    M, N, K, out = _fp8_operands(qa, sa, qw, sw, 2, out_dtype, out)
-    _same_device(qa, sa=sa, qw=qw, sw=sw, out=out)
-    _check(load().q8_gemm_fp8(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), M, N, K, _ptr(out), FLOAT_TYPES[out_dtype],
-                              _stream(stream)), "q8_gemm_fp8")
+    dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 2, out_dtype, out)
+    _check(load().q8_gemm_fp8(pa, psa, pw, psw, M, N, K, py, kind, _handle(dev, stream)), "q8_gemm_fp8")
     return out
 
 
 def q8_gemm_fp8_grouped(qa, sa, qw, sw, offsets, out_dtype=torch.bfloat16, out=None, stream=None):
     """The product of q8_gemm_fp8 with qw[e] (of qw[E, N, K]) for the rows offsets[e] .. offsets[e + 1] - 1 of each
     expert; offsets int32 [E + 1] stay on the device. Rows of no expert are not written."""
-    M, N, K, out = _fp8_operands(qa, sa, qw, sw, 3, out_dtype, out)
+    dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 3, out_dtype, out)
     E = qw.shape[0]
-    _shaped(offsets, torch.int32, (E + 1,), "offsets")
-    _same_device(qa, sa=sa, qw=qw, sw=sw, offsets=offsets, out=out)
-    _check(load().q8_gemm_fp8_grouped(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(offsets), M, E, N, K, _ptr(out),
-                                      FLOAT_TYPES[out_dtype], _stream(stream)), "q8_gemm_fp8_grouped")
+    _check(load().q8_gemm_fp8_grouped(pa, psa, pw, psw, _dense(offsets, torch.int32, (E + 1,), dev, "offsets"), M, E, N, K,
+                                      py, kind, _handle(dev, stream)), "q8_gemm_fp8_grouped")
     return out
 
 
@@ -780,22 +783,19 @@ def q8_moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=
     (idx int32 [T, top_k], weights fp32 [T, top_k]). score: "softmax" or "sigmoid"; bias fp32 [E] takes part in
     the choice only; with n_group groups only experts of the topk_group best groups are chosen. Masked experts
     (logit -inf or NaN) are not chosen; places that stay empty have idx -1 and weight 0."""
-    ldl = _rows(logits, "logits")
-    T, E = logits.shape
+    T, E, ldl, kind = _float_rows(logits, "logits")
     if score not in SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     if top_k < 1:
         raise ValueError("top_k must be positive")
-    if bias is not None:
-        _shaped(bias, torch.float32, (E,), "bias")
-    idx = torch.empty((T, top_k), dtype=torch.int32, device=logits.device) if idx is None else idx
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device) if weights is None else weights
-    _shaped(idx, torch.int32, (T, top_k), "idx")
-    _shaped(weights, torch.float32, (T, top_k), "weights")
-    _same_device(logits, bias=bias, idx=idx, weights=weights)
-    _check(load().q8_moe_route(_ptr(logits), FLOAT_TYPES[logits.dtype], T, E, ldl, top_k, SCORES[score], _ptr(bias),
-                               n_group, topk_group, int(renorm), ctypes.c_float(scale), _ptr(idx), _ptr(weights),
-                               _stream(stream)), "q8_moe_route")
+    dev = logits.get_device()
+    pb = None if bias is None else _dense(bias, torch.float32, (E,), dev, "bias")
+    idx = _new((T, top_k), torch.int32, logits) if idx is None else idx
+    weights = _new((T, top_k), torch.float32, logits) if weights is None else weights
+    _check(load().q8_moe_route(logits.data_ptr(), kind, T, E, ldl, top_k, SCORES[score], pb, n_group, topk_group,
+                               1 if renorm else 0, scale, _dense(idx, torch.int32, (T, top_k), dev, "idx"),
+                               _dense(weights, torch.float32, (T, top_k), dev, "weights"), _handle(dev, stream)),
+           "q8_moe_route")
     return idx, weights
 
 
@@ -803,30 +803,28 @@ def q8_moe_plan(idx: torch.Tensor, n_experts: int, offsets=None, slots=None, str
     """The choices idx int32 [T, k] sorted by expert (stable): (offsets int32 [n_experts + 1], slots int32 [T, k]),
     the first row of each expert and the row of each choice (-1 where idx is outside [0, n_experts))."""
     _need(idx, torch.int32, "idx", 2)
-    T, k = idx.shape
     if n_experts < 1:
         raise ValueError("n_experts must be positive")
-    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=idx.device) if offsets is None else offsets
-    slots = torch.empty((T, k), dtype=torch.int32, device=idx.device) if slots is None else slots
-    _shaped(offsets, torch.int32, (n_experts + 1,), "offsets")
-    _shaped(slots, torch.int32, (T, k), "slots")
-    _same_device(idx, offsets=offsets, slots=slots)
-    _check(load().q8_moe_plan(_ptr(idx), T, k, n_experts, _ptr(offsets), _ptr(slots), _stream(stream)), "q8_moe_plan")
+    T, k = idx.shape
+    dev = idx.get_device()
+    offsets = _new((n_experts + 1,), torch.int32, idx) if offsets is None else offsets
+    slots = _new((T, k), torch.int32, idx) if slots is None else slots
+    _check(load().q8_moe_plan(idx.data_ptr(), T, k, n_experts, _dense(offsets, torch.int32, (n_experts + 1,), dev, "offsets"),
+                              _dense(slots, torch.int32, (T, k), dev, "slots"), _handle(dev, stream)), "q8_moe_plan")
     return offsets, slots
 
 
 def q8_moe_combine(h: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, out=None, stream=None):
     """y[t] = sum_j weights[t, j] h[slots[t, j]] (fp32 sums), h[rows, N] and y[T, N] of one float type. Slots outside
     [0, rows) add nothing."""
-    if _rows(h, "h") != h.shape[1] or not h.is_contiguous():
+    rows, N, pitch, kind = _float_rows(h, "h")
+    if pitch != N:
         raise ValueError("h must be contiguous")
-    rows, N = h.shape
     _need(slots, torch.int32, "slots", 2)
     T, k = slots.shape
-    _shaped(weights, torch.float32, (T, k), "weights")
-    out = torch.empty((T, N), dtype=h.dtype, device=h.device) if out is None else out
-    _shaped(out, h.dtype, (T, N), "out")
-    _same_device(h, slots=slots, weights=weights, out=out)
-    _check(load().q8_moe_combine(_ptr(h), FLOAT_TYPES[h.dtype], rows, N, _ptr(slots), _ptr(weights), T, k, _ptr(out),
-                                 _stream(stream)), "q8_moe_combine")
+    dev = h.get_device()
+    out = _new((T, N), h.dtype, h) if out is None else out
+    _check(load().q8_moe_combine(h.data_ptr(), kind, rows, N, _dense(slots, torch.int32, (T, k), dev, "slots"),
+                                 _dense(weights, torch.float32, (T, k), dev, "weights"), T, k,
+                                 _dense(out, h.dtype, (T, N), dev, "out"), _handle(dev, stream)), "q8_moe_combine")
     return out
