@@ -429,6 +429,347 @@ cudaError_t launch_swap(const CUtensorMap& ma, const CUtensorMap& mw, SwapArgs p
     return e;
 }
 
+
+// ------------------------------------------------------------------ tokens on the MMA's M side, CTA pairs
+// For many tokens: a cluster of two CTAs shares a tile of 256 token rows x 256 weight rows
+// (cta_group::2; each CTA loads half of both and holds its 128 token rows' accumulators). Per CTA:
+//   warp 0     TMA: tokens and weights [128 x 128] of each K block, completing on the even CTA's barrier
+//   warp 1     even CTA: pair MMA issuer; TMEM in both
+//   warps 4-11 drain: a TMEM lane is a token row, so a thread's scale is one product a block,
+//              sa[row] sw[its 128 weight rows], and the sum costs one multiply-add a value
+constexpr int PT = 256, PTH = 128;
+constexpr int kPairThreads = 384;
+constexpr int kPairRegsLow = 56, kPairRegsHigh = 224;
+static_assert(128 * kPairRegsLow + 256 * kPairRegsHigh <= kPairThreads * 168, "above the launch's registers");
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * PTH * BK;         // 32 KB
+constexpr int kPairEpi = 2048;                   // of a drain warp: 32 rows x 64 bytes
+constexpr int kPairOffEpi = kPairStages * kPairStage;
+constexpr int kPairOffBar = kPairOffEpi + 8 * kPairEpi;
+constexpr int kPairSmem = 1024 + kPairOffBar + 8 * (2 * kPairStages + 4) + 32 + 4 * (kMaxExperts + 2);
+static_assert(kPairSmem <= kSmemMax, "above the shared memory of one CTA");
+constexpr uint32_t kIdescPair = idesc_f16(PT, PT);
+constexpr int kBand = 8;                         // token tiles that share a sweep over the weights
+
+struct PairArgs {
+    const float* sa;
+    const float* sw;
+    const int32_t* offsets;
+    int rows, E, N, K;
+    void* y;
+    q8_float_type type;
+};
+
+// Units in bands of kBand token tiles, the weight tiles swept inside a band, so that the tiles that run
+// together share both operands in L2.
+__device__ __forceinline__ void pair_unit(int64_t u, int tiles, int NT, int& t, int& nt) {
+    const int64_t per = (int64_t)kBand * NT;
+    const int band = (int)(u / per), within = (int)(u - band * per);
+    const int here = min(kBand, tiles - band * kBand);
+    t = band * kBand + within % here;
+    nt = within / here;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Two values as stored: one 32-bit word of a 16-bit type, or two words of fp32.
+template <class T>
+__device__ __forceinline__ uint32_t pack16(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A drain warp's 32 rows x 128 columns (one row a lane) to y, 64 bytes of each row at a time through shared
+// memory (16-byte chunk j of row r at j ^ (r / 2 % 4): no bank conflicts either way), so that
+// four lanes write 64 neighbouring bytes. Rows of y that are not whole 16-byte chunks go value by value.
+template <class T>
+__device__ __forceinline__ void store_rows(T* y, int64_t row0, int live, int col0, int N, const uint64_t (&acc)[64],
+                                           uint32_t buf, int lane) {
+    constexpr int kCols = 64 / sizeof(T);         // columns of a step
+    const bool vec = (N * sizeof(T)) % 16 == 0;
+#pragma unroll
+    for (int c = 0; c < 128 / kCols; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if constexpr (sizeof(T) == 2) {
+                const float2 f = unpack2(acc[c * 16 + j]);
+                w[j] = pack16<T>(f.x, f.y);
+            } else {
+                const float2 f = unpack2(acc[c * 8 + j / 2]);
+                w[j] = __float_as_uint(j & 1 ? f.y : f.x);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sts128(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
+                   make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4, j = lane & 3;
+            const int col = col0 + c * kCols + j * (16 / (int)sizeof(T));
+            if (r < live && col < N) {
+                const uint4 v = lds128(buf + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+                T* out = y + (row0 + r) * N + col;
+                if (vec) {
+                    *reinterpret_cast<uint4*>(out) = v;
+                } else {
+                    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 16 / (int)sizeof(T); ++q)
+                        if (col + q < N) {
+                            if constexpr (sizeof(T) == 2) {
+                                const uint16_t h = (uint16_t)(words[q / 2] >> (16 * (q & 1)));
+                                *reinterpret_cast<uint16_t*>(out + q) = h;
+                            } else {
+                                *reinterpret_cast<uint32_t*>(out + q) = words[q];
+                            }
+                        }
+                }
+            }
+        }
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                         PairArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t sraw = smem_u32(smem_raw);
+    const uint32_t sbase = (sraw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (sbase - sraw);
+    const uint32_t bar_full = sbase + kPairOffBar;             // used in the even CTA: both CTAs' loads
+    const uint32_t bar_empty = bar_full + 8 * kPairStages;     // both CTAs: the pair MMA's commit
+    const uint32_t bar_accfull = bar_empty + 8 * kPairStages;  // both CTAs: the pair MMA's commit
+    const uint32_t bar_accempty = bar_accfull + 16;            // used in the even CTA: 2 x 8 drain warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBar + 8 * (2 * kPairStages + 4));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* cum = reinterpret_cast<int*>(tmem_slot + 2);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_accfull + 8 * b, 1);
+            mbar_init(bar_accempty + 8 * b, 16);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+    }
+    const Groups groups{p.offsets, cum, p.rows, p.E, PT};
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    if (warp == 2) groups.scan(cum, lane);
+    tc_fence_before();
+    cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int NT = (p.N + PT - 1) / PT, KB = (p.K + BK - 1) / BK;
+    const int tiles = cum[p.E];
+    const int64_t units = (int64_t)tiles * NT;
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPairRegsLow));
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------------------------ TMA
+            uint32_t s = 0, phase = 1;
+            bool ok = true;
+            for (int64_t u = first; u < units && ok; u += step) {
+                int t, nt, e, row, n;
+                pair_unit(u, tiles, NT, t, nt);
+                groups.tile(t, e, row, n);
+                const int arow = row + rank * PTH, wrow = e * p.N + nt * PT + rank * PTH;
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + s * kPairStage;
+                    if (rank == 0) mbar_expect_tx(bar_full + 8 * s, 2 * kPairStage);
+                    const uint32_t bar = mapa_shared(bar_full + 8 * s, 0);
+                    tma_load_2d_pair(dst, &tmap_a, kb * BK, arow, bar);
+                    tma_load_2d_pair(dst + PTH * BK, &tmap_w, kb * BK, wrow, bar);
+                    if (++s == kPairStages) { s = 0; phase ^= 1; }
+                }
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ------------------------------------------------------------------------ MMA
+            uint32_t s = 0, phase = 0, c = 0;
+            bool ok = true;
+            for (int64_t u = first; u < units && ok; u += step) {
+                for (int kb = 0; kb < KB; ++kb, ++c) {
+                    const uint32_t buf = c & 1;
+                    if (!mbar_wait_cluster(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrMmaAcc,
+                                           &g_fp8_error) ||
+                        !mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a = smem_desc_sw128(sbase + s * kPairStage);
+                    const uint64_t w = smem_desc_sw128(sbase + s * kPairStage + PTH * BK);
+#pragma unroll
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        mma_fp8_pair(tmem_base + buf * PT, a + 2 * kk, w + 2 * kk, kIdescPair, kk ? 1u : 0u);
+                    mma_commit_pair(bar_empty + 8 * s, 3);
+                    mma_commit_pair(bar_accfull + 8 * buf, 3);
+                    if (++s == kPairStages) { s = 0; phase ^= 1; }
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------------------- drain
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kPairRegsHigh));
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * PTH;
+        const uint32_t free_bar = mapa_shared(bar_accempty, 0);
+        const int NB = (p.N + BK - 1) / BK;
+        uint32_t c = 0;
+        bool ok = true;
+        for (int64_t u = first; u < units && ok; u += step) {
+            int t, nt, e, row, n;
+            pair_unit(u, tiles, NT, t, nt);
+            groups.tile(t, e, row, n);
+            const int r0 = rank * PTH + quarter * 32;      // the warp's first row in the tile
+            const float* sa = p.sa + (int64_t)min(row + r0 + lane, p.rows - 1) * KB;
+            const float* sw = p.sw + ((int64_t)e * NB + min(nt * 2 + half, NB - 1)) * KB;
+            uint64_t acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            // the scales of four blocks are loaded while the four before are used
+            float sc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[i] = i < KB ? __ldg(sa + i) * __ldg(sw + i) : 0.0f;
+            for (int kb0 = 0; kb0 < KB && ok; kb0 += 4) {
+                float na[4], nw[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = kb0 + 4 + i < KB;
+                    na[i] = in ? __ldg(sa + kb0 + 4 + i) : 0.0f;
+                    nw[i] = in ? __ldg(sw + kb0 + 4 + i) : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (kb0 + i >= KB) break;
+                    const uint32_t buf = c & 1;
+                    if (!mbar_wait(bar_accfull + 8 * buf, (c >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t s2 = pack2(sc[i], sc[i]);
+                    uint32_t v[64];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_ld64(tlane + buf * PT + h * 64, v);
+                        if (h == 1) {   // everything is read: the buffer may be filled again
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_remote(free_bar + 8 * buf);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            acc[h * 32 + j] = fma2(pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s2,
+                                                   acc[h * 32 + j]);
+                    }
+                    ++c;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[i] = na[i] * nw[i];
+            }
+            if (!ok) break;
+            const int live = min(32, n - r0), col0 = nt * PT + half * PTH;
+            const uint32_t buf = sbase + kPairOffEpi + (warp - 4) * kPairEpi;
+            if (live > 0 && col0 < p.N) {
+                if (p.type == Q8_BF16)
+                    store_rows(static_cast<__nv_bfloat16*>(p.y), row + r0, live, col0, p.N, acc, buf, lane);
+                else if (p.type == Q8_F16)
+                    store_rows(static_cast<__half*>(p.y), row + r0, live, col0, p.N, acc, buf, lane);
+                else
+                    store_rows(static_cast<float*>(p.y), row + r0, live, col0, p.N, acc, buf, lane);
+            }
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1LL << 22)) __nanosleep(1000);
+    }
+    tc_fence_before();
+    cluster_sync();   // neither CTA frees TMEM or leaves while the other may still use its part
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+// Once per device: the shared-memory limit, and the clusters of two that run at once.
+cudaError_t pair_clusters(int& clusters) {
+    static int cached[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && cached[dev] > 0) {
+        clusters = cached[dev];
+        return cudaSuccess;
+    }
+    e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    if (e != cudaSuccess) return e;
+    clusters = device_sm_count() / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = kPairSmem;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, gemm_fp8_pair_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n > 0 && n < clusters) clusters = n;
+    if (dev < 64) cached[dev] = clusters;
+    return cudaSuccess;
+}
+
+cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mw, const PairArgs& p, int64_t max_tiles,
+                        cudaStream_t stream) {
+    int clusters = 0;
+    cudaError_t e = pair_clusters(clusters);
+    if (e != cudaSuccess) return e;
+    const int64_t units = max_tiles * ((p.N + PT - 1) / PT);
+    if (units < clusters) clusters = (int)units;
+    gemm_fp8_pair_kernel<<<2 * clusters, kPairThreads, kPairSmem, stream>>>(ma, mw, p);
+    note_launch();
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
@@ -436,6 +777,14 @@ cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* q
                             q8_float_type t, cudaStream_t stream) {
     // Token rows of a tile: the rows of a group (on average), up to 256.
     const int64_t per = (rows + E - 1) / E;
+    if (per > 256) {
+        const int64_t max_tiles = offsets ? rows / PT + (E < rows ? E : rows) : (rows + PT - 1) / PT;
+        CUtensorMap ma, mw;
+        if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), rows, K, PTH, BK, true) ||
+            !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)E * N, K, PTH, BK, true))
+            return cudaErrorInvalidValue;
+        return launch_pair(ma, mw, PairArgs{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t}, max_tiles, stream);
+    }
     const int tn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
     const int64_t max_tiles = offsets ? rows / tn + (E < rows ? E : rows) : (rows + tn - 1) / tn;
     const int64_t NT = (N + TW - 1) / TW, KB = (K + BK - 1) / BK;
