@@ -435,18 +435,27 @@ cudaError_t launch_swap(const CUtensorMap& ma, const CUtensorMap& mw, SwapArgs p
 // (cta_group::2; each CTA loads half of both and holds its 128 token rows' accumulators). Per CTA:
 //   warp 0     TMA: tokens and weights [128 x 128] of each K block, completing on the even CTA's barrier
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
-//   warps 4-11 drain: a TMEM lane is a token row, so a thread's scale is one product a block,
-//              sa[row] sw[its 128 weight rows], and the sum costs one multiply-add a value
+//   warps 2, 3 scales: sa sw of the CTA's 128 token rows and the tile's two weight blocks, eight K blocks at a
+//              time (a sector of a row of sa), into shared memory
+//   warps 4-11 drain: a TMEM lane is a token row, so a thread's scale is one value a block, and the sum
+//              costs one multiply-add a value; two warps for each quarter of the lanes, 128 columns each
 constexpr int PT = 256, PTH = 128;
-constexpr int kPairThreads = 384;
-constexpr int kPairRegsLow = 56, kPairRegsHigh = 224;
-static_assert(128 * kPairRegsLow + 256 * kPairRegsHigh <= kPairThreads * 168, "above the launch's registers");
+constexpr int kPairDrain = 8;                    // drain warps
+constexpr int kPairThreads = 128 + 32 * kPairDrain;
+constexpr int kPairCols = PT * 4 / kPairDrain;   // accumulator columns of a drain warp
+constexpr int kPairLd = 64;                      // columns of one TMEM load
+constexpr int kPairRegsLow = 88, kPairRegsHigh = 208;
+static_assert(128 * kPairRegsLow + 32 * kPairDrain * kPairRegsHigh <= kPairThreads * (65536 / kPairThreads / 8 * 8), "above the launch's registers");
 constexpr int kPairStages = 6;
 constexpr int kPairStage = 2 * PTH * BK;         // 32 KB
-constexpr int kPairEpi = 2048;                   // of a drain warp: 32 rows x 64 bytes
+constexpr int kPairEpi = 1024;                   // of a drain warp: 32 rows x 32 bytes
 constexpr int kPairOffEpi = kPairStages * kPairStage;
-constexpr int kPairOffBar = kPairOffEpi + 8 * kPairEpi;
-constexpr int kPairSmem = 1024 + kPairOffBar + 8 * (2 * kPairStages + 4) + 32 + 4 * (kMaxExperts + 2);
+constexpr int kScaleBlocks = 8;                  // K blocks of one hand-over of scales
+constexpr int kScalePitch = PTH + 4;             // floats of a block's row of scales: no bank conflicts
+constexpr int kScaleHalf = kScaleBlocks * kScalePitch;
+constexpr int kPairOffScale = kPairOffEpi + kPairDrain * kPairEpi;
+constexpr int kPairOffBar = kPairOffScale + 2 * 2 * kScaleHalf * 4;
+constexpr int kPairSmem = 1024 + kPairOffBar + 8 * (2 * kPairStages + 8) + 32 + 4 * (kMaxExperts + 2);
 static_assert(kPairSmem <= kSmemMax, "above the shared memory of one CTA");
 constexpr uint32_t kIdescPair = idesc_f16(PT, PT);
 constexpr int kBand = 8;                         // token tiles that share a sweep over the weights
@@ -469,6 +478,10 @@ __device__ __forceinline__ void pair_unit(int64_t u, int tiles, int NT, int& t, 
     t = band * kBand + within % here;
     nt = within / here;
 }
+
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[16]) { tmem_ld16(a, v); }
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[32]) { tmem_ld32(a, v); }
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[64]) { tmem_ld64(a, v); }
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -500,39 +513,40 @@ __device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A drain warp's 32 rows x 128 columns (one row a lane) to y, 64 bytes of each row at a time through shared
-// memory (16-byte chunk j of row r at j ^ (r / 2 % 4): no bank conflicts either way), so that
-// four lanes write 64 neighbouring bytes. Rows of y that are not whole 16-byte chunks go value by value.
+// A drain warp's 32 rows x kPairCols columns (one row a lane) to y, 32 bytes of each row at a time through
+// shared memory (16-byte chunk j of row r at j ^ (r / 4 % 2): no bank conflicts either way), so that
+// two lanes write a whole sector. Rows of y that are not whole 16-byte chunks go value by value.
 template <class T>
-__device__ __forceinline__ void store_rows(T* y, int64_t row0, int live, int col0, int N, const uint64_t (&acc)[64],
+__device__ __forceinline__ void store_rows(T* y, int64_t row0, int live, int col0, int N,
+                                           const uint64_t (&acc)[kPairCols / 2],
                                            uint32_t buf, int lane) {
-    constexpr int kCols = 64 / sizeof(T);         // columns of a step
+    constexpr int kCols = 32 / sizeof(T);         // columns of a step
     const bool vec = (N * sizeof(T)) % 16 == 0;
 #pragma unroll
-    for (int c = 0; c < 128 / kCols; ++c) {
-        uint32_t w[16];
+    for (int c = 0; c < kPairCols / kCols; ++c) {
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 8; ++j) {
             if constexpr (sizeof(T) == 2) {
-                const float2 f = unpack2(acc[c * 16 + j]);
+                const float2 f = unpack2(acc[c * 8 + j]);
                 w[j] = pack16<T>(f.x, f.y);
             } else {
-                const float2 f = unpack2(acc[c * 8 + j / 2]);
+                const float2 f = unpack2(acc[c * 4 + j / 2]);
                 w[j] = __float_as_uint(j & 1 ? f.y : f.x);
             }
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            sts128(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
+        for (int j = 0; j < 2; ++j)
+            sts128(buf + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4),
                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + lane / 4, j = lane & 3;
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 16 + lane / 2, j = lane & 1;
             const int col = col0 + c * kCols + j * (16 / (int)sizeof(T));
             if (r < live && col < N) {
-                const uint4 v = lds128(buf + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+                const uint4 v = lds128(buf + r * 32 + ((j ^ ((r >> 2) & 1)) << 4));
                 T* out = y + (row0 + r) * N + col;
                 if (vec) {
                     *reinterpret_cast<uint4*>(out) = v;
@@ -564,8 +578,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t bar_full = sbase + kPairOffBar;             // used in the even CTA: both CTAs' loads
     const uint32_t bar_empty = bar_full + 8 * kPairStages;     // both CTAs: the pair MMA's commit
     const uint32_t bar_accfull = bar_empty + 8 * kPairStages;  // both CTAs: the pair MMA's commit
-    const uint32_t bar_accempty = bar_accfull + 16;            // used in the even CTA: 2 x 8 drain warps
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBar + 8 * (2 * kPairStages + 4));
+    const uint32_t bar_accempty = bar_accfull + 16;            // used in the even CTA: both CTAs' drain warps
+    const uint32_t bar_scfull = bar_accempty + 16;
+    const uint32_t bar_scempty = bar_scfull + 16;
+    float* scales = reinterpret_cast<float*>(smem + kPairOffScale);   // [2 buffers][2 weight blocks][K block][row]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBar + 8 * (2 * kPairStages + 8));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* cum = reinterpret_cast<int*>(tmem_slot + 2);
 
@@ -578,7 +595,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_accfull + 8 * b, 1);
-            mbar_init(bar_accempty + 8 * b, 16);
+            mbar_init(bar_accempty + 8 * b, 2 * kPairDrain);
+            mbar_init(bar_scfull + 8 * b, 2);
+            mbar_init(bar_scempty + 8 * b, kPairDrain);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -647,69 +666,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (++s == kPairStages) { s = 0; phase ^= 1; }
                 }
             }
+        } else if (warp >= 2) {
+            // --------------------------------------------------------------------- scales
+            // A lane loads K block lane % 8 of every eighth row; the next eight blocks' loads are
+            // in flight while it waits for the buffer.
+            constexpr int kRows = PTH / 8;
+            const int NB = (p.N + BK - 1) / BK;
+            const int b = lane & 7, r0 = (warp - 2) * 4 + lane / 8;
+            uint32_t c = 0;
+            bool ok = true;
+            for (int64_t u = first; u < units && ok; u += step) {
+                int t, nt, e, row, n;
+                pair_unit(u, tiles, NT, t, nt);
+                groups.tile(t, e, row, n);
+                row += rank * PTH + r0;
+                const float* w0 = p.sw + ((int64_t)e * NB + nt * 2) * KB;
+                const float* w1 = nt * 2 + 1 < NB ? w0 + KB : w0;
+                const float* sa = p.sa + (int64_t)row * KB;
+                const int have = (p.rows - row + 7) / 8;   // rows of this lane that exist
+                float a[kRows], f0, f1;
+                auto load = [&](int kb) {
+                    const int rows_in = kb < KB ? have : 0;
+                    f0 = kb < KB ? __ldg(w0 + kb) : 0.0f;
+                    f1 = kb < KB ? __ldg(w1 + kb) : 0.0f;
+                    const float* from = sa + kb;
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i, from += 8 * KB) a[i] = i < rows_in ? __ldg(from) : 0.0f;
+                };
+                load(b);
+                for (int kb = 0; kb < KB; kb += kScaleBlocks, ++c) {
+                    const uint32_t buf = c & 1;
+                    if (!mbar_wait(bar_scempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrConvEmpty, &g_fp8_error)) {
+                        ok = false;
+                        break;
+                    }
+                    float* out = scales + buf * 2 * kScaleHalf + b * kScalePitch + r0;
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+                        out[8 * i] = a[i] * f0;
+                        out[8 * i + kScaleHalf] = a[i] * f1;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_scfull + 8 * buf);
+                    load(kb + kScaleBlocks + b);
+                }
+            }
         }
     } else {
         // ---------------------------------------------------------------------------- drain
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kPairRegsHigh));
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * PTH;
+        const int quarter = warp & 3, part = ((warp - 4) >> 2) * kPairCols;   // its first column
+        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + part;
         const uint32_t free_bar = mapa_shared(bar_accempty, 0);
-        const int NB = (p.N + BK - 1) / BK;
-        uint32_t c = 0;
+        const float* own = scales + (part / BK) * kScaleHalf + quarter * 32 + lane;
+        uint32_t c = 0, sc = 0;
         bool ok = true;
         for (int64_t u = first; u < units && ok; u += step) {
             int t, nt, e, row, n;
             pair_unit(u, tiles, NT, t, nt);
             groups.tile(t, e, row, n);
             const int r0 = rank * PTH + quarter * 32;      // the warp's first row in the tile
-            const float* sa = p.sa + (int64_t)min(row + r0 + lane, p.rows - 1) * KB;
-            const float* sw = p.sw + ((int64_t)e * NB + min(nt * 2 + half, NB - 1)) * KB;
-            uint64_t acc[64];
+            uint64_t acc[kPairCols / 2];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
-            // the scales of four blocks are loaded while the four before are used
-            float sc[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[i] = i < KB ? __ldg(sa + i) * __ldg(sw + i) : 0.0f;
-            for (int kb0 = 0; kb0 < KB && ok; kb0 += 4) {
-                float na[4], nw[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = kb0 + 4 + i < KB;
-                    na[i] = in ? __ldg(sa + kb0 + 4 + i) : 0.0f;
-                    nw[i] = in ? __ldg(sw + kb0 + 4 + i) : 0.0f;
+            for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
+            for (int kb = 0; kb < KB; ++kb, ++c) {
+                const uint32_t buf = c & 1, sbuf = sc & 1;
+                const int i = kb % kScaleBlocks;
+                if ((i == 0 && !mbar_wait(bar_scfull + 8 * sbuf, (sc >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) ||
+                    !mbar_wait(bar_accfull + 8 * buf, (c >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) {
+                    ok = false;
+                    break;
                 }
+                tc_fence_after();
+                const float f = own[sbuf * 2 * kScaleHalf + i * kScalePitch];
+                const uint64_t f2 = pack2(f, f);
+                uint32_t v[kPairLd];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (kb0 + i >= KB) break;
-                    const uint32_t buf = c & 1;
-                    if (!mbar_wait(bar_accfull + 8 * buf, (c >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) {
-                        ok = false;
-                        break;
+                for (int h = 0; h < kPairCols / kPairLd; ++h) {
+                    tmem_load(tlane + buf * PT + h * kPairLd, v);
+                    if (h == kPairCols / kPairLd - 1) {   // everything is read: the buffer may be filled again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(free_bar + 8 * buf);
                     }
-                    tc_fence_after();
-                    const uint64_t s2 = pack2(sc[i], sc[i]);
-                    uint32_t v[64];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tmem_ld64(tlane + buf * PT + h * 64, v);
-                        if (h == 1) {   // everything is read: the buffer may be filled again
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_remote(free_bar + 8 * buf);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            acc[h * 32 + j] = fma2(pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s2,
-                                                   acc[h * 32 + j]);
-                    }
-                    ++c;
+                    for (int j = 0; j < kPairLd / 2; ++j)
+                        acc[h * kPairLd / 2 + j] = fma2(pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f2,
+                                                        acc[h * kPairLd / 2 + j]);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sc[i] = na[i] * nw[i];
+                if (i == kScaleBlocks - 1 || kb == KB - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_scempty + 8 * sbuf);
+                    ++sc;
+                }
             }
             if (!ok) break;
-            const int live = min(32, n - r0), col0 = nt * PT + half * PTH;
+            const int live = min(32, n - r0), col0 = nt * PT + part;
             const uint32_t buf = sbase + kPairOffEpi + (warp - 4) * kPairEpi;
             if (live > 0 && col0 < p.N) {
                 if (p.type == Q8_BF16)
