@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     const uint32_t bar_accfull = bar_empty + 8 * kMaxStages;
     const uint32_t bar_accempty = bar_accfull + 16;
     const uint32_t bar_got = bar_accempty + 16;     // split: the partial sums of this CTA's tokens
-    const uint32_t bar_free = bar_got + 8;          // split: the other CTAs have read what this one sent
+    const uint32_t bar_free = bar_got + 8;          // split: every CTA's drain warps are done with a unit
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + off_bar + 8 * (2 * kMaxStages + 6));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* cum = reinterpret_cast<int*>(tmem_slot + 2);
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
             mbar_init(bar_accempty + 8 * b, kDrainThreads / 32);
         }
         mbar_init(bar_got, 1);
-        mbar_init(bar_free, p.split > 1 ? (p.split - 1) * (kDrainThreads / 32) : 1);
+        mbar_init(bar_free, p.split * (kDrainThreads / 32));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
@@ -366,8 +366,10 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                         acc[0][4 * q] = t.x; acc[0][4 * q + 1] = t.y; acc[0][4 * q + 2] = t.z; acc[0][4 * q + 3] = t.w;
                     }
                 }
+                // To every CTA, its own too: a warp arrives for this unit only after it has seen the last one's
+                // phase (the wait above), so no phase can be passed while a warp still waits for it.
                 __syncwarp();
-                if (lane < S && lane != rank) mbar_arrive_remote(mapa_shared(bar_free, lane));
+                if (lane < S) mbar_arrive_remote(mapa_shared(bar_free, lane));
             }
             if (col < p.N) {
 #pragma unroll

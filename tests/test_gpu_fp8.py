@@ -179,6 +179,18 @@ def test_gemm(q8, M, N, K):
     check(y, qa, sa, qw, sw, dtype)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 20480, 512), (3, 28672, 1024), (4, 11000, 2048), (5, 30000, 256), (40, 20000, 512)])
+def test_gemm_few_tokens_many_tiles(q8, M, N, K):
+    """Several tiles for each cluster, K shared by its CTAs, some of which own no token's sum (tokens go round in fours)."""
+    qa, sa, qw, sw = operands(M, 128, K, seed=M)
+    copies = ref.cdiv(N, 128)
+    qw = qw.view(torch.uint8).repeat(copies, 1)[:N].view(qw.dtype)
+    sw = sw.repeat(copies, 1) * (1.0 + torch.arange(copies)[:, None] % 7)
+    for _ in range(3):
+        y = q8.q8_gemm_fp8(qa.cuda(), sa.cuda(), qw.cuda(), sw.cuda(), out_dtype=torch.float32)
+    check(y, qa, sa, qw, sw, torch.float32)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("M,N,K", [(3, 200, 384), (200, 300, 384), (700, 515, 640)])
 def test_gemm_types_and_repeats(q8, dtype, M, N, K):
@@ -222,7 +234,7 @@ def test_gemm_empty_k(q8):
 
 COUNTS = [
     [1], [0, 1, 0], [3, 0, 5, 1], [16, 17, 15, 0, 33], [130, 1, 0, 64, 257], [0, 0, 300], [40] * 9, [513, 2, 700],
-    [1] * 40, [0] * 100 + [7] + [0] * 30,
+    [1] * 40, [0] * 100 + [7] + [0] * 30, [1, 2, 3, 4, 5] * 40,
 ]
 
 
