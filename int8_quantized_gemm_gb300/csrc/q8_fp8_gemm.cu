@@ -26,24 +26,20 @@ constexpr int kTileW = TW * BK;        // 16 KB
 constexpr uint32_t kIdescW = idesc_f16(TW, 0);   // fp32 D, e4m3 A and B, both K-major, M = 128
 
 // -------------------------------------------------------------------------- weights on the MMA's M side
-// A tile is 128 weight rows x up to TN token rows (16 .. 256), for few tokens (a whole weight block
-// is then read once, whatever the tokens) and for groups of few rows.
+// For few tokens a matrix: a tile is 128 weight rows x up to TN = 16, 32 or 64 token rows, so that a weight
+// block is read once whatever the tokens. Bound by the weights' bytes.
 //   warp 0     TMA: weights [128 x 128] and tokens [n x 128] of each K block, 128-byte swizzle
 //   warp 1     MMA issuer (N = n rounded up to 16), TMEM
 //   warps 2, 3 scales of the block's tokens, sa sw, into the buffer's scale row
-//   warps 4-11 drain: two warps for each quarter of the TMEM lanes (weight rows), each takes every
-//              other chunk of 32 tokens
+//   warps 4-11 drain: two warps for each quarter of the TMEM lanes (weight rows), half of the tokens each
 // With few tiles, a cluster of S CTAs splits a tile's K blocks; each CTA sends the partial sums of the
 // tokens it does not own to the CTA that does (st.async), which adds them in the order of the ranks:
 // the same bits every time, no workspace and no second launch.
 constexpr int kSwapThreads = 384;
-constexpr int kDrainThreads = 256;
-constexpr int kRegsLow = 88, kRegsHigh = 208;
-static_assert(128 * kRegsLow + 256 * kRegsHigh <= kSwapThreads * 168, "above the launch's registers");
-constexpr int kMaxStages = 8;
-constexpr int kScaleBytes = 2 * 256 * 4;
-constexpr int kReduceBytes = 32 * 1024;
-constexpr int kTailBytes = 8 * (2 * kMaxStages + 4 + 2) + 32 + 4 * (kMaxExperts + 2);
+constexpr int kDrainWarps = 8;
+constexpr int kBufs = 8;               // accumulator buffers: the MMA runs on while a tile is written out
+constexpr int kMaxStages = 12;
+constexpr int kTailBytes = 8 * (2 * kMaxStages + 2 * kBufs + 2) + 32 + 4 * (kMaxExperts + 2);
 constexpr int kSmemMax = 227 * 1024;
 
 struct SwapArgs {
@@ -52,7 +48,7 @@ struct SwapArgs {
     const int32_t* offsets;   // nullptr: one group of all rows
     int rows, E;
     int N, K;
-    int tn, box, stages;      // token rows of a tile, of a TMA box; stages of the ring
+    int stages;               // of the ring
     int split;                // CTAs of a cluster, sharing a tile's K blocks
     void* y;
     q8_float_type type;
@@ -110,61 +106,113 @@ struct Groups {
     }
 };
 
-__device__ __forceinline__ void store_one(void* y, q8_float_type t, int64_t at, float v) {
-    if (t == Q8_BF16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-    else if (t == Q8_F16) static_cast<__half*>(y)[at] = __float2half_rn(v);
-    else static_cast<float*>(y)[at] = v;
-}
-
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     const uint4 u = lds128(addr);
     return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
 }
 
-template <int CH>   // chunks of 32 tokens of a drain warp: tn <= 64 CH
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[8]) { tmem_ld8(a, v); }
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[16]) { tmem_ld16(a, v); }
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[32]) { tmem_ld32(a, v); }
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[64]) { tmem_ld64(a, v); }
+
+// Two values of a 16-bit type as one word.
+template <class T>
+__device__ __forceinline__ uint32_t pack16(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// acc[j]: weight row (column of y) col, token t0 + j. Tokens are stored where t < n and (t / 4) % split == rank
+// (all of them for split = 1). 16-bit types: neighbouring lanes trade values, so that each stores two
+// columns of one token as a word; y's rows have to start on whole words for that.
+template <class T, int CW>
+__device__ __forceinline__ void store_tokens(T* y, int64_t row, int t0, int n, int col, int N, const float (&acc)[CW],
+                                             int split, int rank, int lane) {
+    if (sizeof(T) == 2 && N % 2 == 0) {
+        const int odd = lane & 1;
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < CW; j += 2) {
+                const float give = odd ? acc[j] : acc[j + 1];
+                const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+                const int t = t0 + j + odd;
+                if (t < n && col < N && (split == 1 || (t / 4) % split == rank))
+                    *reinterpret_cast<uint32_t*>(y + (row + t) * N + (col - odd)) =
+                        odd ? pack16<T>(got, acc[j + 1]) : pack16<T>(acc[j], got);
+            }
+        }
+    } else if (col < N) {
+#pragma unroll
+        for (int j = 0; j < CW; ++j) {
+            const int t = t0 + j;
+            if (t < n && (split == 1 || (t / 4) % split == rank)) y[(row + t) * N + col] = from_float<T>(acc[j]);
+        }
+    }
+}
+
+template <int CW>   // tokens of a drain warp; TN = 2 CW
+struct SwapCfg {
+    static constexpr int TN = 2 * CW;
+    static constexpr int kBox = TN < 32 ? TN : 32;              // token rows of a TMA box
+    static constexpr int kStage = kTileW + TN * BK;
+    static constexpr int kScale = kBufs * TN * 4;
+    static constexpr int kTmem = kBufs * TN;                    // 128, 256 or 512 columns
+    // receive buffer: the groups of four tokens that a CTA owns, from each other CTA
+    static int reduce_bytes(int split) { return (split - 1) * ((TN / 4 + split - 1) / split) * TW * 16; }
+};
+
+template <int CW>
 __global__ void __launch_bounds__(kSwapThreads, 1)
     gemm_fp8_swap_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
-                         SwapArgs p) {
+                         SwapArgs p, int reduce_bytes) {
+    using C = SwapCfg<CW>;
+    constexpr int TN = C::TN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sraw = smem_u32(smem_raw);
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (sbase - sraw);
-    const uint32_t stage_bytes = kTileW + p.tn * BK;
-    const uint32_t off_scale = p.stages * stage_bytes;
-    const uint32_t off_reduce = off_scale + kScaleBytes;
-    const uint32_t off_bar = off_reduce + (p.split > 1 ? kReduceBytes : 0);
+    const uint32_t off_scale = p.stages * C::kStage;
+    const uint32_t off_reduce = off_scale + C::kScale;
+    const uint32_t off_bar = off_reduce + reduce_bytes;
     const uint32_t bar_full = sbase + off_bar;
     const uint32_t bar_empty = bar_full + 8 * kMaxStages;
     const uint32_t bar_accfull = bar_empty + 8 * kMaxStages;
-    const uint32_t bar_accempty = bar_accfull + 16;
-    const uint32_t bar_got = bar_accempty + 16;     // split: the partial sums of this CTA's tokens
-    const uint32_t bar_free = bar_got + 8;          // split: every CTA's drain warps are done with a unit
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + off_bar + 8 * (2 * kMaxStages + 6));
+    const uint32_t bar_accempty = bar_accfull + 8 * kBufs;
+    const uint32_t bar_got = bar_accempty + 8 * kBufs;   // split: the partial sums of this CTA's tokens
+    const uint32_t bar_free = bar_got + 8;               // split: every CTA's drain warps are done with a unit
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + off_bar + 8 * (2 * kMaxStages + 2 * kBufs + 2));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* cum = reinterpret_cast<int*>(tmem_slot + 2);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
-    const int acc_cols = CH * 64 < 32 ? 32 : CH * 64;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kBufs; ++b) {
             mbar_init(bar_accfull + 8 * b, 3);    // the MMA's commit and the two scale warps
-            mbar_init(bar_accempty + 8 * b, kDrainThreads / 32);
+            mbar_init(bar_accempty + 8 * b, kDrainWarps);
         }
         mbar_init(bar_got, 1);
-        mbar_init(bar_free, p.split * (kDrainThreads / 32));
+        mbar_init(bar_free, p.split * kDrainWarps);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
     }
-    const Groups groups{p.offsets, cum, p.rows, p.E, p.tn};
-    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 2 * acc_cols);
+    const Groups groups{p.offsets, cum, p.rows, p.E, TN};
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmem);
     if (warp == 2) groups.scan(cum, lane);
     tc_fence_before();
     if (p.split > 1) cluster_sync();
@@ -177,163 +225,135 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     const int64_t first = blockIdx.x / p.split, step = gridDim.x / p.split;
     const int kb0 = (int)((int64_t)KB * rank / p.split), kb1 = (int)((int64_t)KB * (rank + 1) / p.split);
 
-    if (warp < 4) {
-        if constexpr (CH > 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsLow));
-        if (warp == 0) {
-            // ------------------------------------------------------------------------ TMA
-            if (lane == 0) {
-                uint32_t s = 0, phase = 1;
-                bool ok = true;
-                for (int64_t u = first; u < units && ok; u += step) {
-                    int e, row, n;
-                    groups.tile((int)(u / NT), e, row, n);
-                    const int nt = (int)(u % NT), boxes = (n + p.box - 1) / p.box;
-                    const int wrow = e * p.N + nt * TW;
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t dst = sbase + s * stage_bytes, bar = bar_full + 8 * s;
-                        mbar_expect_tx(bar, kTileW + boxes * p.box * BK);
-                        tma_load_2d(dst, &tmap_w, kb * BK, wrow, bar);
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(dst + kTileW + b * p.box * BK, &tmap_a, kb * BK, row + b * p.box, bar);
-                        if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
-                    }
-                }
-            }
-        } else if (warp == 1) {
-            // ------------------------------------------------------------------------ MMA
-            if (lane == 0) {
-                uint32_t s = 0, phase = 0, c = 0;
-                bool ok = true;
-                for (int64_t u = first; u < units && ok; u += step) {
-                    int e, row, n;
-                    groups.tile((int)(u / NT), e, row, n);
-                    const uint32_t idesc = kIdescW + ((uint32_t)((n + 15) >> 4) << 18);   // N = n rounded up to 16
-                    for (int kb = kb0; kb < kb1; ++kb, ++c) {
-                        const uint32_t buf = c & 1;
-                        if (!mbar_wait(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrMmaAcc,
-                                       &g_fp8_error) ||
-                            !mbar_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t w = smem_desc_sw128(sbase + s * stage_bytes);
-                        const uint64_t a = smem_desc_sw128(sbase + s * stage_bytes + kTileW);
-                        const uint32_t d = tmem_base + buf * acc_cols;
-#pragma unroll
-                        for (int kk = 0; kk < BK / 32; ++kk)
-                            mma_fp8(d, w + 2 * kk, a + 2 * kk, idesc, kk ? 1u : 0u);
-                        mma_commit(bar_empty + 8 * s);
-                        mma_commit(bar_accfull + 8 * buf);
-                        if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
-                    }
-                }
-            }
-        } else {
-            // --------------------------------------------------------------------- scales
-            // Four blocks' scales are loaded ahead of the four being handed out.
-            constexpr int kAhead = 4, kCols = (CH + 1) / 2;   // token columns of a lane: 64 CH / 64, at least 1
-            uint32_t c = 0;
+    if (warp == 0) {
+        // ---------------------------------------------------------------------------- TMA
+        if (lane == 0) {
+            uint32_t s = 0, phase = 1;
             bool ok = true;
             for (int64_t u = first; u < units && ok; u += step) {
                 int e, row, n;
                 groups.tile((int)(u / NT), e, row, n);
-                const int nt = (int)(u % NT);
-                const float* sw = p.sw + ((int64_t)e * NT + nt) * KB;
-                float a[2][kAhead][2 * kCols], w[2][kAhead];
-                auto load = [&](int kb, float (&av)[kAhead][2 * kCols], float (&wv)[kAhead]) {
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        const bool in = kb + i < kb1;
-                        wv[i] = in ? __ldg(sw + kb + i) : 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 2 * kCols; ++j) {
-                            const int col = (warp - 2) * 32 + lane + 64 * j;
-                            av[i][j] = in && col < n ? __ldg(p.sa + (int64_t)(row + col) * KB + kb + i) : 0.0f;
-                        }
+                const int nt = (int)(u % NT), boxes = (n + C::kBox - 1) / C::kBox;
+                const int wrow = e * p.N + nt * TW;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
+                        ok = false;
+                        break;
                     }
-                };
-                load(kb0, a[0], w[0]);
-                for (int kb = kb0; kb < kb1 && ok; kb += kAhead) {
-                    load(kb + kAhead, a[1], w[1]);
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        if (kb + i >= kb1) break;
-                        const uint32_t buf = c & 1;
-                        if (!mbar_wait(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrConvEmpty,
-                                       &g_fp8_error)) {
-                            ok = false;
-                            break;
-                        }
-                        float* out = reinterpret_cast<float*>(smem + off_scale) + buf * 256 + (warp - 2) * 32 + lane;
-#pragma unroll
-                        for (int j = 0; j < 2 * kCols; ++j)
-                            if (j < CH) out[64 * j] = a[0][i][j] * w[0][i];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_accfull + 8 * buf);
-                        ++c;
+                    const uint32_t dst = sbase + s * C::kStage, bar = bar_full + 8 * s;
+                    mbar_expect_tx(bar, kTileW + boxes * C::kBox * BK);
+                    tma_load_2d(dst, &tmap_w, kb * BK, wrow, bar);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d(dst + kTileW + b * C::kBox * BK, &tmap_a, kb * BK, row + b * C::kBox, bar);
+                    if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------------------- MMA
+        if (lane == 0) {
+            uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
+            bool ok = true;
+            for (int64_t u = first; u < units && ok; u += step) {
+                int e, row, n;
+                groups.tile((int)(u / NT), e, row, n);
+                const uint32_t idesc = kIdescW + ((uint32_t)((n + 15) >> 4) << 18);   // N = n rounded up to 16
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc, &g_fp8_error) ||
+                        !mbar_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error)) {
+                        ok = false;
+                        break;
                     }
+                    tc_fence_after();
+                    const uint64_t w = smem_desc_sw128(sbase + s * C::kStage);
+                    const uint64_t a = smem_desc_sw128(sbase + s * C::kStage + kTileW);
+                    const uint32_t d = tmem_base + buf * TN;
 #pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        w[0][i] = w[1][i];
+                    for (int kk = 0; kk < BK / 32; ++kk) mma_fp8(d, w + 2 * kk, a + 2 * kk, idesc, kk ? 1u : 0u);
+                    mma_commit(bar_empty + 8 * s);
+                    mma_commit(bar_accfull + 8 * buf);
+                    if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
+                    if (++buf == kBufs) { buf = 0; bphase ^= 1; }
+                }
+            }
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------------------- scales
+        // A lane has one token. Four blocks' scales are loaded ahead of the four being handed out.
+        constexpr int kAhead = 4;
+        const int col = (warp - 2) * 32 + lane;
+        uint32_t buf = 0, bphase = 1;
+        bool ok = true;
+        for (int64_t u = first; u < units && ok; u += step) {
+            int e, row, n;
+            groups.tile((int)(u / NT), e, row, n);
+            const float* sw = p.sw + ((int64_t)e * NT + (int)(u % NT)) * KB;
+            const float* sa = p.sa + (int64_t)(row + min(col, n - 1)) * KB;
+            float next[kAhead];
+            auto load = [&](int kb) {
 #pragma unroll
-                        for (int j = 0; j < 2 * kCols; ++j) a[0][i][j] = a[1][i][j];
+                for (int i = 0; i < kAhead; ++i)
+                    next[i] = kb + i < kb1 && col < n ? __ldg(sa + kb + i) * __ldg(sw + kb + i) : 0.0f;
+            };
+            load(kb0);
+            for (int kb = kb0; kb < kb1 && ok; kb += kAhead) {
+                float now[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) now[i] = next[i];
+                load(kb + kAhead);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (kb + i >= kb1) break;
+                    if (!mbar_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrConvEmpty, &g_fp8_error)) {
+                        ok = false;
+                        break;
                     }
+                    if (col < TN) reinterpret_cast<float*>(smem + off_scale)[buf * TN + col] = now[i];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_accfull + 8 * buf);
+                    if (++buf == kBufs) { buf = 0; bphase ^= 1; }
                 }
             }
         }
     } else {
-        // ---------------------------------------------------------------------------- drain
-        if constexpr (CH > 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsHigh));
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16);
-        uint32_t c = 0, done = 0;
+        // -------------------------------------------------------------------------- drain
+        const int quarter = warp & 3, t0 = ((warp - 4) >> 2) * CW;   // its first token
+        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + t0;
+        uint32_t buf = 0, bphase = 0, done = 0;
         bool ok = true;
         for (int64_t u = first; u < units && ok; u += step, ++done) {
             int e, row, n;
             groups.tile((int)(u / NT), e, row, n);
             const int col = (int)(u % NT) * TW + quarter * 32 + lane;   // this thread's weight row
-            float acc[CH][32];
+            float acc[CW];
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) acc[i][j] = 0.0f;
-            for (int kb = kb0; kb < kb1; ++kb, ++c) {
-                const uint32_t buf = c & 1;
-                if (!mbar_wait(bar_accfull + 8 * buf, (c >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) {
+            for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain, &g_fp8_error)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sc = sbase + off_scale + buf * 1024;
+                if (t0 < n) {
+                    uint32_t v[CW];
+                    tmem_load(tlane + buf * TN, v);
+                    const uint32_t sc = sbase + off_scale + (buf * TN + t0) * 4;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int t0 = (2 * i + half) * 32;
-                    if (t0 < n) {
-                        uint32_t v[32];
-                        tmem_ld32(tlane + buf * acc_cols + t0, v);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 f = lds_f4(sc + (t0 + j) * 4);
-                            acc[i][j] = __fmaf_rn(__uint_as_float(v[j]), f.x, acc[i][j]);
-                            acc[i][j + 1] = __fmaf_rn(__uint_as_float(v[j + 1]), f.y, acc[i][j + 1]);
-                            acc[i][j + 2] = __fmaf_rn(__uint_as_float(v[j + 2]), f.z, acc[i][j + 2]);
-                            acc[i][j + 3] = __fmaf_rn(__uint_as_float(v[j + 3]), f.w, acc[i][j + 3]);
-                        }
+                    for (int j = 0; j < CW; j += 4) {
+                        const float4 f = lds_f4(sc + j * 4);
+                        acc[j] = __fmaf_rn(__uint_as_float(v[j]), f.x, acc[j]);
+                        acc[j + 1] = __fmaf_rn(__uint_as_float(v[j + 1]), f.y, acc[j + 1]);
+                        acc[j + 2] = __fmaf_rn(__uint_as_float(v[j + 2]), f.z, acc[j + 2]);
+                        acc[j + 3] = __fmaf_rn(__uint_as_float(v[j + 3]), f.w, acc[j + 3]);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_accempty + 8 * buf);
+                if (++buf == kBufs) { buf = 0; bphase ^= 1; }
             }
             if (!ok) break;
-            int own_shift = 0;   // tokens in groups of four: group g is added up by CTA g % split
-            if (CH == 1 && p.split > 1) {
-                own_shift = 1;
+            if (p.split > 1) {   // tokens in groups of four: group g is added up by CTA g % split
                 const int S = p.split, groups4 = (n + 3) / 4;
                 const int per = (groups4 + S - 1) / S;          // slots of groups in the receive buffer
                 const int here = (groups4 - rank + S - 1) / S;  // groups that this CTA owns (may be 0)
@@ -341,29 +361,29 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                 if (done && !mbar_wait_cluster(bar_free, (done - 1) & 1, abort_flag, kErrRelay, &g_fp8_error)) break;
                 if (warp == 4 && lane == 0) mbar_expect_tx(bar_got, (S - 1) * max(here, 0) * TW * 16);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int g = half * 8 + q, owner = g % S;
+                for (int q = 0; q < CW / 4; ++q) {
+                    const int g = t0 / 4 + q, owner = g % S;
                     if (g < groups4 && owner != rank) {
                         const int slot = (rank < owner ? rank : rank - 1) * per + g / S;
                         st_async16(mapa_shared(buffer + slot * (TW * 16) + lane16, owner),
-                                   make_uint4(__float_as_uint(acc[0][4 * q]), __float_as_uint(acc[0][4 * q + 1]),
-                                              __float_as_uint(acc[0][4 * q + 2]), __float_as_uint(acc[0][4 * q + 3])),
+                                   make_uint4(__float_as_uint(acc[4 * q]), __float_as_uint(acc[4 * q + 1]),
+                                              __float_as_uint(acc[4 * q + 2]), __float_as_uint(acc[4 * q + 3])),
                                    mapa_shared(bar_got, owner));
                     }
                 }
                 if (!mbar_wait_cluster(bar_got, done & 1, abort_flag, kErrRelay, &g_fp8_error)) break;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int g = half * 8 + q;
+                for (int q = 0; q < CW / 4; ++q) {
+                    const int g = t0 / 4 + q;
                     if (g < groups4 && g % S == rank) {
                         float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         for (int r = 0; r < S; ++r) {
-                            float4 f = make_float4(acc[0][4 * q], acc[0][4 * q + 1], acc[0][4 * q + 2], acc[0][4 * q + 3]);
+                            float4 f = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
                             if (r != rank)
                                 f = lds_f4(buffer + ((r < rank ? r : r - 1) * per + g / S) * (TW * 16) + lane16);
                             t.x += f.x; t.y += f.y; t.z += f.z; t.w += f.w;
                         }
-                        acc[0][4 * q] = t.x; acc[0][4 * q + 1] = t.y; acc[0][4 * q + 2] = t.z; acc[0][4 * q + 3] = t.w;
+                        acc[4 * q] = t.x; acc[4 * q + 1] = t.y; acc[4 * q + 2] = t.z; acc[4 * q + 3] = t.w;
                     }
                 }
                 // To every CTA, its own too: a warp arrives for this unit only after it has seen the last one's
@@ -371,16 +391,12 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                 __syncwarp();
                 if (lane < S) mbar_arrive_remote(mapa_shared(bar_free, lane));
             }
-            if (col < p.N) {
-#pragma unroll
-                for (int i = 0; i < CH; ++i)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int t = (2 * i + half) * 32 + j;
-                        if (t < n && (!own_shift || (t / 4) % p.split == rank))
-                            store_one(p.y, p.type, (int64_t)(row + t) * p.N + col, acc[i][j]);
-                    }
-            }
+            if (p.type == Q8_BF16)
+                store_tokens(static_cast<__nv_bfloat16*>(p.y), row, t0, n, col, p.N, acc, p.split, rank, lane);
+            else if (p.type == Q8_F16)
+                store_tokens(static_cast<__half*>(p.y), row, t0, n, col, p.N, acc, p.split, rank, lane);
+            else
+                store_tokens(static_cast<float*>(p.y), row, t0, n, col, p.N, acc, p.split, rank, lane);
         }
     }
 
@@ -394,43 +410,83 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     if (p.split > 1) cluster_sync();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, 2 * acc_cols);
+    if (warp == 1) tmem_dealloc(tmem_base, C::kTmem);
 }
 
-template <int CH>
-cudaError_t launch_swap(const CUtensorMap& ma, const CUtensorMap& mw, SwapArgs p, int64_t max_tiles,
-                        cudaStream_t stream) {
-    const int stage = kTileW + p.tn * BK;
-    const int room = kSmemMax - 1024 - kTailBytes - kScaleBytes - (p.split > 1 ? kReduceBytes : 0);
-    p.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    const int smem = 1024 + p.stages * stage + kScaleBytes + (p.split > 1 ? kReduceBytes : 0) + kTailBytes;
-    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_swap_kernel<CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+// Clusters of `split` CTAs that run at once; the kernel's shared-memory limit is raised on the first call.
+// Kept per device and split (a query takes longer than a small product).
+template <int CW>
+cudaError_t swap_clusters(int split, int& clusters) {
+    static int cached[64][4] = {};
+    const int log = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 64 && cached[dev][log] > 0) {
+        clusters = cached[dev][log];
+        return cudaSuccess;
+    }
+    e = cudaFuncSetAttribute(gemm_fp8_swap_kernel<CW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    clusters = device_sm_count() / split;
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * split), 1, 1);
     cfg.blockDim = dim3(kSwapThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmemMax;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    e = cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_swap_kernel<CW>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (fit > 0 && fit < clusters) clusters = fit;
+    if (dev < 64) cached[dev][log] = clusters;
+    return cudaSuccess;
+}
+
+template <int CW>
+cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_t max_tiles, cudaStream_t stream) {
+    using C = SwapCfg<CW>;
+    const int64_t units = max_tiles * ((p.N + TW - 1) / TW), KB = (p.K + BK - 1) / BK;
+    // The split that ends first: rounds of units over the clusters, each a part of K and a fixed cost of about
+    // four blocks (the exchange and the store).
+    int clusters = 0;
+    double best = 0.0;
+    for (int S = 1; S <= 8 && (S == 1 || S * 2 <= KB); S *= 2) {
+        int fit = 0;
+        const cudaError_t e = swap_clusters<CW>(S, fit);
+        if (e != cudaSuccess) return e;
+        const double cost = (double)((units + fit - 1) / fit) * (double)((KB + S - 1) / S + 4);
+        if (S == 1 || cost < best * 0.98) {
+            best = cost;
+            p.split = S;
+            clusters = fit;
+        }
+    }
+    const int reduce = p.split > 1 ? C::reduce_bytes(p.split) : 0;
+    const int room = kSmemMax - 1024 - kTailBytes - C::kScale - reduce;
+    p.stages = room / C::kStage < kMaxStages ? room / C::kStage : kMaxStages;
+    CUtensorMap ma, mw;
+    if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), p.rows, p.K, C::kBox, BK, true) ||
+        !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)p.E * p.N, p.K, TW, BK, true))
+        return cudaErrorInvalidValue;
+    if (units < clusters) clusters = (int)units;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
+    cfg.blockDim = dim3(kSwapThreads, 1, 1);
+    cfg.dynamicSmemBytes = 1024 + p.stages * C::kStage + C::kScale + reduce + kTailBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {(unsigned)p.split, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int64_t clusters = device_sm_count() / p.split;
-    if (p.split > 1) {
-        cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
-        int fit = 0;
-        e = cudaOccupancyMaxActiveClusters(&fit, gemm_fp8_swap_kernel<CH>, &cfg);
-        if (e != cudaSuccess) return e;
-        if (fit > 0 && fit < clusters) clusters = fit;
-    }
-    const int64_t units = max_tiles * ((p.N + TW - 1) / TW);
-    if (units < clusters) clusters = units;
-    cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
-    e = cudaLaunchKernelEx(&cfg, gemm_fp8_swap_kernel<CH>, ma, mw, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp8_swap_kernel<CW>, ma, mw, p, reduce);
     note_launch();
     return e;
 }
-
 
 // ------------------------------------------------------------------ tokens on the MMA's M side, CTA pairs
 // For many tokens: a cluster of two CTAs shares a tile of 256 token rows x 256 weight rows
@@ -481,10 +537,6 @@ __device__ __forceinline__ void pair_unit(int64_t u, int tiles, int NT, int& t, 
     nt = within / here;
 }
 
-__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[16]) { tmem_ld16(a, v); }
-__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[32]) { tmem_ld32(a, v); }
-__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[64]) { tmem_ld64(a, v); }
-
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
@@ -499,20 +551,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
-}
-
-// Two values as stored: one 32-bit word of a 16-bit type, or two words of fp32.
-template <class T>
-__device__ __forceinline__ uint32_t pack16(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <>
-__device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // A drain warp's 32 rows x kPairCols columns (one row a lane) to y, 32 bytes of each row at a time through
@@ -812,11 +850,15 @@ cudaError_t pair_clusters(int& clusters) {
     return cudaSuccess;
 }
 
-cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mw, const PairArgs& p, int64_t max_tiles,
+cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, const PairArgs& p, int64_t max_tiles,
                         cudaStream_t stream) {
     int clusters = 0;
-    cudaError_t e = pair_clusters(clusters);
+    const cudaError_t e = pair_clusters(clusters);
     if (e != cudaSuccess) return e;
+    CUtensorMap ma, mw;
+    if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), p.rows, p.K, PTH, BK, true) ||
+        !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)p.E * p.N, p.K, PTH, BK, true))
+        return cudaErrorInvalidValue;
     const int64_t units = max_tiles * ((p.N + PT - 1) / PT);
     if (units < clusters) clusters = (int)units;
     gemm_fp8_pair_kernel<<<2 * clusters, kPairThreads, kPairSmem, stream>>>(ma, mw, p);
@@ -829,39 +871,15 @@ cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mw, const Pair
 cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
                             const int32_t* offsets, int64_t rows, int E, int64_t N, int64_t K, void* y,
                             q8_float_type t, cudaStream_t stream) {
-    // Token rows of a tile: the rows of a group (on average), up to 256.
-    const int64_t per = (rows + E - 1) / E;
-    if (per > 256) {
-        const int64_t max_tiles = offsets ? rows / PT + (E < rows ? E : rows) : (rows + PT - 1) / PT;
-        CUtensorMap ma, mw;
-        if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), rows, K, PTH, BK, true) ||
-            !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)E * N, K, PTH, BK, true))
-            return cudaErrorInvalidValue;
-        return launch_pair(ma, mw, PairArgs{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t}, max_tiles, stream);
-    }
-    const int tn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
-    const int64_t max_tiles = offsets ? rows / tn + (E < rows ? E : rows) : (rows + tn - 1) / tn;
-    const int64_t NT = (N + TW - 1) / TW, KB = (K + BK - 1) / BK;
-    if (max_tiles * NT >= (1LL << 40)) return cudaErrorNotSupported;
-    SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, tn, tn < 32 ? tn : 32, 0, 1, y, t};
-    if (tn <= 64) {
-        // the split that ends first: rounds of units over the clusters, a part of K each
-        const int sms = device_sm_count();
-        const int64_t units = max_tiles * NT;
-        double best = 1e30;
-        for (int S = 1; S <= 8 && S * 2 <= KB; S *= 2) {
-            const int64_t rounds = (units + sms / S - 1) / (sms / S);
-            const double cost = (double)rounds * ((KB + S - 1) / S + 4.0);
-            if (cost < best * 0.98) { best = cost; p.split = S; }
-        }
-    }
-    CUtensorMap ma, mw;
-    if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), rows, K, p.box, BK, true) ||
-        !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)E * N, K, TW, BK, true))
-        return cudaErrorInvalidValue;
-    if (tn <= 64) return launch_swap<1>(ma, mw, p, max_tiles, stream);
-    if (tn <= 128) return launch_swap<2>(ma, mw, p, max_tiles, stream);
-    return launch_swap<4>(ma, mw, p, max_tiles, stream);
+    const int64_t per = (rows + E - 1) / E;   // rows of a group, on average
+    const int64_t NT = (N + TW - 1) / TW;
+    auto tiles = [&](int tn) { return offsets ? rows / tn + (E < rows ? E : rows) : (rows + tn - 1) / tn; };
+    if (tiles(16) * NT >= (1LL << 40)) return cudaErrorNotSupported;
+    if (per > 64) return launch_pair(qa, qw, PairArgs{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t}, tiles(PT), stream);
+    const SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, 0, 1, y, t};
+    if (per <= 16) return launch_swap<8>(qa, qw, p, tiles(16), stream);
+    if (per <= 32) return launch_swap<16>(qa, qw, p, tiles(32), stream);
+    return launch_swap<32>(qa, qw, p, tiles(64), stream);
 }
 
 cudaError_t read_and_clear_gemm_fp8_error(uint32_t* code) {
