@@ -38,7 +38,8 @@ constexpr uint32_t kIdescW = idesc_f16(TW, 0);   // fp32 D, e4m3 A and B, both K
 constexpr int kSwapThreads = 384;
 constexpr int kDrainWarps = 8;
 constexpr int kBufs = 8;               // accumulator buffers: the MMA runs on while a tile is written out
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;          // more bytes in flight cost DRAM row hits: 128 rows of 64 experts 4096x4096
+                                       // 175 us with 12 stages, 168 with 10, 163 with 8, 166 with 6
 constexpr int kTailBytes = 8 * (2 * kMaxStages + 2 * kBufs + 2) + 32 + 4 * (kMaxExperts + 2);
 constexpr int kSmemMax = 227 * 1024;
 
@@ -139,21 +140,22 @@ __device__ __forceinline__ void store_tokens(T* y, int64_t row, int t0, int n, i
     if (sizeof(T) == 2 && N % 2 == 0) {
         const int odd = lane & 1;
         if constexpr (sizeof(T) == 2) {
+            T* out = y + (row + t0 + odd) * N + (col - odd);
 #pragma unroll
-            for (int j = 0; j < CW; j += 2) {
+            for (int j = 0; j < CW; j += 2, out += 2 * (int64_t)N) {
                 const float give = odd ? acc[j] : acc[j + 1];
                 const float got = __shfl_xor_sync(0xffffffffu, give, 1);
                 const int t = t0 + j + odd;
-                if (t < n && col < N && (split == 1 || (t / 4) % split == rank))
-                    *reinterpret_cast<uint32_t*>(y + (row + t) * N + (col - odd)) =
-                        odd ? pack16<T>(got, acc[j + 1]) : pack16<T>(acc[j], got);
+                if (t < n && col < N && (split == 1 || ((t / 4) & (split - 1)) == rank))
+                    *reinterpret_cast<uint32_t*>(out) = odd ? pack16<T>(got, acc[j + 1]) : pack16<T>(acc[j], got);
             }
         }
     } else if (col < N) {
+        T* out = y + (row + t0) * N + col;
 #pragma unroll
-        for (int j = 0; j < CW; ++j) {
+        for (int j = 0; j < CW; ++j, out += N) {
             const int t = t0 + j;
-            if (t < n && (split == 1 || (t / 4) % split == rank)) y[(row + t) * N + col] = from_float<T>(acc[j]);
+            if (t < n && (split == 1 || ((t / 4) & (split - 1)) == rank)) *out = from_float<T>(acc[j]);
         }
     }
 }
@@ -195,23 +197,30 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, 1);
-        }
-        for (int b = 0; b < kBufs; ++b) {
-            mbar_init(bar_accfull + 8 * b, 3);    // the MMA's commit and the two scale warps
-            mbar_init(bar_accempty + 8 * b, kDrainWarps);
-        }
-        mbar_init(bar_got, 1);
-        mbar_init(bar_free, p.split * kDrainWarps);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
-    }
+    const int NT = (p.N + TW - 1) / TW, KB = (p.K + BK - 1) / BK;
+    const uint32_t first = blockIdx.x / p.split, step = gridDim.x / p.split;
+    const int kb0 = KB / p.split * rank + min(rank, KB % p.split);   // this CTA's share of the K blocks
+    const int kb1 = kb0 + KB / p.split + (rank < KB % p.split ? 1 : 0);
     const Groups groups{p.offsets, cum, p.rows, p.E, TN};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+            for (int s = 0; s < p.stages; ++s) {
+                mbar_init(bar_full + 8 * s, 1);
+                mbar_init(bar_empty + 8 * s, 1);
+            }
+            for (int b = 0; b < kBufs; ++b) {
+                mbar_init(bar_accfull + 8 * b, 3);    // the MMA's commit and the two scale warps
+                mbar_init(bar_accempty + 8 * b, kDrainWarps);
+            }
+            mbar_init(bar_got, 1);
+            mbar_init(bar_free, p.split * kDrainWarps);
+            *abort_flag = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        }
+    }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmem);
     if (warp == 2) groups.scan(cum, lane);
     tc_fence_before();
@@ -219,62 +228,61 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-
-    const int NT = (p.N + TW - 1) / TW, KB = (p.K + BK - 1) / BK;
-    const int64_t units = (int64_t)cum[p.E] * NT;
-    const int64_t first = blockIdx.x / p.split, step = gridDim.x / p.split;
-    const int kb0 = (int)((int64_t)KB * rank / p.split), kb1 = (int)((int64_t)KB * (rank + 1) / p.split);
+    const uint32_t units = (uint32_t)cum[p.E] * NT;
 
     if (warp == 0) {
         // ---------------------------------------------------------------------------- TMA
-        if (lane == 0) {
-            uint32_t s = 0, phase = 1;
-            bool ok = true;
-            for (int64_t u = first; u < units && ok; u += step) {
-                int e, row, n;
-                groups.tile((int)(u / NT), e, row, n);
-                const int nt = (int)(u % NT), boxes = (n + C::kBox - 1) / C::kBox;
-                const int wrow = e * p.N + nt * TW;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t dst = sbase + s * C::kStage, bar = bar_full + 8 * s;
+        uint32_t s = 0, phase = 1;
+        bool ok = true;
+        for (uint32_t u = first; u < units && ok; u += step) {
+            int e, row, n;
+            groups.tile((int)(u / (uint32_t)NT), e, row, n);
+            const int wrow = e * p.N + (int)(u % (uint32_t)NT) * TW, boxes = (n + C::kBox - 1) / C::kBox;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const bool got = mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = sbase + s * C::kStage, bar = bar_full + 8 * s;
+                if (elect_one()) {
                     mbar_expect_tx(bar, kTileW + boxes * C::kBox * BK);
                     tma_load_2d(dst, &tmap_w, kb * BK, wrow, bar);
                     for (int b = 0; b < boxes; ++b)
                         tma_load_2d(dst + kTileW + b * C::kBox * BK, &tmap_a, kb * BK, row + b * C::kBox, bar);
-                    if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
                 }
+                __syncwarp();
+                if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
             }
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------------------- MMA
-        if (lane == 0) {
-            uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
-            bool ok = true;
-            for (int64_t u = first; u < units && ok; u += step) {
-                int e, row, n;
-                groups.tile((int)(u / NT), e, row, n);
-                const uint32_t idesc = kIdescW + ((uint32_t)((n + 15) >> 4) << 18);   // N = n rounded up to 16
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc, &g_fp8_error) ||
-                        !mbar_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t w = smem_desc_sw128(sbase + s * C::kStage);
-                    const uint64_t a = smem_desc_sw128(sbase + s * C::kStage + kTileW);
-                    const uint32_t d = tmem_base + buf * TN;
+        uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
+        bool ok = true;
+        for (uint32_t u = first; u < units && ok; u += step) {
+            int e, row, n;
+            groups.tile((int)(u / (uint32_t)NT), e, row, n);
+            const uint32_t idesc = kIdescW + ((uint32_t)((n + 15) >> 4) << 18);   // N = n rounded up to 16
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const bool got = mbar_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc, &g_fp8_error) &&
+                                 mbar_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t w = smem_desc_sw128(sbase + s * C::kStage);
+                const uint64_t a = smem_desc_sw128(sbase + s * C::kStage + kTileW);
+                const uint32_t d = tmem_base + buf * TN;
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; ++kk) mma_fp8(d, w + 2 * kk, a + 2 * kk, idesc, kk ? 1u : 0u);
                     mma_commit(bar_empty + 8 * s);
                     mma_commit(bar_accfull + 8 * buf);
-                    if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
-                    if (++buf == kBufs) { buf = 0; bphase ^= 1; }
                 }
+                __syncwarp();
+                if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
+                if (++buf == kBufs) { buf = 0; bphase ^= 1; }
             }
         }
     } else if (warp < 4) {
@@ -284,10 +292,10 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
         const int col = (warp - 2) * 32 + lane;
         uint32_t buf = 0, bphase = 1;
         bool ok = true;
-        for (int64_t u = first; u < units && ok; u += step) {
+        for (uint32_t u = first; u < units && ok; u += step) {
             int e, row, n;
-            groups.tile((int)(u / NT), e, row, n);
-            const float* sw = p.sw + ((int64_t)e * NT + (int)(u % NT)) * KB;
+            groups.tile((int)(u / (uint32_t)NT), e, row, n);
+            const float* sw = p.sw + ((int64_t)e * NT + (int)(u % (uint32_t)NT)) * KB;
             const float* sa = p.sa + (int64_t)(row + min(col, n - 1)) * KB;
             float next[kAhead];
             auto load = [&](int kb) {
@@ -321,10 +329,10 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + t0;
         uint32_t buf = 0, bphase = 0, done = 0;
         bool ok = true;
-        for (int64_t u = first; u < units && ok; u += step, ++done) {
+        for (uint32_t u = first; u < units && ok; u += step, ++done) {
             int e, row, n;
-            groups.tile((int)(u / NT), e, row, n);
-            const int col = (int)(u % NT) * TW + quarter * 32 + lane;   // this thread's weight row
+            groups.tile((int)(u / (uint32_t)NT), e, row, n);
+            const int col = (int)(u % (uint32_t)NT) * TW + quarter * 32 + lane;   // this thread's weight row
             float acc[CW];
 #pragma unroll
             for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
             }
             if (!ok) break;
             if (p.split > 1) {   // tokens in groups of four: group g is added up by CTA g % split
-                const int S = p.split, groups4 = (n + 3) / 4;
+                const int S = p.split, log = __ffs(S) - 1, groups4 = (n + 3) / 4;
                 const int per = (groups4 + S - 1) / S;          // slots of groups in the receive buffer
                 const int here = (groups4 - rank + S - 1) / S;  // groups that this CTA owns (may be 0)
                 const uint32_t buffer = sbase + off_reduce, lane16 = (quarter * 32 + lane) * 16;
@@ -362,9 +370,9 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                 if (warp == 4 && lane == 0) mbar_expect_tx(bar_got, (S - 1) * max(here, 0) * TW * 16);
 #pragma unroll
                 for (int q = 0; q < CW / 4; ++q) {
-                    const int g = t0 / 4 + q, owner = g % S;
+                    const int g = t0 / 4 + q, owner = g & (S - 1);
                     if (g < groups4 && owner != rank) {
-                        const int slot = (rank < owner ? rank : rank - 1) * per + g / S;
+                        const int slot = (rank < owner ? rank : rank - 1) * per + (g >> log);
                         st_async16(mapa_shared(buffer + slot * (TW * 16) + lane16, owner),
                                    make_uint4(__float_as_uint(acc[4 * q]), __float_as_uint(acc[4 * q + 1]),
                                               __float_as_uint(acc[4 * q + 2]), __float_as_uint(acc[4 * q + 3])),
@@ -375,12 +383,12 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
 #pragma unroll
                 for (int q = 0; q < CW / 4; ++q) {
                     const int g = t0 / 4 + q;
-                    if (g < groups4 && g % S == rank) {
+                    if (g < groups4 && (g & (S - 1)) == rank) {
                         float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         for (int r = 0; r < S; ++r) {
                             float4 f = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
                             if (r != rank)
-                                f = lds_f4(buffer + ((r < rank ? r : r - 1) * per + g / S) * (TW * 16) + lane16);
+                                f = lds_f4(buffer + ((r < rank ? r : r - 1) * per + (g >> log)) * (TW * 16) + lane16);
                             t.x += f.x; t.y += f.y; t.z += f.z; t.w += f.w;
                         }
                         acc[4 * q] = t.x; acc[4 * q + 1] = t.y; acc[4 * q + 2] = t.z; acc[4 * q + 3] = t.w;
@@ -446,25 +454,33 @@ cudaError_t swap_clusters(int split, int& clusters) {
     return cudaSuccess;
 }
 
+// The split that ends first: rounds of tiles over the clusters, each a part of the K blocks and a fixed cost of
+// about four blocks (the exchange and the store). `cost`: in blocks of one CTA.
 template <int CW>
-cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_t max_tiles, cudaStream_t stream) {
-    using C = SwapCfg<CW>;
-    const int64_t units = max_tiles * ((p.N + TW - 1) / TW), KB = (p.K + BK - 1) / BK;
-    // The split that ends first: rounds of units over the clusters, each a part of K and a fixed cost of about
-    // four blocks (the exchange and the store).
-    int clusters = 0;
-    double best = 0.0;
+cudaError_t swap_plan(int64_t tiles, int64_t N, int64_t K, int& split, int& clusters, double& cost) {
+    const int64_t units = tiles * ((N + TW - 1) / TW), KB = (K + BK - 1) / BK;
     for (int S = 1; S <= 8 && (S == 1 || S * 2 <= KB); S *= 2) {
         int fit = 0;
         const cudaError_t e = swap_clusters<CW>(S, fit);
         if (e != cudaSuccess) return e;
-        const double cost = (double)((units + fit - 1) / fit) * (double)((KB + S - 1) / S + 4);
-        if (S == 1 || cost < best * 0.98) {
-            best = cost;
-            p.split = S;
+        const double c = (double)((units + fit - 1) / fit) * (double)((KB + S - 1) / S + 4);
+        if (S == 1 || c < cost * 0.98) {
+            cost = c;
+            split = S;
             clusters = fit;
         }
     }
+    if (units < clusters) clusters = (int)units;
+    return cudaSuccess;
+}
+
+template <int CW>
+cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_t tiles, cudaStream_t stream) {
+    using C = SwapCfg<CW>;
+    int clusters = 0;
+    double cost = 0.0;
+    cudaError_t e = swap_plan<CW>(tiles, p.N, p.K, p.split, clusters, cost);
+    if (e != cudaSuccess) return e;
     const int reduce = p.split > 1 ? C::reduce_bytes(p.split) : 0;
     const int room = kSmemMax - 1024 - kTailBytes - C::kScale - reduce;
     p.stages = room / C::kStage < kMaxStages ? room / C::kStage : kMaxStages;
@@ -472,7 +488,6 @@ cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_
     if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), p.rows, p.K, C::kBox, BK, true) ||
         !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)p.E * p.N, p.K, TW, BK, true))
         return cudaErrorInvalidValue;
-    if (units < clusters) clusters = (int)units;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
     cfg.blockDim = dim3(kSwapThreads, 1, 1);
@@ -483,7 +498,7 @@ cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_
     attr[0].val.clusterDim = {(unsigned)p.split, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_fp8_swap_kernel<CW>, ma, mw, p, reduce);
+    e = cudaLaunchKernelEx(&cfg, gemm_fp8_swap_kernel<CW>, ma, mw, p, reduce);
     note_launch();
     return e;
 }
@@ -504,7 +519,8 @@ constexpr int kPairCols = PT * 4 / kPairDrain;   // accumulator columns of a dra
 constexpr int kPairLd = 64;                      // columns of one TMEM load
 constexpr int kPairRegsLow = 88, kPairRegsHigh = 208;
 static_assert(128 * kPairRegsLow + 32 * kPairDrain * kPairRegsHigh <= kPairThreads * (65536 / kPairThreads / 8 * 8), "above the launch's registers");
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 6;                   // even: block c is in stage c % 6 and buffer c % 2
+static_assert(kPairStages % 2 == 0, "a stage's buffer is its parity");
 constexpr int kPairStage = 2 * PTH * BK;         // 32 KB
 constexpr int kPairEpi = 1024;                   // of a drain warp: 32 rows x 32 bytes
 constexpr int kPairOffEpi = kPairStages * kPairStage;
@@ -529,8 +545,8 @@ struct PairArgs {
 
 // Units in bands of kBand token tiles, the weight tiles swept inside a band, so that the tiles that run
 // together share both operands in L2.
-__device__ __forceinline__ void pair_unit(int64_t u, int tiles, int NT, int& t, int& nt) {
-    const int64_t per = (int64_t)kBand * NT;
+__device__ __forceinline__ void pair_unit(uint32_t u, int tiles, int NT, int& t, int& nt) {
+    const uint32_t per = (uint32_t)kBand * NT;
     const int band = (int)(u / per), within = (int)(u - band * per);
     const int here = min(kBand, tiles - band * kBand);
     t = band * kBand + within % here;
@@ -616,9 +632,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (sbase - sraw);
     const uint32_t bar_full = sbase + kPairOffBar;             // used in the even CTA: both CTAs' loads
-    const uint32_t bar_empty = bar_full + 8 * kPairStages;     // both CTAs: the pair MMA's commit
-    const uint32_t bar_accfull = bar_empty + 8 * kPairStages;  // both CTAs: the pair MMA's commit
-    const uint32_t bar_accempty = bar_accfull + 16;            // used in the even CTA: both CTAs' drain warps
+    const uint32_t bar_done = bar_full + 8 * kPairStages;      // both CTAs: the pair MMA's commit; the stage may
+                                                               // be filled again, its partial sums be read
+    const uint32_t bar_accempty = bar_done + 8 * kPairStages;  // used in the even CTA: both CTAs' drain warps
     const uint32_t bar_scfull = bar_accempty + 16;
     const uint32_t bar_scempty = bar_scfull + 16;
     float* scales = reinterpret_cast<float*>(smem + kPairOffScale);   // [2 buffers][2 weight blocks][K block][row]
@@ -631,10 +647,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, 1);
+            mbar_init(bar_done + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(bar_accfull + 8 * b, 1);
             mbar_init(bar_accempty + 8 * b, 2 * kPairDrain);
             mbar_init(bar_scfull + 8 * b, 2);
             mbar_init(bar_scempty + 8 * b, kPairDrain);
@@ -655,8 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     const int NT = (p.N + PT - 1) / PT, KB = (p.K + BK - 1) / BK;
     const int tiles = cum[p.E];
-    const int64_t units = (int64_t)tiles * NT;
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const uint32_t units = (uint32_t)tiles * NT, first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPairRegsLow));
@@ -664,13 +678,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // ------------------------------------------------------------------------ TMA
             uint32_t s = 0, phase = 1;
             bool ok = true;
-            for (int64_t u = first; u < units && ok; u += step) {
+            for (uint32_t u = first; u < units && ok; u += step) {
                 int t, nt, e, row, n;
                 pair_unit(u, tiles, NT, t, nt);
                 groups.tile(t, e, row, n);
                 const int arow = row + rank * PTH, wrow = e * p.N + nt * PT + rank * PTH;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
+                    if (!mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
                         ok = false;
                         break;
                     }
@@ -682,27 +696,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (++s == kPairStages) { s = 0; phase ^= 1; }
                 }
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------------------------ MMA
             uint32_t s = 0, phase = 0, c = 0;
             bool ok = true;
-            for (int64_t u = first; u < units && ok; u += step) {
+            for (uint32_t u = first; u < units && ok; u += step) {
                 for (int kb = 0; kb < KB; ++kb, ++c) {
                     const uint32_t buf = c & 1;
-                    if (!mbar_wait_cluster(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrMmaAcc,
-                                           &g_fp8_error) ||
-                        !mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error)) {
+                    const bool got =
+                        mbar_wait_cluster(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrMmaAcc, &g_fp8_error) &&
+                        mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error);
+                    if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t a = smem_desc_sw128(sbase + s * kPairStage);
                     const uint64_t w = smem_desc_sw128(sbase + s * kPairStage + PTH * BK);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk)
-                        mma_fp8_pair(tmem_base + buf * PT, a + 2 * kk, w + 2 * kk, kIdescPair, kk ? 1u : 0u);
-                    mma_commit_pair(bar_empty + 8 * s, 3);
-                    mma_commit_pair(bar_accfull + 8 * buf, 3);
+                        for (int kk = 0; kk < BK / 32; ++kk)
+                            mma_fp8_pair(tmem_base + buf * PT, a + 2 * kk, w + 2 * kk, kIdescPair, kk ? 1u : 0u);
+                        mma_commit_pair(bar_done + 8 * s, 3);
+                    }
+                    __syncwarp();
                     if (++s == kPairStages) { s = 0; phase ^= 1; }
                 }
             }
@@ -715,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int b = lane & 7, r0 = (warp - 2) * 4 + lane / 8;
             uint32_t c = 0;
             bool ok = true;
-            for (int64_t u = first; u < units && ok; u += step) {
+            for (uint32_t u = first; u < units && ok; u += step) {
                 int t, nt, e, row, n;
                 pair_unit(u, tiles, NT, t, nt);
                 groups.tile(t, e, row, n);
@@ -759,9 +776,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + part;
         const uint32_t free_bar = mapa_shared(bar_accempty, 0);
         const float* own = scales + (part / BK) * kScaleHalf + quarter * 32 + lane;
-        uint32_t c = 0, sc = 0;
+        uint32_t s = 0, phase = 0, sc = 0;     // s: the block's stage; its buffer is s & 1
         bool ok = true;
-        for (int64_t u = first; u < units && ok; u += step) {
+        for (uint32_t u = first; u < units && ok; u += step) {
             int t, nt, e, row, n;
             pair_unit(u, tiles, NT, t, nt);
             groups.tile(t, e, row, n);
@@ -769,11 +786,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             uint64_t acc[kPairCols / 2];
 #pragma unroll
             for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
-            for (int kb = 0; kb < KB; ++kb, ++c) {
-                const uint32_t buf = c & 1, sbuf = sc & 1;
+            for (int kb = 0; kb < KB; ++kb) {
+                const uint32_t buf = s & 1, sbuf = sc & 1;
                 const int i = kb % kScaleBlocks;
                 if ((i == 0 && !mbar_wait(bar_scfull + 8 * sbuf, (sc >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) ||
-                    !mbar_wait(bar_accfull + 8 * buf, (c >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) {
+                    !mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrDrain, &g_fp8_error)) {
                     ok = false;
                     break;
                 }
@@ -794,6 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         acc[h * kPairLd / 2 + j] = fma2(pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f2,
                                                         acc[h * kPairLd / 2 + j]);
                 }
+                if (++s == kPairStages) { s = 0; phase ^= 1; }
                 if (i == kScaleBlocks - 1 || kb == KB - 1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_scempty + 8 * sbuf);
@@ -850,8 +868,7 @@ cudaError_t pair_clusters(int& clusters) {
     return cudaSuccess;
 }
 
-cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, const PairArgs& p, int64_t max_tiles,
-                        cudaStream_t stream) {
+cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, const PairArgs& p, int64_t tiles, cudaStream_t stream) {
     int clusters = 0;
     const cudaError_t e = pair_clusters(clusters);
     if (e != cudaSuccess) return e;
@@ -859,7 +876,7 @@ cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, const PairArgs& p,
     if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), p.rows, p.K, PTH, BK, true) ||
         !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)p.E * p.N, p.K, PTH, BK, true))
         return cudaErrorInvalidValue;
-    const int64_t units = max_tiles * ((p.N + PT - 1) / PT);
+    const int64_t units = tiles * ((p.N + PT - 1) / PT);
     if (units < clusters) clusters = (int)units;
     gemm_fp8_pair_kernel<<<2 * clusters, kPairThreads, kPairSmem, stream>>>(ma, mw, p);
     note_launch();
@@ -874,11 +891,27 @@ cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* q
     const int64_t per = (rows + E - 1) / E;   // rows of a group, on average
     const int64_t NT = (N + TW - 1) / TW;
     auto tiles = [&](int tn) { return offsets ? rows / tn + (E < rows ? E : rows) : (rows + tn - 1) / tn; };
-    if (tiles(16) * NT >= (1LL << 40)) return cudaErrorNotSupported;
-    if (per > 64) return launch_pair(qa, qw, PairArgs{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t}, tiles(PT), stream);
+    if (tiles(16) * NT >= (1LL << 31) - 1024) return cudaErrorNotSupported;   // the kernels count tiles in 32 bits
     const SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, 0, 1, y, t};
-    if (per <= 16) return launch_swap<8>(qa, qw, p, tiles(16), stream);
-    if (per <= 32) return launch_swap<16>(qa, qw, p, tiles(32), stream);
+    if (per > 64) {
+        // Pairs take 0.47 us a K block and round (of 256 x 256 tiles over 76 clusters), the other kernel 0.37 us of
+        // 64 x 128 tiles over 152 CTAs or fewer, larger clusters: a pair grid that leaves clusters idle
+        // loses (100x512x16384: 60 us against 17; 128x8192x8192: 35 against 29), a full one wins (256x8192x8192:
+        // 35 against 53; 8192 rows of 64 experts, 4096x4096: 270 against 400).
+        int pairs = 0, split = 1, clusters = 0;
+        double other = 0.0;
+        cudaError_t e = pair_clusters(pairs);
+        if (e == cudaSuccess) e = swap_plan<32>(tiles(64), N, K, split, clusters, other);
+        if (e != cudaSuccess) return e;
+        const int64_t rounds = (tiles(PT) * ((N + PT - 1) / PT) + pairs - 1) / pairs;
+        if (0.47 * (double)(rounds * ((K + BK - 1) / BK + 6)) > 0.37 * other)
+            return launch_swap<32>(qa, qw, p, tiles(64), stream);
+        return launch_pair(qa, qw, PairArgs{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t}, tiles(PT), stream);
+    }
+    // Groups of unequal size: a tile four times the average leaves few of them more than one.
+    const int64_t most = offsets ? 4 * per : per;
+    if (most <= 16) return launch_swap<8>(qa, qw, p, tiles(16), stream);
+    if (most <= 32) return launch_swap<16>(qa, qw, p, tiles(32), stream);
     return launch_swap<32>(qa, qw, p, tiles(64), stream);
 }
 
