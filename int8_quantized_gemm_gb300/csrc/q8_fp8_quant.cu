@@ -7,8 +7,6 @@
 // it, which rounds to 448). The maximum is taken over the bits of |x|, under which an infinity is
 // larger than every number and a NaN larger than an infinity: a block that holds one gets the scale
 // inf or NaN, and its codes times its scale are NaN, so that a broken value is not hidden.
-#include <cuda_fp8.h>
-
 #include "q8_fp8.h"
 #include "q8_internal.h"
 
@@ -26,83 +24,121 @@ __device__ __forceinline__ void scale_of(uint32_t amax_bits, float& s, float& r)
     r = __fdiv_rn(kFp8Max, a);
 }
 
+// Four values as e4m3 codes, the first in the lowest byte.
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// u * g / (1 + exp(-g)). The fast exponential and division are off by a few 2^-22 relative for
-// g > -20 (a thousandth of an e4m3 step); below, the value is under 5e-8 |u|. For 1 + exp(-g) above
-// 2^126 the division gives 0, its limit.
+// u * g / (1 + exp(-g)). The fast exponential and reciprocal are off by a few 2^-22 relative for
+// g > -20 (a thousandth of an e4m3 step); below, the value is under 5e-8 |u|. For exp(-g) above
+// 2^126 the reciprocal gives 0, its limit.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return __fmul_rn(__fdividef(g, 1.0f + __expf(-g)), u);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.0f + __expf(-g)));
+    return __fmul_rn(__fmul_rn(g, r), u);
 }
+
+enum Form : int { kDense = 0, kGated = 1, kSlots = 2 };
 
 // One block of 128 is held by 128 / n lanes, 16 bytes of input each; a warp works on kUnroll x
 // (32 n / 128) blocks at once, all loads first, so that enough bytes are in flight to fill the
-// memory pipe.
-template <class T, bool kGated>
+// memory pipe, and one lane of each block's does its two divisions. kDense, kGated: the blocks of all
+// rows in order; kSlots: `wpr` warps for each row, which copies its blocks to the row's slots.
+template <class T, int kForm>
 __global__ void __launch_bounds__(kThreads)
-    quantize_fp8_kernel(const T* __restrict__ x, uint32_t total, uint32_t KB, uint32_t K, int64_t ldx,
+    quantize_fp8_kernel(const T* __restrict__ x, uint32_t total, uint32_t KB, uint32_t K, int64_t ldx, uint32_t wpr,
                         const int32_t* __restrict__ slots, int top_k, int64_t rows_out, uint8_t* __restrict__ q,
                         float* __restrict__ s) {
     constexpr int n = Vec16<T>::n, kLanes = kFp8Block / n, kGroups = 32 / kLanes;
-    constexpr int kUnroll = kGated ? 2 : 4;
+    constexpr int kUnroll = kForm == kGated ? 2 : 4;
     const int lane = threadIdx.x & 31, sub = lane % kLanes;
     const uint32_t mask = kLanes == 32 ? 0xffffffffu : (0xffffu << (lane & 16));
-    const uint64_t warp = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    const uint64_t b0 = warp * (kUnroll * kGroups) + lane / kLanes;
-    Vec16<T> v[kUnroll], up[kGated ? kUnroll : 1];
-    uint32_t row[kUnroll], k0[kUnroll];
+    const uint32_t warp = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    uint32_t row, kb;    // of the first block
+    bool live;
+    if constexpr (kForm == kSlots) {
+        row = warp / wpr;
+        kb = (warp - row * wpr) * (kUnroll * kGroups) + lane / kLanes;
+        live = row * (uint64_t)KB < total;
+    } else {
+        const uint64_t b = (uint64_t)warp * (kUnroll * kGroups) + lane / kLanes;
+        live = b < total;
+        row = live ? (uint32_t)b / KB : 0;
+        kb = live ? (uint32_t)b - row * KB : 0;
+    }
+    Vec16<T> v[kUnroll], up[kForm == kGated ? kUnroll : 1];
+    uint32_t rows[kUnroll], k0[kUnroll];
     bool in[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        const uint64_t b = b0 + (uint64_t)i * kGroups;
-        row[i] = (uint32_t)b / KB;
-        k0[i] = ((uint32_t)b - row[i] * KB) * kFp8Block + sub * n;
-        in[i] = b < total && k0[i] < K;
+        rows[i] = row;
+        k0[i] = kb * kFp8Block + sub * n;
+        in[i] = live && kb < KB && k0[i] < K && (kForm == kSlots || (uint64_t)row * KB + kb < total);
         v[i].u = make_uint4(0, 0, 0, 0);
-        if (kGated) up[i].u = make_uint4(0, 0, 0, 0);
+        if (kForm == kGated) up[i].u = make_uint4(0, 0, 0, 0);
         if (in[i]) {
-            const T* p = x + (int64_t)row[i] * ldx + k0[i];
+            const T* p = x + (int64_t)row * ldx + k0[i];
             v[i].u = __ldcs(reinterpret_cast<const uint4*>(p));
-            if (kGated) up[i].u = __ldcs(reinterpret_cast<const uint4*>(p + K));
+            if (kForm == kGated) up[i].u = __ldcs(reinterpret_cast<const uint4*>(p + K));
         }
+        kb += kGroups;
+        if (kForm != kSlots)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)   // kGroups blocks on are at most kGroups rows on
+                if (kb >= KB) { kb -= KB; ++row; }
     }
+    float f[kUnroll][n];
+    uint32_t m[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        float f[n];
-        uint32_t m = 0;
+        m[i] = 0;
 #pragma unroll
         for (int j = 0; j < n; ++j) {
-            f[j] = to_float(v[i].t[j]);
-            if (kGated) f[j] = silu_mul(f[j], to_float(up[i].t[j]));
-            m = max(m, abs_bits(f[j]));
+            f[i][j] = to_float(v[i].t[j]);
+            if (kForm == kGated) f[i][j] = silu_mul(f[i][j], to_float(up[i].t[j]));
+            m[i] = max(m[i], abs_bits(f[i][j]));
         }
-        m = __reduce_max_sync(mask, m);
-        float sc, r;
-        scale_of(m, sc, r);
-        uint32_t c[n / 4];
+        m[i] = __reduce_max_sync(mask, m[i]);
+    }
+    // lane i of a block's lanes divides for block i
+    uint32_t own = m[0];
+#pragma unroll
+    for (int i = 1; i < kUnroll; ++i) own = (sub & (kUnroll - 1)) == i ? m[i] : own;
+    float own_s, own_r;
+    scale_of(own, own_s, own_r);
+    float sc[kUnroll];
+    uint32_t c[kUnroll][n / 4];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        sc[i] = __shfl_sync(0xffffffffu, own_s, (lane & ~(kLanes - 1)) + i);
+        const float r = __shfl_sync(0xffffffffu, own_r, (lane & ~(kLanes - 1)) + i);
 #pragma unroll
         for (int j = 0; j < n / 4; ++j)
-            c[j] = pack4(__fmul_rn(f[4 * j], r), __fmul_rn(f[4 * j + 1], r), __fmul_rn(f[4 * j + 2], r),
-                         __fmul_rn(f[4 * j + 3], r));
-        if (!in[i]) continue;
-        auto put = [&](int64_t d) {
-            uint32_t* o = reinterpret_cast<uint32_t*>(q + d * K + k0[i]);
-            if constexpr (n == 8) *reinterpret_cast<uint2*>(o) = make_uint2(c[0], c[n / 4 - 1]);
-            else *o = c[0];
-            if (sub == 0) s[d * KB + k0[i] / kFp8Block] = sc;
-        };
-        if (kGated || !slots) {
-            put(row[i]);
-        } else {
-            for (int j = 0; j < top_k; ++j) {
-                const int64_t d = __ldg(slots + (int64_t)row[i] * top_k + j);
-                if (d >= 0 && d < rows_out) put(d);
-            }
+            c[i][j] = pack4(__fmul_rn(f[i][4 * j], r), __fmul_rn(f[i][4 * j + 1], r), __fmul_rn(f[i][4 * j + 2], r),
+                            __fmul_rn(f[i][4 * j + 3], r));
+    }
+    auto put = [&](uint8_t* qd, float* sd, int i) {
+        if (!in[i]) return;
+        if constexpr (n == 8) *reinterpret_cast<uint2*>(qd + k0[i]) = make_uint2(c[i][0], c[i][n / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(qd + k0[i]) = c[i][0];
+        if (sub == 0) sd[k0[i] / kFp8Block] = sc[i];
+    };
+    if constexpr (kForm == kSlots) {
+        int to = -1;
+        if (live && lane < top_k) to = __ldg(slots + (int64_t)rows[0] * top_k + lane);
+        if (to >= rows_out) to = -1;
+        for (int j = 0; j < top_k; ++j) {
+            const int64_t d = __shfl_sync(0xffffffffu, to, j);
+            if (d < 0) continue;
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) put(q + d * K, s + d * KB, i);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) put(q + (int64_t)rows[i] * K, s + (int64_t)rows[i] * KB, i);
     }
 }
 
@@ -138,17 +174,27 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) s[((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = sc;
 }
 
-template <class T, bool kGated>
+template <class T, int kForm>
 cudaError_t launch(const void* x, int64_t M, int64_t K, int64_t ldx, const int32_t* slots, int top_k,
                    int64_t rows_out, uint8_t* q, float* s, cudaStream_t stream) {
     const int64_t KB = (K + kFp8Block - 1) / kFp8Block, total = M * KB;
     if (total >= (1LL << 31)) return cudaErrorNotSupported;
-    constexpr int kPerCta = (kThreads / 32) * (kGated ? 2 : 4) * (32 * Vec16<T>::n / kFp8Block);
-    const int64_t ctas = (total + kPerCta - 1) / kPerCta;
-    quantize_fp8_kernel<T, kGated><<<(unsigned)ctas, kThreads, 0, stream>>>(
-        static_cast<const T*>(x), (uint32_t)total, (uint32_t)KB, (uint32_t)K, ldx, slots, top_k, rows_out, q, s);
+    constexpr int kPerWarp = (kForm == kGated ? 2 : 4) * (32 * Vec16<T>::n / kFp8Block);
+    const int64_t wpr = (KB + kPerWarp - 1) / kPerWarp;
+    const int64_t warps = kForm == kSlots ? M * wpr : (total + kPerWarp - 1) / kPerWarp;
+    const int64_t ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    quantize_fp8_kernel<T, kForm><<<(unsigned)ctas, kThreads, 0, stream>>>(
+        static_cast<const T*>(x), (uint32_t)total, (uint32_t)KB, (uint32_t)K, ldx, (uint32_t)wpr, slots, top_k, rows_out,
+        q, s);
     note_launch();
     return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_plain(const void* x, int64_t M, int64_t K, int64_t ldx, const int32_t* slots, int top_k,
+                         int64_t rows_out, uint8_t* q, float* s, cudaStream_t stream) {
+    return slots ? launch<T, kSlots>(x, M, K, ldx, slots, top_k, rows_out, q, s, stream)
+                 : launch<T, kDense>(x, M, K, ldx, nullptr, 0, M, q, s, stream);
 }
 
 }  // namespace
@@ -157,18 +203,18 @@ cudaError_t launch_quantize_fp8(const void* x, q8_float_type t, int64_t M, int64
                                 const int32_t* slots, int top_k, int64_t rows_out, uint8_t* q, float* s,
                                 cudaStream_t stream) {
     switch (t) {
-        case Q8_F32: return launch<float, false>(x, M, K, ldx, slots, top_k, rows_out, q, s, stream);
-        case Q8_BF16: return launch<__nv_bfloat16, false>(x, M, K, ldx, slots, top_k, rows_out, q, s, stream);
-        default: return launch<__half, false>(x, M, K, ldx, slots, top_k, rows_out, q, s, stream);
+        case Q8_F32: return launch_plain<float>(x, M, K, ldx, slots, top_k, rows_out, q, s, stream);
+        case Q8_BF16: return launch_plain<__nv_bfloat16>(x, M, K, ldx, slots, top_k, rows_out, q, s, stream);
+        default: return launch_plain<__half>(x, M, K, ldx, slots, top_k, rows_out, q, s, stream);
     }
 }
 
 cudaError_t launch_swiglu_quantize_fp8(const void* h, q8_float_type t, int64_t M, int64_t I, int64_t ldh, uint8_t* q,
                                        float* s, cudaStream_t stream) {
     switch (t) {
-        case Q8_F32: return launch<float, true>(h, M, I, ldh, nullptr, 0, M, q, s, stream);
-        case Q8_BF16: return launch<__nv_bfloat16, true>(h, M, I, ldh, nullptr, 0, M, q, s, stream);
-        default: return launch<__half, true>(h, M, I, ldh, nullptr, 0, M, q, s, stream);
+        case Q8_F32: return launch<float, kGated>(h, M, I, ldh, nullptr, 0, M, q, s, stream);
+        case Q8_BF16: return launch<__nv_bfloat16, kGated>(h, M, I, ldh, nullptr, 0, M, q, s, stream);
+        default: return launch<__half, kGated>(h, M, I, ldh, nullptr, 0, M, q, s, stream);
     }
 }
 

@@ -58,7 +58,8 @@ struct Place {      // where a lane's experts are
 };
 
 // Group choice and top-k over a lane's keys. Returns the chosen expert of lane j in `mine` (-1: none)
-// for j < k. eps >= 0 asks for a report of decisions closer than eps + rel |key| (group sums: twice).
+// for j < k. With eps >= 0 (fp32 keys) it reports whether a decision was closer than eps + rel |key| (group sums:
+// twice that).
 template <int VPL, class K>
 __device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, float eps,
                                        float rel, int lane, int& mine) {
@@ -85,8 +86,8 @@ __device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const Rou
         for (int g = 0; g < a.n_group; ++g) {
             const K o = __shfl_sync(kFull, score, g * pl.lpg);
             rank += (o > score || (o == score && g < pl.group)) ? 1 : 0;
-            if (eps >= 0.0f && g != pl.group && pl.group < a.n_group)
-                close |= fabs((double)o - (double)score) <= 2.0 * (eps + rel * fabs((double)score));
+            if constexpr (sizeof(K) == 4)
+                close |= g != pl.group && pl.group < a.n_group && fabsf(o - score) <= 2.0f * (eps + rel * fabsf(score));
         }
         if (rank >= a.topk_group) {
 #pragma unroll
@@ -98,13 +99,13 @@ __device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const Rou
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         if (key[i] > best) { best = key[i]; at = i; }
-    const int rounds = a.k + (eps >= 0.0f ? 1 : 0);
+    const int rounds = a.k + (sizeof(K) == 4 && eps >= 0.0f ? 1 : 0);
     mine = -1;
     for (int j = 0; j < rounds; ++j) {
         int who;
         const K top = warp_best(best, who);
         if (!(top > masked_key<K>())) break;
-        if (eps >= 0.0f && j) close |= (float)last - (float)top <= eps + rel * fabsf((float)top);
+        if constexpr (sizeof(K) == 4) close |= j && last - top <= eps + rel * fabsf(top);
         last = top;
         if (j == a.k) break;
         const int e = __shfl_sync(kFull, pl.base + at, who);
@@ -188,13 +189,14 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
         inv_z = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
     }
     if (a.bias) {
-        // The fp32 key's error: the score's (sigmoid: exp, add and divide, under 2^-21; softmax: the
-        // rounding of l - m, exp, and a sum of up to 512 terms, under 2^-20 of the largest score)
-        // and the sum's, half a step of |key|. Two of them, and twice that for safety.
+        // The fp32 key's error. Sigmoid: exp(-l) by the fast exponential is off by |l| 2^-23 + 2^-22 relative, which
+        // moves p by p (1 - p) of that (|l| p (1 - p) < 0.23), and the add and the fast division by a
+        // few 2^-24: under 2^-21. Softmax: the same exponential, and a sum of up to 512 terms, under 2^-20 of
+        // the largest score. The sum with the bias: half a step of |key|. Two keys, and twice that for safety.
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (key[i] > -INFINITY)
-                key[i] = (a.softmax ? expf(key[i] - m) * inv_z : __fdiv_rn(1.0f, 1.0f + expf(-key[i]))) +
+                key[i] = (a.softmax ? __expf(key[i] - m) * inv_z : __fdividef(1.0f, 1.0f + __expf(-key[i]))) +
                          __ldg(a.bias + pl.base + i) + 0.0f;
         const float eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-19f;
         const bool close = choose<VPL, float>(key, pl, a, true, eps, 0x1p-22f, lane, mine);
@@ -241,10 +243,11 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
 // contiguous share of the entries, each warp with a contiguous share of its CTA's. Sweep 1 counts
 // the entries of each (warp, expert); prefix sums over warps, then CTAs (distributed shared memory),
 // then experts give each warp its first slot of each expert; sweep 2 hands the slots out in order.
-constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+// Bound by latencies: each lane loads eight entries at once.
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32, kPlanAhead = 8;
 
 __global__ void __launch_bounds__(kPlanThreads)
-    moe_plan_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int32_t* __restrict__ offsets,
+    moe_plan_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int bits, int32_t* __restrict__ offsets,
                     int32_t* __restrict__ slots) {
     extern __shared__ int32_t plan_smem[];
     int32_t* count = plan_smem;                       // [warps][E]
@@ -253,38 +256,57 @@ __global__ void __launch_bounds__(kPlanThreads)
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) count[i] = 0;
-    __syncthreads();
     // shares in whole warps of entries
     const int64_t share = (n + (int64_t)ctas * kPlanThreads - 1) / ((int64_t)ctas * kPlanThreads) * 32;
     const int64_t lo = min(n, ((int64_t)rank * kPlanWarps + warp) * share), hi = min(n, lo + share);
+    int e[kPlanAhead];
+    // eight entries of this lane from i0 on: the expert, or E for nobody's and past the end
+    auto load = [&](int64_t i0) {
+#pragma unroll
+        for (int j = 0; j < kPlanAhead; ++j) {
+            const int64_t i = i0 + 32 * j + lane;
+            e[j] = i < hi ? __ldg(idx + i) : E;
+        }
+#pragma unroll
+        for (int j = 0; j < kPlanAhead; ++j)
+            if (e[j] < 0 || e[j] > E) e[j] = E;
+    };
+    load(lo);
+    for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) count[i] = 0;
+    __syncthreads();
     int32_t* mine = count + warp * E;
-    for (int64_t i = lo; i < hi; i += 32) {
-        int e = i + lane < hi ? __ldg(idx + i + lane) : -1;
-        if (e < 0 || e >= E) e = E;
-        const unsigned same = __match_any_sync(kFull, e);
-        if (e < E && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kPlanAhead) {
+        if (i0 != lo) load(i0);
+#pragma unroll
+        for (int j = 0; j < kPlanAhead; ++j)
+            if (e[j] < E) atomicAdd(mine + e[j], 1);   // counts: the order does not matter
     }
+    if (hi - lo > 32 * kPlanAhead) load(lo);
     __syncthreads();
     if (threadIdx.x < E) {
-        int run = 0;
-#pragma unroll 8
+        int c[kPlanWarps], run = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) c[w] = count[w * E + threadIdx.x];
+#pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) {
-            const int c = count[w * E + threadIdx.x];
             count[w * E + threadIdx.x] = run;
-            run += c;
+            run += c[w];
         }
         total[threadIdx.x] = run;
     }
-    cluster.sync();
+    if (ctas > 1) cluster.sync();
     int before = 0, all = 0;
-    if (threadIdx.x < E)
-        for (int c = 0; c < ctas; ++c) {
-            const int v = cluster.map_shared_rank(total, c)[threadIdx.x];
-            all += v;
-            if (c < rank) before += v;
+    if (threadIdx.x < E) {
+        if (ctas == 1) {
+            all = total[threadIdx.x];
+        } else {
+            for (int c = 0; c < ctas; ++c) {
+                const int v = cluster.map_shared_rank(total, c)[threadIdx.x];
+                all += v;
+                if (c < rank) before += v;
+            }
         }
+    }
     int incl = all;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -292,10 +314,11 @@ __global__ void __launch_bounds__(kPlanThreads)
         if (lane >= d) incl += o;
     }
     if (lane == 31) scan[warp] = incl;
-    cluster.sync();   // also: nobody reads this CTA's totals any more
-    int start = incl - all;
-    for (int w = 0; w < warp; ++w) start += scan[w];
+    if (ctas > 1) cluster.sync();   // also: nobody reads this CTA's totals any more
+    else __syncthreads();
     if (threadIdx.x < E) {
+        int start = incl - all;
+        for (int w = 0; w < warp; ++w) start += scan[w];
         total[threadIdx.x] = start + before;
         if (rank == 0) {
             if (threadIdx.x == 0) offsets[0] = 0;
@@ -303,17 +326,26 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
     }
     __syncthreads();
-    for (int64_t i = lo; i < hi; i += 32) {
-        const bool live = i + lane < hi;
-        int e = live ? __ldg(idx + i + lane) : -1;
-        if (e < 0 || e >= E) e = E;
-        const unsigned same = __match_any_sync(kFull, e);
-        int slot = -1;
-        if (e < E) slot = total[e] + mine[e] + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-        if (e < E && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-        if (live) slots[i + lane] = slot;
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kPlanAhead) {
+        if (i0 != lo) load(i0);
+#pragma unroll
+        for (int j = 0; j < kPlanAhead; ++j) {
+            const int64_t i = i0 + 32 * j;
+            if (i >= hi) break;
+            // the lanes with the same expert, from one vote on each bit of it
+            unsigned same = kFull;
+            for (int b = 0; b < bits; ++b) {
+                const bool bit = (e[j] >> b) & 1;
+                const unsigned vote = __ballot_sync(kFull, bit);
+                same &= bit ? vote : ~vote;
+            }
+            int slot = -1;
+            if (e[j] < E) slot = total[e[j]] + mine[e[j]] + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (e[j] < E && lane == __ffs(same) - 1) mine[e[j]] += __popc(same);
+            __syncwarp();
+            if (i + lane < hi) slots[i + lane] = slot;
+        }
     }
 }
 
@@ -381,11 +413,15 @@ cudaError_t launch_moe_route(const RouteArgs& a, q8_float_type t, cudaStream_t s
 cudaError_t launch_moe_plan(const int32_t* idx, int64_t n, int E, int32_t* offsets, int32_t* slots,
                             cudaStream_t stream) {
     const size_t smem = (size_t)(kPlanWarps + 1) * E * 4;
-    cudaError_t e = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     // A CTA for each 2048 entries, up to the portable cluster of 8.
-    int ctas = 1;
+    int ctas = 1, bits = 1;
     while (ctas < 8 && (int64_t)ctas * 2048 < n) ctas *= 2;
+    while ((1 << bits) <= E) ++bits;   // of 0 .. E
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(kPlanThreads, 1, 1);
@@ -396,7 +432,7 @@ cudaError_t launch_moe_plan(const int32_t* idx, int64_t n, int E, int32_t* offse
     attr[0].val.clusterDim = {(unsigned)ctas, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, moe_plan_kernel, idx, n, E, offsets, slots);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_plan_kernel, idx, n, E, bits, offsets, slots);
     note_launch();
     return e;
 }
