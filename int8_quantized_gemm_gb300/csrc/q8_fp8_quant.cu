@@ -36,9 +36,17 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
 // g > -20 (a thousandth of an e4m3 step); below, the value is under 5e-8 |u|. For exp(-g) above
 // 2^126 the reciprocal gives 0, its limit.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.0f + __expf(-g)));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));   // exp(-g) = 2^(-g log2 e)
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.0f + e));
     return __fmul_rn(__fmul_rn(g, r), u);
+}
+
+// max(m, |a|, |b|), NaN if one is (its bits are then above those of inf).
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
 }
 
 enum Form : int { kDense = 0, kGated = 1, kSlots = 2 };
@@ -46,8 +54,9 @@ enum Form : int { kDense = 0, kGated = 1, kSlots = 2 };
 // One block of 128 is held by 128 / n lanes, 16 bytes of input each; a warp works on kUnroll x
 // (32 n / 128) blocks at once, all loads first, so that enough bytes are in flight to fill the
 // memory pipe, and one lane of each block's does its two divisions. kDense, kGated: the blocks of all
-// rows in order; kSlots: `wpr` warps for each row, which copies its blocks to the row's slots.
-template <class T, int kForm>
+// rows in order; kSlots: `wpr` warps for each row, which copies its blocks to the row's slots. kWhole:
+// K is a multiple of 128, so that block b's codes are at 128 b and its scale at b.
+template <class T, int kForm, bool kWhole>
 __global__ void __launch_bounds__(kThreads)
     quantize_fp8_kernel(const T* __restrict__ x, uint32_t total, uint32_t KB, uint32_t K, int64_t ldx, uint32_t wpr,
                         const int32_t* __restrict__ slots, int top_k, int64_t rows_out, uint8_t* __restrict__ q,
@@ -57,30 +66,41 @@ __global__ void __launch_bounds__(kThreads)
     const int lane = threadIdx.x & 31, sub = lane % kLanes;
     const uint32_t mask = kLanes == 32 ? 0xffffffffu : (0xffffu << (lane & 16));
     const uint32_t warp = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    uint32_t row, kb;    // of the first block
-    bool live;
+    // first block, and its row and place in the row
+    uint64_t b0;
+    uint32_t row, kb;
     if constexpr (kForm == kSlots) {
         row = warp / wpr;
         kb = (warp - row * wpr) * (kUnroll * kGroups) + lane / kLanes;
-        live = row * (uint64_t)KB < total;
+        b0 = (uint64_t)row * KB + kb;
     } else {
-        const uint64_t b = (uint64_t)warp * (kUnroll * kGroups) + lane / kLanes;
-        live = b < total;
-        row = live ? (uint32_t)b / KB : 0;
-        kb = live ? (uint32_t)b - row * KB : 0;
+        b0 = (uint64_t)warp * (kUnroll * kGroups) + lane / kLanes;
+        const uint32_t b = b0 < total ? (uint32_t)b0 : 0;
+        row = b / KB;
+        kb = b - row * KB;
     }
+    const uint32_t row0 = row;
     Vec16<T> v[kUnroll], up[kForm == kGated ? kUnroll : 1];
-    uint32_t rows[kUnroll], k0[kUnroll];
+    uint32_t rows[kUnroll], k0[kUnroll];   // not kWhole: where block i goes
     bool in[kUnroll];
+    const T* from = x + b0 * kFp8Block + sub * n;   // kWhole: block b of row r is at 128 b + r (ldx - K)
+    const int64_t skip = ldx - K;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        rows[i] = row;
-        k0[i] = kb * kFp8Block + sub * n;
-        in[i] = live && kb < KB && k0[i] < K && (kForm == kSlots || (uint64_t)row * KB + kb < total);
+        in[i] = b0 + i * kGroups < total;
+        if (kForm == kSlots) in[i] = in[i] && kb < KB;
+        const T* p;
+        if constexpr (kWhole) {
+            p = from + i * (kGroups * kFp8Block) + row * skip;
+        } else {
+            rows[i] = row;
+            k0[i] = kb * kFp8Block + sub * n;
+            in[i] = in[i] && k0[i] < K;
+            p = x + row * ldx + k0[i];
+        }
         v[i].u = make_uint4(0, 0, 0, 0);
         if (kForm == kGated) up[i].u = make_uint4(0, 0, 0, 0);
         if (in[i]) {
-            const T* p = x + (int64_t)row * ldx + k0[i];
             v[i].u = __ldcs(reinterpret_cast<const uint4*>(p));
             if (kForm == kGated) up[i].u = __ldcs(reinterpret_cast<const uint4*>(p + K));
         }
@@ -94,14 +114,15 @@ __global__ void __launch_bounds__(kThreads)
     uint32_t m[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        m[i] = 0;
+        float most = 0.0f;
 #pragma unroll
         for (int j = 0; j < n; ++j) {
             f[i][j] = to_float(v[i].t[j]);
             if (kForm == kGated) f[i][j] = silu_mul(f[i][j], to_float(up[i].t[j]));
-            m[i] = max(m[i], abs_bits(f[i][j]));
         }
-        m[i] = __reduce_max_sync(mask, m[i]);
+#pragma unroll
+        for (int j = 0; j < n; j += 2) most = max_abs(most, f[i][j], f[i][j + 1]);
+        m[i] = __reduce_max_sync(mask, __float_as_uint(most));
     }
     // lane i of a block's lanes divides for block i
     uint32_t own = m[0];
@@ -113,32 +134,41 @@ __global__ void __launch_bounds__(kThreads)
     uint32_t c[kUnroll][n / 4];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-        sc[i] = __shfl_sync(0xffffffffu, own_s, (lane & ~(kLanes - 1)) + i);
-        const float r = __shfl_sync(0xffffffffu, own_r, (lane & ~(kLanes - 1)) + i);
+        sc[i] = __shfl_sync(0xffffffffu, own_s, i, kLanes);
+        const float r = __shfl_sync(0xffffffffu, own_r, i, kLanes);
 #pragma unroll
         for (int j = 0; j < n / 4; ++j)
             c[i][j] = pack4(__fmul_rn(f[i][4 * j], r), __fmul_rn(f[i][4 * j + 1], r), __fmul_rn(f[i][4 * j + 2], r),
                             __fmul_rn(f[i][4 * j + 3], r));
     }
-    auto put = [&](uint8_t* qd, float* sd, int i) {
+    auto put = [&](uint8_t* to, float* scale, int i) {
         if (!in[i]) return;
-        if constexpr (n == 8) *reinterpret_cast<uint2*>(qd + k0[i]) = make_uint2(c[i][0], c[i][n / 4 - 1]);
-        else *reinterpret_cast<uint32_t*>(qd + k0[i]) = c[i][0];
-        if (sub == 0) sd[k0[i] / kFp8Block] = sc[i];
+        if constexpr (n == 8) *reinterpret_cast<uint2*>(to) = make_uint2(c[i][0], c[i][n / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(to) = c[i][0];
+        if (sub == 0) *scale = sc[i];
     };
     if constexpr (kForm == kSlots) {
         int to = -1;
-        if (live && lane < top_k) to = __ldg(slots + (int64_t)rows[0] * top_k + lane);
+        if (b0 - lane / kLanes < total && lane < top_k) to = __ldg(slots + (int64_t)row0 * top_k + lane);
         if (to >= rows_out) to = -1;
+        const uint32_t first = (uint32_t)(b0 - (uint64_t)row0 * KB);
         for (int j = 0; j < top_k; ++j) {
             const int64_t d = __shfl_sync(0xffffffffu, to, j);
             if (d < 0) continue;
+            uint8_t* qd = q + d * K + first * kFp8Block + sub * n;
+            float* sd = s + d * KB + first;
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) put(q + d * K, s + d * KB, i);
+            for (int i = 0; i < kUnroll; ++i) put(qd + i * (kGroups * kFp8Block), sd + i * kGroups, i);
         }
+    } else if constexpr (kWhole) {
+        uint8_t* qd = q + b0 * kFp8Block + sub * n;
+        float* sd = s + b0;
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) put(qd + i * (kGroups * kFp8Block), sd + i * kGroups, i);
     } else {
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) put(q + (int64_t)rows[i] * K, s + (int64_t)rows[i] * KB, i);
+        for (int i = 0; i < kUnroll; ++i)
+            put(q + (uint64_t)rows[i] * K + k0[i], s + (uint64_t)rows[i] * KB + k0[i] / kFp8Block, i);
     }
 }
 
@@ -183,9 +213,9 @@ cudaError_t launch(const void* x, int64_t M, int64_t K, int64_t ldx, const int32
     const int64_t wpr = (KB + kPerWarp - 1) / kPerWarp;
     const int64_t warps = kForm == kSlots ? M * wpr : (total + kPerWarp - 1) / kPerWarp;
     const int64_t ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    quantize_fp8_kernel<T, kForm><<<(unsigned)ctas, kThreads, 0, stream>>>(
-        static_cast<const T*>(x), (uint32_t)total, (uint32_t)KB, (uint32_t)K, ldx, (uint32_t)wpr, slots, top_k, rows_out,
-        q, s);
+    auto* kernel = K % kFp8Block == 0 ? quantize_fp8_kernel<T, kForm, true> : quantize_fp8_kernel<T, kForm, false>;
+    kernel<<<(unsigned)ctas, kThreads, 0, stream>>>(static_cast<const T*>(x), (uint32_t)total, (uint32_t)KB, (uint32_t)K,
+                                                    ldx, (uint32_t)wpr, slots, top_k, rows_out, q, s);
     note_launch();
     return cudaGetLastError();
 }

@@ -20,8 +20,9 @@ constexpr float kFloatMax = 3.402823466e38f;
 //
 // Without a bias the order is that of the logits (both scores grow with the logit), which is exact.
 // With a bias the order is that of score + bias in 64 bits: keys are computed in fp32, and where two
-// that decide something are nearer than the fp32 keys' error bound, the warp does the token again in
-// fp64 (about one token in a thousand on Gaussian logits). The scores of the weights stay fp32.
+// that decide something are nearer than the fp32 keys' error bound (about one token in a thousand on
+// Gaussian logits), the warp decides again in fp64: among the few experts about the border where only their
+// order is in doubt, over all of them where the choice of the groups is. The scores of the weights stay fp32.
 template <class K>
 __device__ __forceinline__ K masked_key();
 template <>
@@ -57,13 +58,18 @@ struct Place {      // where a lane's experts are
     int group, first, lpg;
 };
 
-// Group choice and top-k over a lane's keys. Returns the chosen expert of lane j in `mine` (-1: none)
-// for j < k. With eps >= 0 (fp32 keys) it reports whether a decision was closer than eps + rel |key| (group sums:
-// twice that).
+struct Doubt {
+    bool group = false, order = false;   // closer than the error bound: two groups, two of the best experts
+    bool kept = true;                    // this lane's group can be chosen from
+    float last = -INFINITY;              // the first key that was not chosen (fp32 keys)
+};
+
+// Group choice and top-k over a lane's keys. Returns the chosen expert of lane j in `mine` (-1: none) for
+// j < k. With eps >= 0 (fp32 keys) it reports decisions closer than eps + rel |key| (group sums: twice that).
 template <int VPL, class K>
-__device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, float eps,
-                                       float rel, int lane, int& mine) {
-    bool close = false;
+__device__ __forceinline__ Doubt choose(K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, float eps,
+                                        float rel, int lane, int& mine) {
+    Doubt doubt;
     if (a.n_group > 1) {
         K m1 = masked_key<K>(), m2 = masked_key<K>();
 #pragma unroll
@@ -87,9 +93,11 @@ __device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const Rou
             const K o = __shfl_sync(kFull, score, g * pl.lpg);
             rank += (o > score || (o == score && g < pl.group)) ? 1 : 0;
             if constexpr (sizeof(K) == 4)
-                close |= g != pl.group && pl.group < a.n_group && fabsf(o - score) <= 2.0f * (eps + rel * fabsf(score));
+                doubt.group |= eps >= 0.0f && g != pl.group && pl.group < a.n_group &&
+                               fabsf(o - score) <= 2.0f * (eps + rel * fabsf(score));
         }
-        if (rank >= a.topk_group) {
+        doubt.kept = rank < a.topk_group;
+        if (!doubt.kept) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) key[i] = none;
         }
@@ -105,9 +113,12 @@ __device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const Rou
         int who;
         const K top = warp_best(best, who);
         if (!(top > masked_key<K>())) break;
-        if constexpr (sizeof(K) == 4) close |= j && last - top <= eps + rel * fabsf(top);
+        if constexpr (sizeof(K) == 4) doubt.order |= j && last - top <= eps + rel * fabsf(top);
         last = top;
-        if (j == a.k) break;
+        if (j == a.k) {
+            doubt.last = (float)top;
+            break;
+        }
         const int e = __shfl_sync(kFull, pl.base + at, who);
         if (lane == j) mine = e;
         if (lane == who) {
@@ -121,7 +132,7 @@ __device__ __forceinline__ bool choose(K (&key)[VPL], const Place& pl, const Rou
             at = next;
         }
     }
-    return close;
+    return doubt;
 }
 
 template <class T>
@@ -130,28 +141,75 @@ __device__ __forceinline__ float load_logit(const T* p) {
     return l != l ? -INFINITY : fminf(l, kFloatMax) + 0.0f;   // + 0: -0 and 0 are one value
 }
 
+// A lane's logits (-inf: masked).
 template <int VPL, class T>
-__device__ __noinline__ int route_exact(const T* row, const Place pl, const RouteArgs a, int lane) {
-    double key[VPL];
-    float m = -INFINITY;
-#pragma unroll 1
-    for (int i = 0; i < pl.have; ++i) m = fmaxf(m, load_logit(row + pl.base + i));
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-    double z = 0.0;
+__device__ __forceinline__ void load_logits(const T* row, const Place& pl, float (&l)[VPL]) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const double l = i < pl.have ? (double)load_logit(row + pl.base + i) : -(double)INFINITY;
-        double p = 0.0;
-        if (l > -(double)INFINITY) p = a.softmax ? exp(l - (double)m) : 1.0 / (1.0 + exp(-l));
-        key[i] = l > -(double)INFINITY ? p : -1.0;
-        z += p;
-    }
-    for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
+    for (int i = 0; i < VPL; ++i) l[i] = i < pl.have ? load_logit(row + pl.base + i) : -INFINITY;
+}
+
+// The fp32 keys of a router with a bias, in place of the logits.
+template <int VPL>
+__device__ __forceinline__ void fast_keys(float (&key)[VPL], const Place& pl, const RouteArgs& a, float m, float inv_z) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        key[i] = key[i] < 0.0 ? masked_key<double>()
-                              : (a.softmax ? key[i] / z : key[i]) + (double)__ldg(a.bias + pl.base + i);
-    int mine;
+        if (key[i] > -INFINITY)
+            key[i] = (a.softmax ? __expf(key[i] - m) * inv_z : __fdividef(1.0f, 1.0f + __expf(-key[i]))) +
+                     __ldg(a.bias + pl.base + i) + 0.0f;
+}
+
+// The choice again, in fp64. Only the order is in doubt: the experts with an fp32 key of at least `from` in the
+// groups that were kept, one a lane, ranked against one another. Otherwise, or with more of them
+// than lanes: all experts.
+template <int VPL, class T>
+__device__ __noinline__ int route_exact(const T* row, const Place pl, const RouteArgs a, int lane, float m, float inv_z,
+                                        const Doubt doubt, float from, int16_t* list) {
+    double z = 1.0;
+    if (a.softmax) {
+        z = 0.0;
+        for (int i = 0; i < pl.have; ++i) {
+            const float l = load_logit(row + pl.base + i);
+            if (l > -INFINITY) z += exp((double)l - (double)m);
+        }
+        for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
+    }
+    auto exact_key = [&](int e) {
+        const double l = load_logit(row + e);
+        return (a.softmax ? exp(l - (double)m) / z : 1.0 / (1.0 + exp(-l))) + (double)__ldg(a.bias + e);
+    };
+    int count = 0, mine = -1;
+    if (!__any_sync(kFull, doubt.group)) {
+        float key[VPL];
+        load_logits<VPL>(row, pl, key);
+        fast_keys<VPL>(key, pl, a, m, inv_z);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool in = doubt.kept && key[i] > -INFINITY && key[i] >= from;
+            const unsigned vote = __ballot_sync(kFull, in);
+            const int at = count + __popc(vote & ((1u << lane) - 1));
+            if (in && at < 32) list[at] = (int16_t)(pl.base + i);
+            count += __popc(vote);
+        }
+        __syncwarp();
+        if (count <= 32) {
+            const int e = lane < count ? list[lane] : -1;
+            const double k = e >= 0 ? exact_key(e) : masked_key<double>();
+            int rank = 0;
+            for (int t = 0; t < count; ++t) {
+                const double o = __shfl_sync(kFull, k, t);
+                const int oe = __shfl_sync(kFull, e, t);
+                rank += o > k || (o == k && oe < e) ? 1 : 0;
+            }
+            __syncwarp();
+            if (e >= 0) list[rank] = (int16_t)e;
+            __syncwarp();
+            return lane < min(count, a.k) ? list[lane] : -1;
+        }
+    }
+    double key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? exact_key(pl.base + i) : masked_key<double>();
     choose<VPL, double>(key, pl, a, true, -1.0f, 0.0f, lane, mine);
     return mine;
 }
@@ -170,16 +228,14 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
     const int r = lane - pl.first;
     pl.base = pl.group * per + r * VPL;
     pl.have = pl.group < a.n_group ? max(0, min(VPL, per - r * VPL)) : 0;
+    __shared__ int16_t lists[4][32];
     float key[VPL];
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        key[i] = i < pl.have ? load_logit(row + pl.base + i) : -INFINITY;
-        m = fmaxf(m, key[i]);
-    }
+    load_logits<VPL>(row, pl, key);
     int mine, who;
-    float inv_z = 1.0f;
+    float m = -INFINITY, inv_z = 1.0f;
     if (a.softmax) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) m = fmaxf(m, key[i]);
         m = warp_best(m, who);
         float z = 0.0f;
 #pragma unroll
@@ -193,14 +249,14 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
         // moves p by p (1 - p) of that (|l| p (1 - p) < 0.23), and the add and the fast division by a
         // few 2^-24: under 2^-21. Softmax: the same exponential, and a sum of up to 512 terms, under 2^-20 of
         // the largest score. The sum with the bias: half a step of |key|. Two keys, and twice that for safety.
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (key[i] > -INFINITY)
-                key[i] = (a.softmax ? __expf(key[i] - m) * inv_z : __fdividef(1.0f, 1.0f + __expf(-key[i]))) +
-                         __ldg(a.bias + pl.base + i) + 0.0f;
-        const float eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-19f;
-        const bool close = choose<VPL, float>(key, pl, a, true, eps, 0x1p-22f, lane, mine);
-        if (__any_sync(kFull, close)) mine = route_exact<VPL, T>(row, pl, a, lane);
+        fast_keys<VPL>(key, pl, a, m, inv_z);
+        const float eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-19f, rel = 0x1p-22f;
+        const Doubt doubt = choose<VPL, float>(key, pl, a, true, eps, rel, lane, mine);
+        if (__any_sync(kFull, doubt.group || doubt.order)) {
+            // whatever can be among the chosen in 64 bits: within the bound of the first not chosen
+            const float from = doubt.last - 2.0f * (eps + rel * fabsf(doubt.last));
+            mine = route_exact<VPL, T>(row, pl, a, lane, m, inv_z, doubt, from, lists[threadIdx.x / 32]);
+        }
     } else {
         choose<VPL, float>(key, pl, a, false, -1.0f, 0.0f, lane, mine);
     }
