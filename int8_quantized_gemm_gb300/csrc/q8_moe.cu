@@ -18,41 +18,13 @@ constexpr float kFloatMax = 3.402823466e38f;
 // experts, lane r of them the VPL experts from r * VPL on: a lane never mixes groups, and lower
 // lanes hold lower experts, so that "the lowest lane that has the maximum" is the lowest index.
 //
-// Without a bias the order is that of the logits (both scores grow with the logit), which is exact.
-// With a bias the order is that of score + bias in 64 bits: keys are computed in fp32, and where two
-// that decide something are nearer than the fp32 keys' error bound (about one token in a thousand on
-// Gaussian logits), the warp decides again in fp64: among the few experts about the border where only their
-// order is in doubt, over all of them where the choice of the groups is. The scores of the weights stay fp32.
-template <class K>
-__device__ __forceinline__ K masked_key();
-template <>
-__device__ __forceinline__ float masked_key<float>() { return -INFINITY; }
-template <>
-__device__ __forceinline__ double masked_key<double>() { return -(double)INFINITY; }
-
-// Ascending order of the floats as unsigned values; -inf (masked) is 0x007fffff.
-__device__ __forceinline__ uint32_t ordered(float f) {
-    const uint32_t b = __float_as_uint(f);
-    return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
-// Warp maximum and the lowest lane that has it.
-__device__ __forceinline__ float warp_best(float v, int& who) {
-    const uint32_t u = ordered(v), m = __reduce_max_sync(kFull, u);
-    who = __ffs(__ballot_sync(kFull, u == m)) - 1;
-    return unordered(m);
-}
-__device__ __forceinline__ double warp_best(double v, int& who) {
-    double m = v;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, d));
-    who = __ffs(__ballot_sync(kFull, v == m)) - 1;
-    return m;
-}
-
+// A lane sorts its keys, as order-preserving integers whose lowest bits are replaced by their place in the
+// lane; the best of the warp is then one reduction a choice, and the lane that had it moves its list up.
+// Without a bias the order is that of the logits (both scores grow with the logit); with one it is that of
+// score + bias in 64 bits. Where two of the chosen (or the first not chosen) are nearer than the
+// fp32 keys' error bound and the replaced bits (about one token in a thousand on Gaussian logits with
+// a bias), the warp decides again in fp64: among the few experts about the border where only their
+// order is in doubt, over all of them where the choice of the groups is. The scores of the weights are fp32.
 struct Place {      // where a lane's experts are
     int base, have; // first expert, how many (<= VPL, may be 0)
     int group, first, lpg;
@@ -61,77 +33,113 @@ struct Place {      // where a lane's experts are
 struct Doubt {
     bool group = false, order = false;   // closer than the error bound: two groups, two of the best experts
     bool kept = true;                    // this lane's group can be chosen from
-    float last = -INFINITY;              // the first key that was not chosen (fp32 keys)
+    float last = -INFINITY;              // the first key that was not chosen
 };
 
-// Group choice and top-k over a lane's keys. Returns the chosen expert of lane j in `mine` (-1: none) for
-// j < k. With eps >= 0 (fp32 keys) it reports decisions closer than eps + rel |key| (group sums: twice that).
+// Ascending order of the floats as unsigned values; 0 is free for "masked".
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(kFull, ordered(v))); }
+
+template <class K>
+__device__ __forceinline__ K masked_key() { return -(K)INFINITY; }
+
+// A group's score: its best key, or (sum2) the sum of its two best. Returns whether this lane's group is among the
+// topk_group best; x, y: the scores of the last that is and the first that is not (where there is one).
 template <int VPL, class K>
-__device__ __forceinline__ Doubt choose(K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, float eps,
-                                        float rel, int lane, int& mine) {
+__device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, K& x,
+                                           K& y) {
+    const K none = masked_key<K>();
+    K m1 = none, m2 = none;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        m2 = fmax(m2, fmin(m1, key[i]));
+        m1 = fmax(m1, key[i]);
+    }
+    const K l1 = m1, l2 = m2;
+    const int lane = threadIdx.x & 31;
+    for (int d = 1; d < pl.lpg; ++d) {
+        int src = lane + d;
+        src = src >= pl.first + pl.lpg ? src - pl.lpg : src;
+        const K o1 = __shfl_sync(kFull, l1, src & 31), o2 = __shfl_sync(kFull, l2, src & 31);
+        m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+        m1 = fmax(m1, o1);
+    }
+    const K score = sum2 && m2 > none ? m1 + m2 : m1;
+    int rank = 0;
+    for (int g = 0; g < a.n_group; ++g) {
+        const K o = __shfl_sync(kFull, score, g * pl.lpg);
+        rank += (o > score || (o == score && g < pl.group)) ? 1 : 0;
+    }
+    if (a.topk_group < a.n_group) {
+        const bool counts = pl.group < a.n_group;
+        const unsigned in = __ballot_sync(kFull, counts && rank == a.topk_group - 1);
+        const unsigned out = __ballot_sync(kFull, counts && rank == a.topk_group);
+        x = __shfl_sync(kFull, score, __ffs(in) - 1);
+        y = __shfl_sync(kFull, score, __ffs(out) - 1);
+    }
+    return rank < a.topk_group;
+}
+
+// The chosen expert of lane j in `mine` (-1: none) for j < k, from a lane's keys (-inf: masked). check: report
+// decisions closer than eps + rel |key| (group sums: twice that).
+template <int VPL>
+__device__ __forceinline__ Doubt choose_fast(float (&key)[VPL], const Place& pl, const RouteArgs& a, bool check,
+                                             float eps, float rel, int lane, int& mine) {
     Doubt doubt;
     if (a.n_group > 1) {
-        K m1 = masked_key<K>(), m2 = masked_key<K>();
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const K v = key[i];
-            m2 = fmax(m2, fmin(m1, v));
-            m1 = fmax(m1, v);
-        }
-        const K l1 = m1, l2 = m2;
-        for (int d = 1; d < pl.lpg; ++d) {
-            int src = lane - pl.first + d;
-            src = pl.first + (src >= pl.lpg ? src - pl.lpg : src);
-            const K o1 = __shfl_sync(kFull, l1, src & 31), o2 = __shfl_sync(kFull, l2, src & 31);
-            m2 = fmax(fmin(m1, o1), fmax(m2, o2));
-            m1 = fmax(m1, o1);
-        }
-        const K none = masked_key<K>();
-        const K score = sum2 && m2 > none ? m1 + m2 : m1;
-        int rank = 0;
-        for (int g = 0; g < a.n_group; ++g) {
-            const K o = __shfl_sync(kFull, score, g * pl.lpg);
-            rank += (o > score || (o == score && g < pl.group)) ? 1 : 0;
-            if constexpr (sizeof(K) == 4)
-                doubt.group |= eps >= 0.0f && g != pl.group && pl.group < a.n_group &&
-                               fabsf(o - score) <= 2.0f * (eps + rel * fabsf(score));
-        }
-        doubt.kept = rank < a.topk_group;
-        if (!doubt.kept) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) key[i] = none;
-        }
+        float x = INFINITY, y = 0.0f;
+        doubt.kept = keep_group<VPL, float>(key, pl, a, a.bias != nullptr, x, y);
+        // without a bias the scores are logits, and exact
+        doubt.group = a.bias != nullptr && x - y <= 2.0f * (eps + rel * fabsf(x));
     }
-    K best = masked_key<K>(), last = K(0);
-    int at = 0;
+    uint32_t o[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) { best = key[i]; at = i; }
-    const int rounds = a.k + (sizeof(K) == 4 && eps >= 0.0f ? 1 : 0);
+        o[i] = doubt.kept && key[i] > -INFINITY ? (ordered(key[i]) & ~(uint32_t)(VPL - 1)) | (VPL - 1 - i) : 0;
+    // Batcher's odd-even merge sort, falling
+#pragma unroll
+    for (int p = 1; p < VPL; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < VPL; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if ((i + j) / (2 * p) == (i + j + k) / (2 * p) && i + j + k < VPL) {
+                        const uint32_t hi = max(o[i + j], o[i + j + k]), lo = min(o[i + j], o[i + j + k]);
+                        o[i + j] = hi;
+                        o[i + j + k] = lo;
+                    }
     mine = -1;
-    for (int j = 0; j < rounds; ++j) {
-        int who;
-        const K top = warp_best(best, who);
-        if (!(top > masked_key<K>())) break;
-        if constexpr (sizeof(K) == 4) doubt.order |= j && last - top <= eps + rel * fabsf(top);
+    float last = INFINITY;
+    for (int j = 0; j <= a.k; ++j) {
+        // equal keys: the lowest lane, and in it the lowest place
+        const uint32_t head = o[0] & ~(uint32_t)(VPL - 1), m = __reduce_max_sync(kFull, head);
+        if (m == 0) break;
+        const float top = unordered(m);
+        doubt.order |= last - top <= eps + rel * fabsf(top);
         last = top;
         if (j == a.k) {
-            doubt.last = (float)top;
+            doubt.last = top;
             break;
         }
-        const int e = __shfl_sync(kFull, pl.base + at, who);
+        const int who = __ffs(__ballot_sync(kFull, head == m)) - 1;
+        const int e = __shfl_sync(kFull, pl.base + (VPL - 1) - (int)(o[0] & (VPL - 1)), who);
         if (lane == j) mine = e;
         if (lane == who) {
-            best = masked_key<K>();
-            int next = 0;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (i == at) key[i] = masked_key<K>();
-                if (key[i] > best) { best = key[i]; next = i; }
-            }
-            at = next;
+            for (int i = 0; i + 1 < VPL; ++i) o[i] = o[i + 1];
+            o[VPL - 1] = 0;
         }
     }
+    doubt.order = doubt.order && check;
+    doubt.group = doubt.group && check;
     return doubt;
 }
 
@@ -148,14 +156,26 @@ __device__ __forceinline__ void load_logits(const T* row, const Place& pl, float
     for (int i = 0; i < VPL; ++i) l[i] = i < pl.have ? load_logit(row + pl.base + i) : -INFINITY;
 }
 
+__device__ __forceinline__ float fast_exp(float x) {   // 2^(x log2 e)
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(__fmul_rn(x, 1.4426950408889634f)));
+    return e;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // The fp32 keys of a router with a bias, in place of the logits.
 template <int VPL>
 __device__ __forceinline__ void fast_keys(float (&key)[VPL], const Place& pl, const RouteArgs& a, float m, float inv_z) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (key[i] > -INFINITY)
-            key[i] = (a.softmax ? __expf(key[i] - m) * inv_z : __fdividef(1.0f, 1.0f + __expf(-key[i]))) +
-                     __ldg(a.bias + pl.base + i) + 0.0f;
+    for (int i = 0; i < VPL; ++i) {
+        const float p = a.softmax ? fast_exp(key[i] - m) * inv_z : fast_rcp(1.0f + fast_exp(-key[i]));
+        const float b = i < pl.have ? __ldg(a.bias + pl.base + i) : 0.0f;
+        key[i] = key[i] > -INFINITY ? p + b + 0.0f : -INFINITY;
+    }
 }
 
 // The choice again, in fp64. Only the order is in doubt: the experts with an fp32 key of at least `from` in the
@@ -165,7 +185,7 @@ template <int VPL, class T>
 __device__ __noinline__ int route_exact(const T* row, const Place pl, const RouteArgs a, int lane, float m, float inv_z,
                                         const Doubt doubt, float from, int16_t* list) {
     double z = 1.0;
-    if (a.softmax) {
+    if (a.bias && a.softmax) {
         z = 0.0;
         for (int i = 0; i < pl.have; ++i) {
             const float l = load_logit(row + pl.base + i);
@@ -175,13 +195,14 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
     }
     auto exact_key = [&](int e) {
         const double l = load_logit(row + e);
+        if (!a.bias) return l;
         return (a.softmax ? exp(l - (double)m) / z : 1.0 / (1.0 + exp(-l))) + (double)__ldg(a.bias + e);
     };
-    int count = 0, mine = -1;
+    int count = 0;
     if (!__any_sync(kFull, doubt.group)) {
         float key[VPL];
         load_logits<VPL>(row, pl, key);
-        fast_keys<VPL>(key, pl, a, m, inv_z);
+        if (a.bias) fast_keys<VPL>(key, pl, a, m, inv_z);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const bool in = doubt.kept && key[i] > -INFINITY && key[i] >= from;
@@ -210,7 +231,27 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? exact_key(pl.base + i) : masked_key<double>();
-    choose<VPL, double>(key, pl, a, true, -1.0f, 0.0f, lane, mine);
+    double x, y;
+    if (a.n_group > 1 && !keep_group<VPL, double>(key, pl, a, a.bias != nullptr, x, y))
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = masked_key<double>();
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double best = masked_key<double>();
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > best) { best = key[i]; at = i; }
+        double top = best;
+        for (int d = 16; d; d >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, d));
+        if (!(top > masked_key<double>())) break;
+        const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
+        const int e = __shfl_sync(kFull, pl.base + at, who);
+        if (lane == j) mine = e;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (lane == who && i == at) key[i] = masked_key<double>();
+    }
     return mine;
 }
 
@@ -219,6 +260,7 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
     if (t >= a.T) return;
+    __shared__ int16_t lists[4][32];
     const T* row = static_cast<const T*>(a.logits) + t * a.ldl;
     const int per = a.E / a.n_group;
     Place pl;
@@ -228,15 +270,13 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
     const int r = lane - pl.first;
     pl.base = pl.group * per + r * VPL;
     pl.have = pl.group < a.n_group ? max(0, min(VPL, per - r * VPL)) : 0;
-    __shared__ int16_t lists[4][32];
     float key[VPL];
     load_logits<VPL>(row, pl, key);
-    int mine, who;
     float m = -INFINITY, inv_z = 1.0f;
     if (a.softmax) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) m = fmaxf(m, key[i]);
-        m = warp_best(m, who);
+        m = warp_max(m);
         float z = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) z += key[i] > -INFINITY ? expf(key[i] - m) : 0.0f;
@@ -244,21 +284,23 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
         for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
         inv_z = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
     }
+    // The fp32 key's error. Sigmoid: exp(-l) by the fast exponential is off by |l| 2^-23 + 2^-22 relative, which moves
+    // p by p (1 - p) of that (|l| p (1 - p) < 0.23), and the add and the fast reciprocal by a few
+    // 2^-24: under 2^-21. Softmax: the same exponential, and a sum of up to 512 terms, under 2^-20 of the
+    // largest score. The sum with the bias: half a step of |key|. Two keys, and twice that for safety. The
+    // replaced bits: VPL steps, 2 VPL 2^-23 of a key at most. Logits are exact; of 16-bit ones the replaced bits are 0.
+    float eps = 0.0f, rel = VPL * 0x1p-21f;
     if (a.bias) {
-        // The fp32 key's error. Sigmoid: exp(-l) by the fast exponential is off by |l| 2^-23 + 2^-22 relative, which
-        // moves p by p (1 - p) of that (|l| p (1 - p) < 0.23), and the add and the fast division by a
-        // few 2^-24: under 2^-21. Softmax: the same exponential, and a sum of up to 512 terms, under 2^-20 of
-        // the largest score. The sum with the bias: half a step of |key|. Two keys, and twice that for safety.
         fast_keys<VPL>(key, pl, a, m, inv_z);
-        const float eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-19f, rel = 0x1p-22f;
-        const Doubt doubt = choose<VPL, float>(key, pl, a, true, eps, rel, lane, mine);
-        if (__any_sync(kFull, doubt.group || doubt.order)) {
-            // whatever can be among the chosen in 64 bits: within the bound of the first not chosen
-            const float from = doubt.last - 2.0f * (eps + rel * fabsf(doubt.last));
-            mine = route_exact<VPL, T>(row, pl, a, lane, m, inv_z, doubt, from, lists[threadIdx.x / 32]);
-        }
-    } else {
-        choose<VPL, float>(key, pl, a, false, -1.0f, 0.0f, lane, mine);
+        eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-19f;
+        rel += 0x1p-22f;
+    }
+    int mine;
+    const Doubt doubt = choose_fast<VPL>(key, pl, a, a.bias || (sizeof(T) == 4 && VPL > 1), eps, rel, lane, mine);
+    if (__any_sync(kFull, doubt.group || doubt.order)) {
+        // whatever can be among the chosen in 64 bits: within the bound of the first not chosen
+        const float from = doubt.last - 2.0f * (eps + rel * fabsf(doubt.last));
+        mine = route_exact<VPL, T>(row, pl, a, lane, m, inv_z, doubt, from, lists[threadIdx.x / 32]);
     }
     float p = 0.0f;
     if (mine >= 0) {
@@ -340,13 +382,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (hi - lo > 32 * kPlanAhead) load(lo);
     __syncthreads();
     if (threadIdx.x < E) {
-        int c[kPlanWarps], run = 0;
+        int run = 0;
+        for (int w0 = 0; w0 < kPlanWarps; w0 += 16) {
+            int c[16];
 #pragma unroll
-        for (int w = 0; w < kPlanWarps; ++w) c[w] = count[w * E + threadIdx.x];
+            for (int w = 0; w < 16; ++w) c[w] = count[(w0 + w) * E + threadIdx.x];
 #pragma unroll
-        for (int w = 0; w < kPlanWarps; ++w) {
-            count[w * E + threadIdx.x] = run;
-            run += c[w];
+            for (int w = 0; w < 16; ++w) {
+                count[(w0 + w) * E + threadIdx.x] = run;
+                run += c[w];
+            }
         }
         total[threadIdx.x] = run;
     }
