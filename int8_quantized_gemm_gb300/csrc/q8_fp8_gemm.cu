@@ -112,10 +112,6 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
 }
 
-__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[8]) { tmem_ld8(a, v); }
-__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[16]) { tmem_ld16(a, v); }
-__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[32]) { tmem_ld32(a, v); }
-__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[64]) { tmem_ld64(a, v); }
 
 // Two values of a 16-bit type as one word.
 template <class T>

@@ -46,20 +46,31 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 }
 __device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(kFull, ordered(v))); }
 
-template <class K>
-__device__ __forceinline__ K masked_key() { return -(K)INFINITY; }
+// The same for doubles: fp64 comparisons run at a small fraction of the integer rate.
+__device__ __forceinline__ uint64_t ordered(double f) {
+    const uint64_t b = (uint64_t)__double_as_longlong(f);
+    return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double unordered(uint64_t u) {
+    return __longlong_as_double((int64_t)(u ^ ((u >> 63) ? 0x8000000000000000ull : ~0ull)));
+}
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+    const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(v >> 32));
+    return (uint64_t)hi << 32 | __reduce_max_sync(kFull, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+}
 
-// A group's score: its best key, or (sum2) the sum of its two best. Returns whether this lane's group is among the
-// topk_group best; x, y: the scores of the last that is and the first that is not (where there is one).
+// A group's score: its best key, or (sum2) the sum of its two best. Keys are floats (-inf: masked) or ordered
+// doubles (0: masked). Returns whether this lane's group is among the topk_group best; x, y: the scores
+// of the last that is and the first that is not (where there is one).
 template <int VPL, class K>
 __device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, K& x,
                                            K& y) {
-    const K none = masked_key<K>();
+    const K none = sizeof(K) == 4 ? (K)-INFINITY : (K)0;
     K m1 = none, m2 = none;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        m2 = fmax(m2, fmin(m1, key[i]));
-        m1 = fmax(m1, key[i]);
+        m2 = max(m2, min(m1, key[i]));
+        m1 = max(m1, key[i]);
     }
     const K l1 = m1, l2 = m2;
     const int lane = threadIdx.x & 31;
@@ -67,10 +78,14 @@ __device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl,
         int src = lane + d;
         src = src >= pl.first + pl.lpg ? src - pl.lpg : src;
         const K o1 = __shfl_sync(kFull, l1, src & 31), o2 = __shfl_sync(kFull, l2, src & 31);
-        m2 = fmax(fmin(m1, o1), fmax(m2, o2));
-        m1 = fmax(m1, o1);
+        m2 = max(min(m1, o1), max(m2, o2));
+        m1 = max(m1, o1);
     }
-    const K score = sum2 && m2 > none ? m1 + m2 : m1;
+    K score = m1;
+    if (sum2 && m2 > none) {
+        if constexpr (sizeof(K) == 4) score = m1 + m2;
+        else score = ordered(unordered(m1) + unordered(m2));
+    }
     int rank = 0;
     for (int g = 0; g < a.n_group; ++g) {
         const K o = __shfl_sync(kFull, score, g * pl.lpg);
@@ -214,10 +229,10 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
         __syncwarp();
         if (count <= 32) {
             const int e = lane < count ? list[lane] : -1;
-            const double k = e >= 0 ? exact_key(e) : masked_key<double>();
+            const uint64_t k = e >= 0 ? ordered(exact_key(e)) : 0;
             int rank = 0;
             for (int t = 0; t < count; ++t) {
-                const double o = __shfl_sync(kFull, k, t);
+                const uint64_t o = __shfl_sync(kFull, k, t);
                 const int oe = __shfl_sync(kFull, e, t);
                 rank += o > k || (o == k && oe < e) ? 1 : 0;
             }
@@ -227,30 +242,29 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
             return lane < min(count, a.k) ? list[lane] : -1;
         }
     }
-    double key[VPL];
+    uint64_t key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? exact_key(pl.base + i) : masked_key<double>();
-    double x, y;
-    if (a.n_group > 1 && !keep_group<VPL, double>(key, pl, a, a.bias != nullptr, x, y))
+        key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? ordered(exact_key(pl.base + i)) : 0;
+    uint64_t x, y;
+    if (a.n_group > 1 && !keep_group<VPL, uint64_t>(key, pl, a, a.bias != nullptr, x, y))
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = masked_key<double>();
+        for (int i = 0; i < VPL; ++i) key[i] = 0;
     int mine = -1;
     for (int j = 0; j < a.k; ++j) {
-        double best = masked_key<double>();
+        uint64_t best = 0;
         int at = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (key[i] > best) { best = key[i]; at = i; }
-        double top = best;
-        for (int d = 16; d; d >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, d));
-        if (!(top > masked_key<double>())) break;
+        const uint64_t top = warp_max(best);
+        if (top == 0) break;
         const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
         const int e = __shfl_sync(kFull, pl.base + at, who);
         if (lane == j) mine = e;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (lane == who && i == at) key[i] = masked_key<double>();
+            if (lane == who && i == at) key[i] = 0;
     }
     return mine;
 }
@@ -284,15 +298,16 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
         for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
         inv_z = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
     }
-    // The fp32 key's error. Sigmoid: exp(-l) by the fast exponential is off by |l| 2^-23 + 2^-22 relative, which moves
-    // p by p (1 - p) of that (|l| p (1 - p) < 0.23), and the add and the fast reciprocal by a few
-    // 2^-24: under 2^-21. Softmax: the same exponential, and a sum of up to 512 terms, under 2^-20 of the
-    // largest score. The sum with the bias: half a step of |key|. Two keys, and twice that for safety. The
-    // replaced bits: VPL steps, 2 VPL 2^-23 of a key at most. Logits are exact; of 16-bit ones the replaced bits are 0.
-    float eps = 0.0f, rel = VPL * 0x1p-21f;
+    // The fp32 keys' error. Sigmoid: the fast exponential is off by |l| 2^-24 + 2^-22 relative, which moves p by
+    // p (1 - p) of that, at most 1.23 2^-24 (|l| p (1 - p) < 0.23); the sum 1 + e and the fast reciprocal
+    // add 3 2^-24: under 2^-21.8, for two keys 2^-20.8. Softmax: the same exponential of a rounded l - m, and the
+    // sum of up to 512 terms, under 2^-18.8 of the largest score for two. The sum with the bias: half a step
+    // of |key| each. The replaced bits lower a key by less than VPL steps, so the difference of two by less than
+    // that. Logits are exact, and the replaced bits of 16-bit ones are 0 anyway.
+    float eps = 0.0f, rel = VPL * 0x1p-23f;
     if (a.bias) {
         fast_keys<VPL>(key, pl, a, m, inv_z);
-        eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-19f;
+        eps = a.softmax ? inv_z * 0x1p-18f : 0x1p-20f;
         rel += 0x1p-22f;
     }
     int mine;
