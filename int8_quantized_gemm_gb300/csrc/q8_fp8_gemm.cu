@@ -670,8 +670,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPairRegsLow));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------------------------------ TMA
+            const uint32_t full0 = mapa_shared(bar_full, 0);
             uint32_t s = 0, phase = 1;
             bool ok = true;
             for (uint32_t u = first; u < units && ok; u += step) {
@@ -680,15 +681,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 groups.tile(t, e, row, n);
                 const int arow = row + rank * PTH, wrow = e * p.N + nt * PT + rank * PTH;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error)) {
+                    const bool got = mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error);
+                    if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
                     const uint32_t dst = sbase + s * kPairStage;
-                    if (rank == 0) mbar_expect_tx(bar_full + 8 * s, 2 * kPairStage);
-                    const uint32_t bar = mapa_shared(bar_full + 8 * s, 0);
-                    tma_load_2d_pair(dst, &tmap_a, kb * BK, arow, bar);
-                    tma_load_2d_pair(dst + PTH * BK, &tmap_w, kb * BK, wrow, bar);
+                    if (elect_one()) {
+                        if (rank == 0) mbar_expect_tx(bar_full + 8 * s, 2 * kPairStage);
+                        tma_load_2d_pair(dst, &tmap_a, kb * BK, arow, full0 + 8 * s);
+                        tma_load_2d_pair(dst + PTH * BK, &tmap_w, kb * BK, wrow, full0 + 8 * s);
+                    }
+                    __syncwarp();
                     if (++s == kPairStages) { s = 0; phase ^= 1; }
                 }
             }
@@ -887,7 +891,8 @@ cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* q
     const int64_t per = (rows + E - 1) / E;   // rows of a group, on average
     const int64_t NT = (N + TW - 1) / TW;
     auto tiles = [&](int tn) { return offsets ? rows / tn + (E < rows ? E : rows) : (rows + tn - 1) / tn; };
-    if (tiles(16) * NT >= (1LL << 31) - 1024) return cudaErrorNotSupported;   // the kernels count tiles in 32 bits
+    // The kernels count tiles in 32 bits, whatever the offsets are (each group at most all rows).
+    if (tiles(16) * NT >= (1LL << 31) - 1024 || (rows / 16 + 1) * E >= (1LL << 31)) return cudaErrorNotSupported;
     const SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, 0, 1, y, t};
     if (per > 64) {
         // Pairs take 0.47 us a K block and round (of 256 x 256 tiles over 76 clusters), the other kernel 0.37 us of

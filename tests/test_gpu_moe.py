@@ -182,3 +182,15 @@ def test_layer_and_its_capture(q8, T):
         torch.cuda.synchronize()
         assert torch.equal(out, eager[i][0])
     assert q8.q8_device_error() == 0
+
+
+def test_example_runs_small():
+    """examples/moe_layer.py on a small layer with sizes that are no multiple of a tile."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_layer.py")
+    spec = importlib.util.spec_from_file_location("moe_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    worst = example.main(["--experts", "12", "--top-k", "3", "--hidden", "528", "--inter", "272", "--tokens", "1,7,130"])
+    assert worst < 2.0 ** -4
