@@ -500,34 +500,42 @@ cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_
 }
 
 // ------------------------------------------------------------------ tokens on the MMA's M side, CTA pairs
-// For many tokens: a cluster of two CTAs shares a tile of 256 token rows x 256 weight rows
+// For many tokens: a cluster of two CTAs shares a tile of 256 token rows x PN = 256 or 128 weight rows
 // (cta_group::2; each CTA loads half of both and holds its 128 token rows' accumulators). Per CTA:
-//   warp 0     TMA: tokens and weights [128 x 128] of each K block, completing on the even CTA's barrier
+//   warp 0     TMA: tokens [128 x 128] and weights [PN / 2 x 128] of each K block, completing on the even CTA's
+//              barrier
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
-//   warps 2, 3 scales: sa sw of the CTA's 128 token rows and the tile's two weight blocks, eight K blocks at a
-//              time (a sector of a row of sa), into shared memory
+//   warps 2, 3 scales: sa sw of the CTA's 128 token rows and the tile's one or two weight blocks, eight K blocks at
+//              a time (a sector of a row of sa), into shared memory
 //   warps 4-11 drain: a TMEM lane is a token row, so a thread's scale is one value a block, and the sum
-//              costs one multiply-add a value; two warps for each quarter of the lanes, 128 columns each
+//              costs one multiply-add a value; two warps for each quarter of the lanes, PN / 2 columns each
 constexpr int PT = 256, PTH = 128;
 constexpr int kPairDrain = 8;                    // drain warps
 constexpr int kPairThreads = 128 + 32 * kPairDrain;
-constexpr int kPairCols = PT * 4 / kPairDrain;   // accumulator columns of a drain warp
 constexpr int kPairLd = 64;                      // columns of one TMEM load
 constexpr int kPairRegsLow = 88, kPairRegsHigh = 208;
-static_assert(128 * kPairRegsLow + 32 * kPairDrain * kPairRegsHigh <= kPairThreads * (65536 / kPairThreads / 8 * 8), "above the launch's registers");
-constexpr int kPairStages = 6;                   // even: block c is in stage c % 6 and buffer c % 2
-static_assert(kPairStages % 2 == 0, "a stage's buffer is its parity");
-constexpr int kPairStage = 2 * PTH * BK;         // 32 KB
+static_assert(128 * kPairRegsLow + 32 * kPairDrain * kPairRegsHigh <= kPairThreads * (65536 / kPairThreads / 8 * 8),
+              "above the launch's registers");
 constexpr int kPairEpi = 1024;                   // of a drain warp: 32 rows x 32 bytes
-constexpr int kPairOffEpi = kPairStages * kPairStage;
 constexpr int kScaleBlocks = 8;                  // K blocks of one hand-over of scales
 constexpr int kScalePitch = PTH + 4;             // floats of a block's row of scales: no bank conflicts
 constexpr int kScaleHalf = kScaleBlocks * kScalePitch;
-constexpr int kPairOffScale = kPairOffEpi + kPairDrain * kPairEpi;
-constexpr int kPairOffBar = kPairOffScale + 2 * 2 * kScaleHalf * 4;
-constexpr int kPairSmem = 1024 + kPairOffBar + 8 * (2 * kPairStages + 8) + 32 + 4 * (kMaxExperts + 2);
-static_assert(kPairSmem <= kSmemMax, "above the shared memory of one CTA");
-constexpr uint32_t kIdescPair = idesc_f16(PT, PT);
+
+template <int PN>
+struct Pair8Cfg {
+    static constexpr int kHalf = PN / 2;                      // weight rows of a CTA; columns of a drain warp
+    static constexpr int kStage = (PTH + kHalf) * BK;         // 32 KB, 24 KB
+    static constexpr int kStages = PN == 256 ? 6 : 8;
+    static constexpr int kBufs = 512 / PN;                    // accumulator buffers: block c is in stage c % kStages
+    static_assert(kStages % kBufs == 0, "a stage has its buffer");   // and buffer c % kBufs
+    static constexpr int kOffEpi = kStages * kStage;
+    static constexpr int kOffScale = kOffEpi + kPairDrain * kPairEpi;
+    static constexpr int kOffBar = kOffScale + 2 * 2 * kScaleHalf * 4;
+    static constexpr int kBars = 2 * kStages + kBufs + 4;
+    static constexpr int kSmem = 1024 + kOffBar + 8 * kBars + 32 + 4 * (kMaxExperts + 2);
+    static_assert(kSmem <= kSmemMax, "above the shared memory of one CTA");
+    static constexpr uint32_t kIdesc = idesc_f16(PT, PN);
+};
 constexpr int kBand = 8;                         // token tiles that share a sweep over the weights
 
 struct PairArgs {
@@ -565,17 +573,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
-// A drain warp's 32 rows x kPairCols columns (one row a lane) to y, 32 bytes of each row at a time through
+// A drain warp's 32 rows x 2 NC columns (one row a lane) to y, 32 bytes of each row at a time through
 // shared memory (16-byte chunk j of row r at j ^ (r / 4 % 2): no bank conflicts either way), so that
 // two lanes write a whole sector. Rows of y that are not whole 16-byte chunks go value by value.
-template <class T>
-__device__ __forceinline__ void store_rows(T* y, int64_t row0, int live, int col0, int N,
-                                           const uint64_t (&acc)[kPairCols / 2],
+template <class T, int NC>
+__device__ __forceinline__ void store_rows(T* y, int64_t row0, int live, int col0, int N, const uint64_t (&acc)[NC],
                                            uint32_t buf, int lane) {
     constexpr int kCols = 32 / sizeof(T);         // columns of a step
     const bool vec = (N * sizeof(T)) % 16 == 0;
 #pragma unroll
-    for (int c = 0; c < kPairCols / kCols; ++c) {
+    for (int c = 0; c < 2 * NC / kCols; ++c) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -620,33 +627,36 @@ __device__ __forceinline__ void store_rows(T* y, int64_t row0, int live, int col
     }
 }
 
+template <int PN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
                          PairArgs p) {
+    using C = Pair8Cfg<PN>;
+    constexpr int kStages = C::kStages, kBufs = C::kBufs;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sraw = smem_u32(smem_raw);
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (sbase - sraw);
-    const uint32_t bar_full = sbase + kPairOffBar;             // used in the even CTA: both CTAs' loads
-    const uint32_t bar_done = bar_full + 8 * kPairStages;      // both CTAs: the pair MMA's commit; the stage may
+    const uint32_t bar_full = sbase + C::kOffBar;             // used in the even CTA: both CTAs' loads
+    const uint32_t bar_done = bar_full + 8 * kStages;      // both CTAs: the pair MMA's commit; the stage may
                                                                // be filled again, its partial sums be read
-    const uint32_t bar_accempty = bar_done + 8 * kPairStages;  // used in the even CTA: both CTAs' drain warps
-    const uint32_t bar_scfull = bar_accempty + 16;
+    const uint32_t bar_accempty = bar_done + 8 * kStages;  // used in the even CTA: both CTAs' drain warps
+    const uint32_t bar_scfull = bar_accempty + 8 * kBufs;
     const uint32_t bar_scempty = bar_scfull + 16;
-    float* scales = reinterpret_cast<float*>(smem + kPairOffScale);   // [2 buffers][2 weight blocks][K block][row]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBar + 8 * (2 * kPairStages + 8));
+    float* scales = reinterpret_cast<float*>(smem + C::kOffScale);   // [2 buffers][2 weight blocks][K block][row]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* cum = reinterpret_cast<int*>(tmem_slot + 2);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = (int)cluster_ctarank();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_done + 8 * s, 1);
         }
+        for (int b = 0; b < kBufs; ++b) mbar_init(bar_accempty + 8 * b, 2 * kPairDrain);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(bar_accempty + 8 * b, 2 * kPairDrain);
             mbar_init(bar_scfull + 8 * b, 2);
             mbar_init(bar_scempty + 8 * b, kPairDrain);
         }
@@ -664,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    const int NT = (p.N + PT - 1) / PT, KB = (p.K + BK - 1) / BK;
+    const int NT = (p.N + PN - 1) / PN, KB = (p.K + BK - 1) / BK;
     const int tiles = cum[p.E];
     const uint32_t units = (uint32_t)tiles * NT, first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
@@ -679,21 +689,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 int t, nt, e, row, n;
                 pair_unit(u, tiles, NT, t, nt);
                 groups.tile(t, e, row, n);
-                const int arow = row + rank * PTH, wrow = e * p.N + nt * PT + rank * PTH;
+                const int arow = row + rank * PTH, wrow = e * p.N + nt * PN + rank * C::kHalf;
                 for (int kb = 0; kb < KB; ++kb) {
                     const bool got = mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sbase + s * kPairStage;
+                    const uint32_t dst = sbase + s * C::kStage;
                     if (elect_one()) {
-                        if (rank == 0) mbar_expect_tx(bar_full + 8 * s, 2 * kPairStage);
+                        if (rank == 0) mbar_expect_tx(bar_full + 8 * s, 2 * C::kStage);
                         tma_load_2d_pair(dst, &tmap_a, kb * BK, arow, full0 + 8 * s);
                         tma_load_2d_pair(dst + PTH * BK, &tmap_w, kb * BK, wrow, full0 + 8 * s);
                     }
                     __syncwarp();
-                    if (++s == kPairStages) { s = 0; phase ^= 1; }
+                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
             }
         } else if (warp == 1 && rank == 0) {
@@ -702,25 +712,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             bool ok = true;
             for (uint32_t u = first; u < units && ok; u += step) {
                 for (int kb = 0; kb < KB; ++kb, ++c) {
-                    const uint32_t buf = c & 1;
+                    const uint32_t buf = c % kBufs;
                     const bool got =
-                        mbar_wait_cluster(bar_accempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrMmaAcc, &g_fp8_error) &&
+                        mbar_wait_cluster(bar_accempty + 8 * buf, ((c / kBufs) & 1) ^ 1, abort_flag, kErrMmaAcc, &g_fp8_error) &&
                         mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a = smem_desc_sw128(sbase + s * kPairStage);
-                    const uint64_t w = smem_desc_sw128(sbase + s * kPairStage + PTH * BK);
+                    const uint64_t a = smem_desc_sw128(sbase + s * C::kStage);
+                    const uint64_t w = smem_desc_sw128(sbase + s * C::kStage + PTH * BK);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < BK / 32; ++kk)
-                            mma_fp8_pair(tmem_base + buf * PT, a + 2 * kk, w + 2 * kk, kIdescPair, kk ? 1u : 0u);
+                            mma_fp8_pair(tmem_base + buf * PN, a + 2 * kk, w + 2 * kk, C::kIdesc, kk ? 1u : 0u);
                         mma_commit_pair(bar_done + 8 * s, 3);
                     }
                     __syncwarp();
-                    if (++s == kPairStages) { s = 0; phase ^= 1; }
+                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
             }
         } else if (warp >= 2) {
@@ -737,8 +747,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 pair_unit(u, tiles, NT, t, nt);
                 groups.tile(t, e, row, n);
                 row += rank * PTH + r0;
-                const float* w0 = p.sw + ((int64_t)e * NB + nt * 2) * KB;
-                const float* w1 = nt * 2 + 1 < NB ? w0 + KB : w0;
+                const float* w0 = p.sw + ((int64_t)e * NB + nt * (PN / BK)) * KB;
+                const float* w1 = PN > BK && nt * (PN / BK) + 1 < NB ? w0 + KB : w0;
                 const float* sa = p.sa + (int64_t)row * KB;
                 const int have = (p.rows - row + 7) / 8;   // rows of this lane that exist
                 float a[kRows], f0, f1;
@@ -761,7 +771,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) {
                         out[8 * i] = a[i] * f0;
-                        out[8 * i + kScaleHalf] = a[i] * f1;
+                        if (PN > BK) out[8 * i + kScaleHalf] = a[i] * f1;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_scfull + 8 * buf);
@@ -772,22 +782,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else {
         // ---------------------------------------------------------------------------- drain
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kPairRegsHigh));
-        const int quarter = warp & 3, part = ((warp - 4) >> 2) * kPairCols;   // its first column
+        const int quarter = warp & 3, part = ((warp - 4) >> 2) * C::kHalf;   // its first column
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + part;
         const uint32_t free_bar = mapa_shared(bar_accempty, 0);
         const float* own = scales + (part / BK) * kScaleHalf + quarter * 32 + lane;
-        uint32_t s = 0, phase = 0, sc = 0;     // s: the block's stage; its buffer is s & 1
+        uint32_t s = 0, phase = 0, sc = 0;     // s: the block's stage; its buffer is s % kBufs
         bool ok = true;
         for (uint32_t u = first; u < units && ok; u += step) {
             int t, nt, e, row, n;
             pair_unit(u, tiles, NT, t, nt);
             groups.tile(t, e, row, n);
             const int r0 = rank * PTH + quarter * 32;      // the warp's first row in the tile
-            uint64_t acc[kPairCols / 2];
+            uint64_t acc[C::kHalf / 2];
 #pragma unroll
-            for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
+            for (int j = 0; j < C::kHalf / 2; ++j) acc[j] = 0;
             for (int kb = 0; kb < KB; ++kb) {
-                const uint32_t buf = s & 1, sbuf = sc & 1;
+                const uint32_t buf = s % kBufs, sbuf = sc & 1;
                 const int i = kb % kScaleBlocks;
                 if ((i == 0 && !mbar_wait(bar_scfull + 8 * sbuf, (sc >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) ||
                     !mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrDrain, &g_fp8_error)) {
@@ -799,9 +809,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint64_t f2 = pack2(f, f);
                 uint32_t v[kPairLd];
 #pragma unroll
-                for (int h = 0; h < kPairCols / kPairLd; ++h) {
-                    tmem_load(tlane + buf * PT + h * kPairLd, v);
-                    if (h == kPairCols / kPairLd - 1) {   // everything is read: the buffer may be filled again
+                for (int h = 0; h < C::kHalf / kPairLd; ++h) {
+                    tmem_load(tlane + buf * PN + h * kPairLd, v);
+                    if (h == C::kHalf / kPairLd - 1) {   // everything is read: the buffer may be filled again
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_remote(free_bar + 8 * buf);
@@ -811,7 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         acc[h * kPairLd / 2 + j] = fma2(pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f2,
                                                         acc[h * kPairLd / 2 + j]);
                 }
-                if (++s == kPairStages) { s = 0; phase ^= 1; }
+                if (++s == kStages) { s = 0; phase ^= 1; }
                 if (i == kScaleBlocks - 1 || kb == KB - 1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_scempty + 8 * sbuf);
@@ -819,8 +829,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             }
             if (!ok) break;
-            const int live = min(32, n - r0), col0 = nt * PT + part;
-            const uint32_t buf = sbase + kPairOffEpi + (warp - 4) * kPairEpi;
+            const int live = min(32, n - r0), col0 = nt * PN + part;
+            const uint32_t buf = sbase + C::kOffEpi + (warp - 4) * kPairEpi;
             if (live > 0 && col0 < p.N) {
                 if (p.type == Q8_BF16)
                     store_rows(static_cast<__nv_bfloat16*>(p.y), row + r0, live, col0, p.N, acc, buf, lane);
@@ -844,7 +854,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // Once per device: the shared-memory limit, and the clusters of two that run at once.
+template <int PN>
 cudaError_t pair_clusters(int& clusters) {
+    using C = Pair8Cfg<PN>;
     static int cached[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -853,32 +865,34 @@ cudaError_t pair_clusters(int& clusters) {
         clusters = cached[dev];
         return cudaSuccess;
     }
-    e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    e = cudaFuncSetAttribute(gemm_fp8_pair_kernel<PN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     clusters = device_sm_count() / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.dynamicSmemBytes = C::kSmem;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, gemm_fp8_pair_kernel, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, gemm_fp8_pair_kernel<PN>, &cfg);
     if (e != cudaSuccess) return e;
     if (n > 0 && n < clusters) clusters = n;
     if (dev < 64) cached[dev] = clusters;
     return cudaSuccess;
 }
 
+template <int PN>
 cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, const PairArgs& p, int64_t tiles, cudaStream_t stream) {
+    using C = Pair8Cfg<PN>;
     int clusters = 0;
-    const cudaError_t e = pair_clusters(clusters);
+    const cudaError_t e = pair_clusters<PN>(clusters);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mw;
     if (!make_tma_map_i8(&ma, reinterpret_cast<const int8_t*>(qa), p.rows, p.K, PTH, BK, true) ||
-        !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)p.E * p.N, p.K, PTH, BK, true))
+        !make_tma_map_i8(&mw, reinterpret_cast<const int8_t*>(qw), (int64_t)p.E * p.N, p.K, C::kHalf, BK, true))
         return cudaErrorInvalidValue;
-    const int64_t units = tiles * ((p.N + PT - 1) / PT);
+    const int64_t units = tiles * ((p.N + PN - 1) / PN);
     if (units < clusters) clusters = (int)units;
-    gemm_fp8_pair_kernel<<<2 * clusters, kPairThreads, kPairSmem, stream>>>(ma, mw, p);
+    gemm_fp8_pair_kernel<PN><<<2 * clusters, kPairThreads, C::kSmem, stream>>>(ma, mw, p);
     note_launch();
     return cudaGetLastError();
 }
@@ -895,19 +909,24 @@ cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* q
     if (tiles(16) * NT >= (1LL << 31) - 1024 || (rows / 16 + 1) * E >= (1LL << 31)) return cudaErrorNotSupported;
     const SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, 0, 1, y, t};
     if (per > 64) {
-        // Pairs take 0.47 us a K block and round (of 256 x 256 tiles over 76 clusters), the other kernel 0.37 us of
-        // 64 x 128 tiles over 152 CTAs or fewer, larger clusters: a pair grid that leaves clusters idle
-        // loses (100x512x16384: 60 us against 17; 128x8192x8192: 35 against 29), a full one wins (256x8192x8192:
-        // 35 against 53; 8192 rows of 64 experts, 4096x4096: 270 against 400).
+        // What a round of tiles costs a K block: 0.47 us for 256 x 256 tiles over 76 pairs, 0.30 us for 256 x 128, 0.37 us
+        // for 64 x 128 tiles of the other kernel over 152 CTAs (or fewer, larger clusters); and about six
+        // blocks a tile. Measured, wide pairs / narrow pairs / other kernel, us: 100x512x16384 62 / 41 / 15; 128x8192x8192
+        // 34 / 25 / 27; 517x2056x4112 25 / 17 / 27; 512x8192x8192 38 / 44 / 91; 2048x4096x4096 38 / 51 / 77; 8192
+        // rows of 64 experts, 4096x4096, 268 / 311 / 369. The estimate picks the fastest in each.
         int pairs = 0, split = 1, clusters = 0;
         double other = 0.0;
-        cudaError_t e = pair_clusters(pairs);
+        cudaError_t e = pair_clusters<256>(pairs);
         if (e == cudaSuccess) e = swap_plan<32>(tiles(64), N, K, split, clusters, other);
         if (e != cudaSuccess) return e;
-        const int64_t rounds = (tiles(PT) * ((N + PT - 1) / PT) + pairs - 1) / pairs;
-        if (0.47 * (double)(rounds * ((K + BK - 1) / BK + 6)) > 0.37 * other)
-            return launch_swap<32>(qa, qw, p, tiles(64), stream);
-        return launch_pair(qa, qw, PairArgs{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t}, tiles(PT), stream);
+        auto rounds = [&](int pn) {
+            return (double)(((tiles(PT) * ((N + pn - 1) / pn) + pairs - 1) / pairs) * ((K + BK - 1) / BK + 6));
+        };
+        const double wide = 0.47 * rounds(256), narrow = 0.30 * rounds(128);
+        const PairArgs pa{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t};
+        if (0.37 * other < wide && 0.37 * other < narrow) return launch_swap<32>(qa, qw, p, tiles(64), stream);
+        if (narrow < wide) return launch_pair<128>(qa, qw, pa, tiles(PT), stream);
+        return launch_pair<256>(qa, qw, pa, tiles(PT), stream);
     }
     // Groups of unequal size: a tile four times the average leaves few of them more than one.
     const int64_t most = offsets ? 4 * per : per;

@@ -168,7 +168,7 @@ def check(y, qa, sa, qw, sw, dtype):
 
 SHAPES = [(1, 128, 128), (1, 8, 16), (1, 1, 1040), (2, 130, 144), (15, 257, 512), (16, 2056, 4112), (17, 128, 2048),
           (33, 640, 1040), (64, 256, 4096), (65, 136, 256), (128, 384, 640), (129, 264, 400), (256, 256, 1024),
-          (300, 520, 528), (517, 1032, 784), (1000, 96, 2064)]
+          (300, 520, 528), (517, 1032, 784), (1000, 96, 2064), (2500, 1500, 400), (400, 1500, 2064)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -254,6 +254,19 @@ def test_grouped(q8, i, N, K):
         at = slice(int(offsets[e]), int(offsets[e + 1]))
         if counts[e]:
             check(y[at], qa[at], sa[at], qw[e], sw[e], dtype)
+
+
+@pytest.mark.parametrize("counts,N,K", [([900, 0, 1500], 1500, 272), ([300, 260, 0, 411], 900, 1040)])
+def test_grouped_many_rows(q8, counts, N, K):
+    """Whole tiles and ragged last ones of the kernels for many rows, in a group's middle and end."""
+    rows, E = sum(counts), len(counts)
+    qa, sa, qw, sw = operands(rows, N, K, seed=N, E=E)
+    offsets = torch.tensor([sum(counts[:e]) for e in range(E + 1)], dtype=torch.int32)
+    y = q8.q8_gemm_fp8_grouped(qa.cuda(), sa.cuda(), qw.cuda(), sw.cuda(), offsets.cuda(), out_dtype=torch.float16)
+    for e in range(E):
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        if counts[e]:
+            check(y[at], qa[at], sa[at], qw[e], sw[e], torch.float16)
 
 
 def test_grouped_offsets_are_cut_to_the_rows(q8):
