@@ -25,6 +25,9 @@ constexpr float kFloatMax = 3.402823466e38f;
 // fp32 keys' error bound and the replaced bits (about one token in a thousand on Gaussian logits with
 // a bias), the warp decides again in fp64: among the few experts about the border where only their
 // order is in doubt, over all of them where the choice of the groups is. The scores of the weights are fp32.
+// Bound by issue slots (about 1000 instructions a token at 256 experts): 8192 tokens take 10 us without a bias, 17 to
+// 21 us with one and groups, of which the last few tokens' fp64 (64 clocks an instruction) are 7 to 10; one
+// token 3.9 us, mostly launch.
 struct Place {      // where a lane's experts are
     int base, have; // first expert, how many (<= VPL, may be 0)
     int group, first, lpg;
@@ -356,7 +359,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
 // contiguous share of the entries, each warp with a contiguous share of its CTA's. Sweep 1 counts
 // the entries of each (warp, expert); prefix sums over warps, then CTAs (distributed shared memory),
 // then experts give each warp its first slot of each expert; sweep 2 hands the slots out in order.
-// Bound by latencies: each lane loads eight entries at once.
+// Bound by latencies (each lane loads eight entries at once): 65536 entries of 256 experts 9.6 us, 8 entries 3.7 us.
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32, kPlanAhead = 8;
 
 __global__ void __launch_bounds__(kPlanThreads)
@@ -467,7 +470,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // ----------------------------------------------------------------------------------- combine
 // 16 bytes of a token's output for each thread, its k rows' loads in flight four at a time; the sum in
-// fp32 in the order of the choices. Reads k rows and writes one for each token: memory bound.
+// fp32 in the order of the choices. Reads k rows and writes one for each token: bound by memory, 8192 x 4096 with 8
+// rows each 82 us on the device, 92 us back to back (6.6 TB/s, 0.97 of the measured copy).
 template <class T>
 __global__ void __launch_bounds__(256)
     moe_combine_kernel(const T* __restrict__ h, int64_t rows, uint32_t chunks, const int32_t* __restrict__ slots,
