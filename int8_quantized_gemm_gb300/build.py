@@ -43,6 +43,7 @@ def _stale() -> bool:
     deps = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, "q8_internal.h"),
                                                       os.path.join(CSRC, "q8_tc_ptx.cuh"),
                                                       os.path.join(CSRC, "q8_fp8.h"),
+                                                      os.path.join(CSRC, "q8_fp8_ptx.cuh"),
                                                       os.path.join(ROOT, "include", "q8.h"),
                                                       os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)

@@ -11,7 +11,7 @@
 
 #include "q8_fp8.h"
 #include "q8_internal.h"
-#include "q8_tc_ptx.cuh"
+#include "q8_fp8_ptx.cuh"
 
 namespace q8 {
 namespace {
