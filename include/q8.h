@@ -640,7 +640,7 @@ q8_status q8_gemm_fp8_grouped(const uint8_t* qa, const float* sa, const uint8_t*
  *  - weights = p of the chosen, divided by their sum if renorm (0 where that is 0), times scale.
  *  - An expert whose logit is -inf or NaN is masked: its score is 0 and it is never chosen. A token
  *    that has too few experts left gets idx -1 and weight 0 in the places that remain. A logit of +inf
- *    counts as the largest fp32 value.
+ *    counts as the largest fp32 value. A bias of -inf or NaN masks its expert for every token.
  *
  * logits  : [T, E] of `type`, rows ldl elements apart. bias : fp32 [E] or NULL.
  * idx     : int32 [T, top_k], weights : fp32 [T, top_k], written.

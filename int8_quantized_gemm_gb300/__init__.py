@@ -679,8 +679,16 @@ def _handle(device: int, stream) -> int:
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _new(shape, dtype, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _out(t, shape, dtype, like: torch.Tensor, device: int, stream, name: str):
+    """A result and its address: the caller's tensor, or a new one, allocated on the stream that writes it."""
+    if t is not None:
+        return t, _dense(t, dtype, shape, device, name)
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=like.device)
+    return t, t.data_ptr()
 
 
 def q8_quantize_fp8(x: torch.Tensor, slots=None, rows: int | None = None, q=None, s=None, stream=None):
@@ -699,11 +707,9 @@ def q8_quantize_fp8(x: torch.Tensor, slots=None, rows: int | None = None, q=None
         raise ValueError("rows goes with slots")
     else:
         rows = M
-    KB = _cdiv(K, FP8_BLOCK)
-    q = _new((rows, K), _FP8, x) if q is None else q
-    s = _new((rows, KB), torch.float32, x) if s is None else s
-    _check(load().q8_quantize_fp8(x.data_ptr(), kind, M, K, ldx, to, top_k, rows, _dense(q, _FP8, (rows, K), dev, "q"),
-                                  _dense(s, torch.float32, (rows, KB), dev, "s"), _handle(dev, stream)),
+    q, pq = _out(q, (rows, K), _FP8, x, dev, stream, "q")
+    s, ps = _out(s, (rows, -(-K // FP8_BLOCK)), torch.float32, x, dev, stream, "s")
+    _check(load().q8_quantize_fp8(x.data_ptr(), kind, M, K, ldx, to, top_k, rows, pq, ps, _handle(dev, stream)),
            "q8_quantize_fp8")
     return q, s
 
@@ -713,11 +719,10 @@ def q8_swiglu_quantize_fp8(h: torch.Tensor, q=None, s=None, stream=None):
     M, cols, ldh, kind = _float_rows(h, "h")
     if cols % 2:
         raise ValueError("h must have an even number of columns")
-    I, KB, dev = cols // 2, _cdiv(cols // 2, FP8_BLOCK), h.get_device()
-    q = _new((M, I), _FP8, h) if q is None else q
-    s = _new((M, KB), torch.float32, h) if s is None else s
-    _check(load().q8_swiglu_quantize_fp8(h.data_ptr(), kind, M, I, ldh, _dense(q, _FP8, (M, I), dev, "q"),
-                                         _dense(s, torch.float32, (M, KB), dev, "s"), _handle(dev, stream)),
+    I, dev = cols // 2, h.get_device()
+    q, pq = _out(q, (M, I), _FP8, h, dev, stream, "q")
+    s, ps = _out(s, (M, -(-I // FP8_BLOCK)), torch.float32, h, dev, stream, "s")
+    _check(load().q8_swiglu_quantize_fp8(h.data_ptr(), kind, M, I, ldh, pq, ps, _handle(dev, stream)),
            "q8_swiglu_quantize_fp8")
     return q, s
 
@@ -733,16 +738,15 @@ def q8_quantize_weight_fp8(w: torch.Tensor, qw=None, sw=None, stream=None):
     E = w.shape[0] if w.dim() == 3 else 1
     dev = w.get_device()
     scales = (*w.shape[:-2], _cdiv(N, FP8_BLOCK), _cdiv(K, FP8_BLOCK))
-    qw = _new(w.shape, _FP8, w) if qw is None else qw
-    sw = _new(scales, torch.float32, w) if sw is None else sw
-    _check(load().q8_quantize_weight_fp8(w.data_ptr(), FLOAT_TYPES[w.dtype], E, N, K, _dense(qw, _FP8, w.shape, dev, "qw"),
-                                         _dense(sw, torch.float32, scales, dev, "sw"), _handle(dev, stream)),
+    qw, pq = _out(qw, tuple(w.shape), _FP8, w, dev, stream, "qw")
+    sw, ps = _out(sw, scales, torch.float32, w, dev, stream, "sw")
+    _check(load().q8_quantize_weight_fp8(w.data_ptr(), FLOAT_TYPES[w.dtype], E, N, K, pq, ps, _handle(dev, stream)),
            "q8_quantize_weight_fp8")
     return qw, sw
 
 
-def _fp8_operands(qa, sa, qw, sw, ndim, out_dtype, out):
-    """Addresses and sizes of a product: (device, M, N, K, pointers of qa, sa, qw, sw and out, type, out)."""
+def _fp8_operands(qa, sa, qw, sw, ndim, out_dtype, out, stream):
+    """Addresses and sizes of a product: (device, M, N, K, addresses of qa, sa, qw, sw and out, type, out)."""
     _need(qa, _FP8, "qa", 2)
     _need(qw, _FP8, "qw", ndim)
     M, K = qa.shape
@@ -753,16 +757,18 @@ def _fp8_operands(qa, sa, qw, sw, ndim, out_dtype, out):
     kind = FLOAT_TYPES.get(out_dtype)
     if kind is None:
         raise TypeError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
-    dev, KB = qa.get_device(), _cdiv(K, FP8_BLOCK)
-    out = _new((M, N), out_dtype, qa) if out is None else out
-    return (dev, M, N, K, qa.data_ptr(), _dense(sa, torch.float32, (M, KB), dev, "sa"), _dense(qw, _FP8, shape, dev, "qw"),
-            _dense(sw, torch.float32, (*shape[:-2], _cdiv(N, FP8_BLOCK), KB), dev, "sw"),
-            _dense(out, out_dtype, (M, N), dev, "out"), kind, out)
+    dev, KB, NB = qa.get_device(), -(-K // FP8_BLOCK), -(-N // FP8_BLOCK)
+    if qw.get_device() != dev:
+        raise ValueError(f"qw is on {qw.device}, not on cuda:{dev}")
+    psa = _dense(sa, torch.float32, (M, KB), dev, "sa")
+    psw = _dense(sw, torch.float32, (NB, KB) if ndim == 2 else (shape[0], NB, KB), dev, "sw")
+    out, py = _out(out, (M, N), out_dtype, qa, dev, stream, "out")
+    return dev, M, N, K, qa.data_ptr(), psa, qw.data_ptr(), psw, py, kind, out
 
 
 def q8_gemm_fp8(qa, sa, qw, sw, out_dtype=torch.bfloat16, out=None, stream=None):
     """y[m, n] = sum over blocks b of sa[m, b] sw[n / 128, b] (qa . qw over block b), as out_dtype [M, N]."""
-    dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 2, out_dtype, out)
+    dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 2, out_dtype, out, stream)
     _check(load().q8_gemm_fp8(pa, psa, pw, psw, M, N, K, py, kind, _handle(dev, stream)), "q8_gemm_fp8")
     return out
 
@@ -770,7 +776,7 @@ def q8_gemm_fp8(qa, sa, qw, sw, out_dtype=torch.bfloat16, out=None, stream=None)
 def q8_gemm_fp8_grouped(qa, sa, qw, sw, offsets, out_dtype=torch.bfloat16, out=None, stream=None):
     """The product of q8_gemm_fp8 with qw[e] (of qw[E, N, K]) for the rows offsets[e] .. offsets[e + 1] - 1 of each
     expert; offsets int32 [E + 1] stay on the device. Rows of no expert are not written."""
-    dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 3, out_dtype, out)
+    dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 3, out_dtype, out, stream)
     E = qw.shape[0]
     _check(load().q8_gemm_fp8_grouped(pa, psa, pw, psw, _dense(offsets, torch.int32, (E + 1,), dev, "offsets"), M, E, N, K,
                                       py, kind, _handle(dev, stream)), "q8_gemm_fp8_grouped")
@@ -790,12 +796,10 @@ def q8_moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=
         raise ValueError("top_k must be positive")
     dev = logits.get_device()
     pb = None if bias is None else _dense(bias, torch.float32, (E,), dev, "bias")
-    idx = _new((T, top_k), torch.int32, logits) if idx is None else idx
-    weights = _new((T, top_k), torch.float32, logits) if weights is None else weights
+    idx, pi = _out(idx, (T, top_k), torch.int32, logits, dev, stream, "idx")
+    weights, pw = _out(weights, (T, top_k), torch.float32, logits, dev, stream, "weights")
     _check(load().q8_moe_route(logits.data_ptr(), kind, T, E, ldl, top_k, SCORES[score], pb, n_group, topk_group,
-                               1 if renorm else 0, scale, _dense(idx, torch.int32, (T, top_k), dev, "idx"),
-                               _dense(weights, torch.float32, (T, top_k), dev, "weights"), _handle(dev, stream)),
-           "q8_moe_route")
+                               1 if renorm else 0, scale, pi, pw, _handle(dev, stream)), "q8_moe_route")
     return idx, weights
 
 
@@ -807,10 +811,9 @@ def q8_moe_plan(idx: torch.Tensor, n_experts: int, offsets=None, slots=None, str
         raise ValueError("n_experts must be positive")
     T, k = idx.shape
     dev = idx.get_device()
-    offsets = _new((n_experts + 1,), torch.int32, idx) if offsets is None else offsets
-    slots = _new((T, k), torch.int32, idx) if slots is None else slots
-    _check(load().q8_moe_plan(idx.data_ptr(), T, k, n_experts, _dense(offsets, torch.int32, (n_experts + 1,), dev, "offsets"),
-                              _dense(slots, torch.int32, (T, k), dev, "slots"), _handle(dev, stream)), "q8_moe_plan")
+    offsets, po = _out(offsets, (n_experts + 1,), torch.int32, idx, dev, stream, "offsets")
+    slots, ps = _out(slots, (T, k), torch.int32, idx, dev, stream, "slots")
+    _check(load().q8_moe_plan(idx.data_ptr(), T, k, n_experts, po, ps, _handle(dev, stream)), "q8_moe_plan")
     return offsets, slots
 
 
@@ -823,8 +826,8 @@ def q8_moe_combine(h: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, 
     _need(slots, torch.int32, "slots", 2)
     T, k = slots.shape
     dev = h.get_device()
-    out = _new((T, N), h.dtype, h) if out is None else out
-    _check(load().q8_moe_combine(h.data_ptr(), kind, rows, N, _dense(slots, torch.int32, (T, k), dev, "slots"),
-                                 _dense(weights, torch.float32, (T, k), dev, "weights"), T, k,
-                                 _dense(out, h.dtype, (T, N), dev, "out"), _handle(dev, stream)), "q8_moe_combine")
+    ps = _dense(slots, torch.int32, (T, k), dev, "slots")
+    pw = _dense(weights, torch.float32, (T, k), dev, "weights")
+    out, py = _out(out, (T, N), h.dtype, h, dev, stream, "out")
+    _check(load().q8_moe_combine(h.data_ptr(), kind, rows, N, ps, pw, T, k, py, _handle(dev, stream)), "q8_moe_combine")
     return out

@@ -212,9 +212,10 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
         for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(kFull, z, d);
     }
     auto exact_key = [&](int e) {
-        const double l = load_logit(row + e);
-        if (!a.bias) return l;
-        return (a.softmax ? exp(l - (double)m) / z : 1.0 / (1.0 + exp(-l))) + (double)__ldg(a.bias + e);
+        const double l = load_logit(row + e);   // not masked
+        if (!a.bias) return ordered(l);
+        const double k = (a.softmax ? exp(l - (double)m) / z : 1.0 / (1.0 + exp(-l))) + (double)__ldg(a.bias + e);
+        return k > -(double)INFINITY ? ordered(k) : (uint64_t)0;   // a bias of -inf or NaN masks as well
     };
     int count = 0;
     if (!__any_sync(kFull, doubt.group)) {
@@ -232,7 +233,7 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
         __syncwarp();
         if (count <= 32) {
             const int e = lane < count ? list[lane] : -1;
-            const uint64_t k = e >= 0 ? ordered(exact_key(e)) : 0;
+            const uint64_t k = e >= 0 ? exact_key(e) : 0;
             int rank = 0;
             for (int t = 0; t < count; ++t) {
                 const uint64_t o = __shfl_sync(kFull, k, t);
@@ -248,7 +249,7 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
     uint64_t key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? ordered(exact_key(pl.base + i)) : 0;
+        key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? exact_key(pl.base + i) : 0;
     uint64_t x, y;
     if (a.n_group > 1 && !keep_group<VPL, uint64_t>(key, pl, a, a.bias != nullptr, x, y))
 #pragma unroll

@@ -83,7 +83,7 @@ def route(logits, k, score, bias=None, n_group=1, topk_group=1, renorm=True, sca
         else:
             p = {e: (1.0 / (1.0 + math.exp(-float(l[t, e]))) if float(l[t, e]) > -700 else 0.0) for e in live}
         key = {e: (float(l[t, e]) if bias is None else p[e] + float(bias[e])) for e in live}
-        key = {e: v for e, v in key.items() if v > -math.inf}
+        key = {e: v for e, v in key.items() if v > -math.inf}      # nor NaN: a bias can mask too
         if n_group > 1:
             per = E // n_group
             rank = []

@@ -85,6 +85,27 @@ def test_route_near_ties_are_decided_in_64_bits(q8, score):
     check_route(q8, logits, 8, bias, score=score, n_group=8, topk_group=3, renorm=True, scale=1.0)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_too_few_experts_and_masking_bias(q8, score):
+    """One group of four cannot give six experts; a bias of -inf or NaN masks, +inf puts first; equal keys throughout."""
+    g = torch.Generator().manual_seed(5)
+    logits = torch.randn((40, 32), generator=g)
+    bias = torch.zeros(32)
+    idx, w = check_route(q8, logits, 6, bias, score=score, n_group=8, topk_group=1)
+    assert (idx[:, 4:] == -1).all() and (w[:, 4:] == 0).all()
+    bias[3], bias[7], bias[11], bias[30] = -math.inf, math.nan, math.inf, -math.inf
+    check_route(q8, logits, 6, bias, score=score)
+    check_route(q8, logits, 31, bias, score=score, renorm=False)
+    check_route(q8, torch.zeros(9, 32), 30, bias, score=score)         # every key equal, more than 28 left: -1
+    check_route(q8, torch.zeros(9, 32), 5, bias, score=score, n_group=4, topk_group=2)
+
+
+def test_route_all_equal_over_lanes(q8):
+    """512 equal keys: the first experts, through the fp64 path with more candidates than lanes."""
+    for bias in (None, torch.zeros(512)):
+        check_route(q8, torch.full((3, 512), 0.25), 32, bias, score="sigmoid")
+
+
 def test_route_strided_rows(q8):
     base = torch.randn((21, 100), generator=torch.Generator().manual_seed(1)).cuda()
     x = base[::3, 5:69]
@@ -182,6 +203,20 @@ def test_layer_and_its_capture(q8, T):
         torch.cuda.synchronize()
         assert torch.equal(out, eager[i][0])
     assert q8.q8_device_error() == 0
+
+
+def test_results_belong_to_the_stream_that_writes_them(q8):
+    """Results allocated by a call with a stream come from that stream's memory."""
+    side = torch.cuda.Stream()
+    logits = torch.randn((64, 16), device="cuda")
+    torch.cuda.synchronize()
+    idx, w = q8.q8_moe_route(logits, 2, stream=side)
+    offsets, slots = q8.q8_moe_plan(idx, 16, stream=side)
+    side.synchronize()
+    want, _ = ref.route(logits.cpu(), 2, "softmax")
+    assert torch.equal(idx.cpu(), want)
+    wo, ws = ref.plan(want, 16)
+    assert torch.equal(offsets.cpu(), wo) and torch.equal(slots.cpu(), ws)
 
 
 def test_example_runs_small():
