@@ -508,8 +508,8 @@ cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_
 //   warp 0     TMA: tokens [128 x 128] and weights [PN / 2 x 128] of each K block, completing on the even CTA's
 //              barrier
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
-//   warps 2, 3 scales: sa sw of the CTA's 128 token rows and the tile's one or two weight blocks, eight K blocks at
-//              a time (a sector of a row of sa), into shared memory
+//   warps 2, 3 scales: sa sw of the CTA's 128 token rows and the tile's one or two weight blocks, four K blocks at
+//              a time (half a sector of a row of sa), into shared memory
 //   warps 4-11 drain: a TMEM lane is a token row, so a thread's scale is one value a block, and the sum
 //              costs one multiply-add a value; two warps for each quarter of the lanes, PN / 2 columns each
 // Measured at 8192x8192x16384: 804 us from a cool start (2.7 PFLOP/s), 880 to 900 us back to back, where the power
@@ -525,9 +525,9 @@ constexpr int kPairLd = 64;                      // columns of one TMEM load
 constexpr int kPairRegsLow = 88, kPairRegsHigh = 208;
 static_assert(128 * kPairRegsLow + 32 * kPairDrain * kPairRegsHigh <= kPairThreads * (65536 / kPairThreads / 8 * 8),
               "above the launch's registers");
-constexpr int kPairEpi = 1024;                   // of a drain warp: 32 rows x 32 bytes
-constexpr int kScaleBlocks = 8;                  // K blocks of one hand-over of scales
-constexpr int kScalePitch = PTH + 4;             // floats of a block's row of scales: no bank conflicts
+constexpr int kPairEpi = 2048;                   // of a drain warp: 32 rows x 64 bytes
+constexpr int kScaleBlocks = 4;                  // K blocks of one hand-over of scales
+constexpr int kScalePitch = PTH + 8;             // floats of a block's row of scales: no bank conflicts
 constexpr int kScaleHalf = kScaleBlocks * kScalePitch;
 
 template <int PN>
@@ -582,48 +582,48 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
-// A drain warp's 32 rows x 2 NC columns (one row a lane) to y, 32 bytes of each row at a time through
-// shared memory (16-byte chunk j of row r at j ^ (r / 4 % 2): no bank conflicts either way), so that
-// two lanes write a whole sector. Rows of y that are not whole 16-byte chunks go by words, or by 16-bit values for
+// A drain warp's 32 rows x 2 NC columns (one row a lane) to y, 64 bytes of each row at a time through
+// shared memory (16-byte chunk j of row r at j ^ (r / 2 % 4): no bank conflicts either way), so that
+// four lanes write two sectors. Rows of y that are not whole 16-byte chunks go by words, or by 16-bit values for
 // an odd number of them, the lanes of a row side by side (6532 fp32 rows of 4575 columns, K = 320: 147 us when
 // a lane wrote its 16 bytes value by value).
 template <class T, int NC>
 __device__ __forceinline__ void store_rows(T* y, int64_t row0, int live, int col0, int N, const uint64_t (&acc)[NC],
                                            uint32_t buf, int lane) {
-    constexpr int kCols = 32 / sizeof(T);         // columns of a step
+    constexpr int kCols = 64 / sizeof(T);         // columns of a step
     const int unit = (N * sizeof(T)) % 16 == 0 ? 16 : (N * sizeof(T)) % 4 == 0 ? 4 : 2;
 #pragma unroll
     for (int c = 0; c < 2 * NC / kCols; ++c) {
-        uint32_t w[8];
+        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 16; ++j) {
             if constexpr (sizeof(T) == 2) {
-                const float2 f = unpack2(acc[c * 8 + j]);
+                const float2 f = unpack2(acc[c * 16 + j]);
                 w[j] = pack16<T>(f.x, f.y);
             } else {
-                const float2 f = unpack2(acc[c * 4 + j / 2]);
+                const float2 f = unpack2(acc[c * 8 + j / 2]);
                 w[j] = __float_as_uint(j & 1 ? f.y : f.x);
             }
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            sts128(buf + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4),
+        for (int j = 0; j < 4; ++j)
+            sts128(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
         __syncwarp();
         const int at = col0 + c * kCols;
         // byte b of row r of the staged step
-        auto staged = [&](int r, int b) { return buf + r * 32 + (((b >> 4) ^ ((r >> 2) & 1)) << 4) + (b & 15); };
+        auto staged = [&](int r, int b) { return buf + r * 64 + (((b >> 4) ^ ((r >> 1) & 3)) << 4) + (b & 15); };
         if (unit == 16) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = i * 16 + lane / 2, b = (lane & 1) * 16, col = at + b / (int)sizeof(T);
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 8 + lane / 4, b = (lane & 3) * 16, col = at + b / (int)sizeof(T);
                 const uint4 v = lds128(staged(r, b));
                 if (r < live && col < N) *reinterpret_cast<uint4*>(y + (row0 + r) * N + col) = v;
             }
         } else {
             // lane's bytes b of rows r, r + step, ...: loops, so that their addresses do not cost registers here
-            const int lanes = 32 / unit, step = unit;   // lanes of a row, rows of a pass: 8 and 4, or 16 and 2
+            const int lanes = 64 / unit, step = unit / 2;   // lanes of a row, rows of a pass: 16 and 2, or 32 and 1
             const int b = lane % lanes * unit, col = at + b / (int)sizeof(T);
 #pragma unroll 2
             for (int r = lane / lanes; r < live && col < N; r += step) {
@@ -750,11 +750,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         } else if (warp >= 2) {
             // --------------------------------------------------------------------- scales
-            // A lane loads K block lane % 8 of every eighth row; the next eight blocks' loads are
-            // in flight while it waits for the buffer.
-            constexpr int kRows = PTH / 8;
+            // A lane loads K block lane % 4 of every 16th row; the next four blocks' loads are in
+            // flight while it waits for the buffer.
+            constexpr int kStep = 64 / kScaleBlocks, kRows = PTH / kStep;   // rows of a pass, passes
             const int NB = (p.N + BK - 1) / BK;
-            const int b = lane & 7, r0 = (warp - 2) * 4 + lane / 8;
+            const int b = lane % kScaleBlocks, r0 = (warp - 2) * (kStep / 2) + lane / kScaleBlocks;
             uint32_t c = 0;
             bool ok = true;
             for (uint32_t u = first; u < units && ok; u += step) {
@@ -765,7 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const float* w0 = p.sw + ((int64_t)e * NB + nt * (PN / BK)) * KB;
                 const float* w1 = PN > BK && nt * (PN / BK) + 1 < NB ? w0 + KB : w0;
                 const float* sa = p.sa + (int64_t)row * KB;
-                const int have = (p.rows - row + 7) / 8;   // rows of this lane that exist
+                const int have = (p.rows - row + kStep - 1) / kStep;   // rows of this lane that exist
                 float a[kRows], f0, f1;
                 auto load = [&](int kb) {
                     const int rows_in = kb < KB ? have : 0;
@@ -773,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     f1 = kb < KB ? __ldg(w1 + kb) : 0.0f;
                     const float* from = sa + kb;
 #pragma unroll
-                    for (int i = 0; i < kRows; ++i, from += 8 * KB) a[i] = i < rows_in ? __ldg(from) : 0.0f;
+                    for (int i = 0; i < kRows; ++i, from += kStep * KB) a[i] = i < rows_in ? __ldg(from) : 0.0f;
                 };
                 load(b);
                 for (int kb = 0; kb < KB; kb += kScaleBlocks, ++c) {
@@ -785,8 +785,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     float* out = scales + buf * 2 * kScaleHalf + b * kScalePitch + r0;
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) {
-                        out[8 * i] = a[i] * f0;
-                        if (PN > BK) out[8 * i + kScaleHalf] = a[i] * f1;
+                        out[kStep * i] = a[i] * f0;
+                        if (PN > BK) out[kStep * i + kScaleHalf] = a[i] * f1;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_scfull + 8 * buf);
