@@ -20,6 +20,15 @@ using namespace tc;
 
 __device__ unsigned int g_fp8_error = 0;
 
+// Bounded waits of a whole warp: its lanes agree on how the wait ended, so that none goes on alone to an
+// instruction that takes them all.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, code, &g_fp8_error));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned code) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag, code, &g_fp8_error));
+}
+
 constexpr int BK = kFp8Block;          // K of a stage: one scale block, 128 bytes a row
 constexpr int TW = 128;                // weight rows of a tile: one scale block, the MMA's M side
 constexpr int kTileW = TW * BK;        // 16 KB
@@ -238,8 +247,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
             groups.tile((int)(u / (uint32_t)NT), e, row, n);
             const int wrow = e * p.N + (int)(u % (uint32_t)NT) * TW, boxes = (n + C::kBox - 1) / C::kBox;
             for (int kb = kb0; kb < kb1; ++kb) {
-                const bool got = mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error);
-                if (!__all_sync(0xffffffffu, got)) {
+                if (!warp_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer)) {
                     ok = false;
                     break;
                 }
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     if (kb + i >= kb1) break;
-                    if (!mbar_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrConvEmpty, &g_fp8_error)) {
+                    if (!warp_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrConvEmpty)) {
                         ok = false;
                         break;
                     }
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
 #pragma unroll
             for (int j = 0; j < CW; ++j) acc[j] = 0.0f;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain, &g_fp8_error)) {
+                if (!warp_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain)) {
                     ok = false;
                     break;
                 }
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                 const int per = (groups4 + S - 1) / S;          // slots of groups in the receive buffer
                 const int here = (groups4 - rank + S - 1) / S;  // groups that this CTA owns (may be 0)
                 const uint32_t buffer = sbase + off_reduce, lane16 = (quarter * 32 + lane) * 16;
-                if (done && !mbar_wait_cluster(bar_free, (done - 1) & 1, abort_flag, kErrRelay, &g_fp8_error)) break;
+                if (done && !warp_wait_cluster(bar_free, (done - 1) & 1, abort_flag, kErrRelay)) break;
                 if (warp == 4 && lane == 0) mbar_expect_tx(bar_got, (S - 1) * max(here, 0) * TW * 16);
 #pragma unroll
                 for (int q = 0; q < CW / 4; ++q) {
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                                    mapa_shared(bar_got, owner));
                     }
                 }
-                if (!mbar_wait_cluster(bar_got, done & 1, abort_flag, kErrRelay, &g_fp8_error)) break;
+                if (!warp_wait_cluster(bar_got, done & 1, abort_flag, kErrRelay)) break;
 #pragma unroll
                 for (int q = 0; q < CW / 4; ++q) {
                     const int g = t0 / 4 + q;
@@ -706,8 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 groups.tile(t, e, row, n);
                 const int arow = row + rank * PTH, wrow = e * p.N + nt * PN + rank * C::kHalf;
                 for (int kb = 0; kb < KB; ++kb) {
-                    const bool got = mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer, &g_fp8_error);
-                    if (!__all_sync(0xffffffffu, got)) {
+                    if (!warp_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer)) {
                         ok = false;
                         break;
                     }
@@ -778,7 +785,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 load(b);
                 for (int kb = 0; kb < KB; kb += kScaleBlocks, ++c) {
                     const uint32_t buf = c & 1;
-                    if (!mbar_wait(bar_scempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrConvEmpty, &g_fp8_error)) {
+                    if (!warp_wait(bar_scempty + 8 * buf, ((c >> 1) & 1) ^ 1, abort_flag, kErrConvEmpty)) {
                         ok = false;
                         break;
                     }
@@ -814,11 +821,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int kb = 0; kb < KB; ++kb) {
                 const uint32_t buf = s % kBufs, sbuf = sc & 1;
                 const int i = kb % kScaleBlocks;
-                if ((i == 0 && !mbar_wait(bar_scfull + 8 * sbuf, (sc >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error)) ||
-                    !mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrDrain, &g_fp8_error)) {
-                    ok = false;
-                    break;
+                // A wait for a block that runs out sets the abort flag; the warp goes on together, and leaves where it
+                // votes, at the next four blocks (a vote in every block costs 2 %).
+                if (i == 0) {
+                    const bool go = mbar_wait(bar_scfull + 8 * sbuf, (sc >> 1) & 1, abort_flag, kErrDrain, &g_fp8_error) &&
+                                    !*abort_flag;
+                    if (!__all_sync(0xffffffffu, go)) {
+                        ok = false;
+                        break;
+                    }
                 }
+                mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrDrain, &g_fp8_error);
                 tc_fence_after();
                 const float f = own[sbuf * 2 * kScaleHalf + i * kScalePitch];
                 const uint64_t f2 = pack2(f, f);
