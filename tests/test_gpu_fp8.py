@@ -288,3 +288,78 @@ def test_on_another_stream(q8):
     q8.q8_gemm_fp8(*dev, out_dtype=torch.float32, out=y, stream=side)
     side.synchronize()
     check(y, qa, sa, qw, sw, torch.float32)
+
+
+# ------------------------------------------------------------------------------- sizes, refusals
+
+def test_outputs_past_32_bit_offsets(q8):
+    """More than 2^31 elements in x, the codes and y: the last rows are where they belong."""
+    M, K = 131100, 16384
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = ref.tokens(3, K, seed=1).to(torch.bfloat16).cuda()
+    q, s = q8.q8_quantize_fp8(x)
+    wq, ws = ref.quantize(x[-3:].float().cpu())
+    same_codes(q[-3:], wq)
+    same_scales(s[-3:], ws)
+    del x, q, s
+    for M, N in ((65600, 32800), (40, (1 << 31) // 40 + 1000)):
+        qa, sa, qw, sw = operands(64, 256, 16, seed=M)
+        qa, sa = (t.repeat(ref.cdiv(M, 64), 1)[:M] for t in (qa.view(torch.uint8).cuda(), sa.cuda()))
+        qw = qw.view(torch.uint8).cuda().repeat(ref.cdiv(N, 256), 1)[:N]
+        sw = sw.cuda().repeat(ref.cdiv(N, 256), 1)[:ref.cdiv(N, 128)].contiguous()
+        y = q8.q8_gemm_fp8(qa.view(torch.float8_e4m3fn), sa, qw.view(torch.float8_e4m3fn), sw, out_dtype=torch.bfloat16)
+        rows, cols = slice(M - 40, M), slice((N - 300) // 128 * 128, N)
+        part = [t.cpu() for t in (qa[rows], sa[rows], qw[cols], sw[cols.start // 128:])]
+        check(y[rows, cols], part[0].view(torch.float8_e4m3fn), part[1], part[2].view(torch.float8_e4m3fn), part[3],
+              torch.bfloat16)
+        del qa, sa, qw, sw, y
+
+
+def test_binding_refusals(q8):
+    qa, sa, qw, sw = (t.cuda() for t in operands(8, 256, 256, seed=1))
+    for change in (dict(sa=sa[:, :1]), dict(sa=sa.half()), dict(qa=qa[:, :240]), dict(sw=sw[:1]), dict(qa=qa.view(torch.uint8)),
+                   dict(qw=qw.view(torch.uint8)), dict(out=torch.empty(8, 255, device="cuda", dtype=torch.bfloat16)),
+                   dict(out=torch.empty(8, 256, device="cuda")), dict(out_dtype=torch.float64), dict(sw=sw.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            q8.q8_gemm_fp8(**{**dict(qa=qa, sa=sa, qw=qw, sw=sw), **change})
+    with pytest.raises(ValueError):
+        q8.q8_gemm_fp8_grouped(qa, sa, qw[None], sw[None], torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(TypeError):
+        q8.q8_gemm_fp8_grouped(qa, sa, qw[None], sw[None], torch.zeros(2, dtype=torch.int64, device="cuda"))
+    x = torch.zeros((4, 256), device="cuda")
+    with pytest.raises(ValueError):
+        q8.q8_quantize_fp8(x, slots=torch.zeros((3, 2), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        q8.q8_quantize_fp8(x, rows=5)
+    with pytest.raises(ValueError):
+        q8.q8_quantize_fp8(x[:1].expand(4, 256))
+    with pytest.raises(q8.Q8Error):
+        q8.q8_quantize_fp8(torch.zeros((4, 100), device="cuda"))
+    with pytest.raises(ValueError):
+        q8.q8_swiglu_quantize_fp8(torch.zeros((4, 33), device="cuda"))
+    with pytest.raises(ValueError):
+        q8.q8_moe_route(x, 2, score="relu")
+    with pytest.raises(q8.Q8Error):
+        q8.q8_moe_route(x, 257)
+    with pytest.raises(ValueError):
+        q8.q8_moe_combine(x[:, :128], torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.zeros((1, 1), device="cuda"))
+
+
+def test_nothing_to_do(q8):
+    """No rows, no experts with rows, no answers: empty results, or zeros."""
+    e = torch.empty((0, 256), device="cuda")
+    q, s = q8.q8_quantize_fp8(e)
+    assert q.shape == (0, 256) and s.shape == (0, 2)
+    qw, sw = q8.q8_quantize_weight_fp8(torch.randn((2, 128, 256), device="cuda"))
+    assert q8.q8_gemm_fp8(q, s, qw[0], sw[0]).shape == (0, 128)
+    offsets = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert q8.q8_gemm_fp8_grouped(q, s, qw, sw, offsets).shape == (0, 128)
+    q, s = q8.q8_quantize_fp8(torch.randn((5, 256), device="cuda"))
+    y = torch.full((5, 128), 3.0, device="cuda")
+    q8.q8_gemm_fp8_grouped(q, s, qw, sw, offsets, out_dtype=torch.float32, out=y)
+    assert (y == 3).all()
+    idx, w = q8.q8_moe_route(torch.empty((0, 8), device="cuda"), 2)
+    assert idx.shape == (0, 2) and w.shape == (0, 2)
+    y = q8.q8_moe_combine(torch.empty((0, 64), device="cuda"), torch.full((3, 2), -1, dtype=torch.int32, device="cuda"),
+                          torch.ones((3, 2), device="cuda"))
+    assert y.shape == (3, 64) and (y == 0).all()
