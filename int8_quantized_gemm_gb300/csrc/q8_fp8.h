@@ -74,6 +74,28 @@ struct Vec16 {
     };
     __device__ __forceinline__ Vec16() {}
 };
+__device__ __forceinline__ void to_floats(const Vec16<float>& v, float (&f)[4]) {
+    f[0] = v.t[0];
+    f[1] = v.t[1];
+    f[2] = v.t[2];
+    f[3] = v.t[3];
+}
+__device__ __forceinline__ void to_floats(const Vec16<__nv_bfloat16>& v, float (&f)[8]) {   // a shift or a mask each
+    const uint32_t w[4] = {v.u.x, v.u.y, v.u.z, v.u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void to_floats(const Vec16<__half>& v, float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 t = __half22float2(__halves2half2(v.t[2 * j], v.t[2 * j + 1]));
+        f[2 * j] = t.x;
+        f[2 * j + 1] = t.y;
+    }
+}
 #endif
 
 }  // namespace q8

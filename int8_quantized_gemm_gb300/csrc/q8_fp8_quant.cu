@@ -32,14 +32,39 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// u * g / (1 + exp(-g)). The fast exponential and reciprocal are off by a few 2^-22 relative for
-// g > -20 (a thousandth of an e4m3 step); below, the value is under 5e-8 |u|. For exp(-g) above
-// 2^126 the reciprocal gives 0, its limit.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));   // exp(-g) = 2^(-g log2 e)
-    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.0f + e));
-    return __fmul_rn(__fmul_rn(g, r), u);
+// Two fp32 values as one operand: the pair operations take one issue slot for two.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Two of u * g / (1 + exp(-g)), exp(-g) = 2^(-g log2 e). The fast exponential and reciprocal are off by a few 2^-22
+// relative for g > -20 (a thousandth of an e4m3 step); below, the value is under 5e-8 |u|. For exp(-g)
+// above 2^126 the reciprocal gives 0, its limit.
+__device__ __forceinline__ void silu_mul2(float& g0, float& g1, float u0, float u1) {
+    const uint64_t g = pack2(g0, g1);
+    float e0, e1, r0, r1;
+    unpack2(mul2(g, pack2(-1.4426950408889634f, -1.4426950408889634f)), e0, e1);
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e0) : "f"(e0));
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e1) : "f"(e1));
+    unpack2(add2(pack2(e0, e1), pack2(1.0f, 1.0f)), e0, e1);
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r0) : "f"(e0));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r1) : "f"(e1));
+    unpack2(mul2(mul2(g, pack2(r0, r1)), pack2(u0, u1)), g0, g1);
 }
 
 // max(m, |a|, |b|), NaN if one is (its bits are then above those of inf).
@@ -57,8 +82,7 @@ enum Form : int { kDense = 0, kGated = 1, kSlots = 2 };
 // rows in order; kSlots: `wpr` warps for each row, which copies its blocks to the row's slots. kWhole:
 // K is a multiple of 128, so that block b's codes are at 128 b and its scale at b.
 // Bound by memory: 8192 x 16384 fp32 92 us on the device (98 us back to back, 6.9 TB/s); the gated form,
-// 32768 x 2048 bf16, 53 us (56, 6.0 TB/s), is near the issue rate (82 %: 12 instructions an
-// element); 1037 x 4096 bf16 to 8 slots 10.5 us, 4.2 TB/s of mostly writes, launch and tail included.
+// 32768 x 2048 bf16, 51 us (54 back to back; issue slots 75 % busy); 1037 x 4096 bf16 to 8 slots 10.5 us, 4.2 TB/s of mostly writes, launch and tail included.
 template <class T, int kForm, bool kWhole>
 __global__ void __launch_bounds__(kThreads)
     quantize_fp8_kernel(const T* __restrict__ x, uint32_t total, uint32_t KB, uint32_t K, int64_t ldx, uint32_t wpr,
@@ -118,10 +142,12 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
         float most = 0.0f;
+        to_floats(v[i], f[i]);
+        if constexpr (kForm == kGated) {
+            float by[n];
+            to_floats(up[i], by);
 #pragma unroll
-        for (int j = 0; j < n; ++j) {
-            f[i][j] = to_float(v[i].t[j]);
-            if (kForm == kGated) f[i][j] = silu_mul(f[i][j], to_float(up[i].t[j]));
+            for (int j = 0; j < n; j += 2) silu_mul2(f[i][j], f[i][j + 1], by[j], by[j + 1]);
         }
 #pragma unroll
         for (int j = 0; j < n; j += 2) most = max_abs(most, f[i][j], f[i][j + 1]);
@@ -140,9 +166,12 @@ __global__ void __launch_bounds__(kThreads)
         sc[i] = __shfl_sync(0xffffffffu, own_s, i, kLanes);
         const float r = __shfl_sync(0xffffffffu, own_r, i, kLanes);
 #pragma unroll
-        for (int j = 0; j < n / 4; ++j)
-            c[i][j] = pack4(__fmul_rn(f[i][4 * j], r), __fmul_rn(f[i][4 * j + 1], r), __fmul_rn(f[i][4 * j + 2], r),
-                            __fmul_rn(f[i][4 * j + 3], r));
+        for (int j = 0; j < n / 4; ++j) {
+            float a, b, d, e;
+            unpack2(mul2(pack2(f[i][4 * j], f[i][4 * j + 1]), pack2(r, r)), a, b);
+            unpack2(mul2(pack2(f[i][4 * j + 2], f[i][4 * j + 3]), pack2(r, r)), d, e);
+            c[i][j] = pack4(a, b, d, e);
+        }
     }
     auto put = [&](uint8_t* to, float* scale, int i) {
         if (!in[i]) return;

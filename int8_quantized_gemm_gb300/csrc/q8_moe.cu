@@ -499,9 +499,12 @@ __global__ void __launch_bounds__(256)
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-            if (in[j])
+            if (in[j]) {
+                float f[n];
+                to_floats(v[j], f);
 #pragma unroll
-                for (int q = 0; q < n; ++q) acc[q] = __fmaf_rn(wt[j], to_float(v[j].t[q]), acc[q]);
+                for (int q = 0; q < n; ++q) acc[q] = __fmaf_rn(wt[j], f[q], acc[q]);
+            }
     }
     Vec16<T> o;
 #pragma unroll
