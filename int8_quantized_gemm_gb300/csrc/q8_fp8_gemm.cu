@@ -516,8 +516,8 @@ cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_
 //   warp 0     TMA: tokens [128 x 128] and weights [PN / 2 x 128] of each K block, completing on the even CTA's
 //              barrier
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
-//   warps 2, 3 scales: sa sw of the CTA's 128 token rows and the tile's one or two weight blocks, four K blocks at
-//              a time (half a sector of a row of sa), into shared memory
+//   warps 2, 3 scales: sa sw of the CTA's 128 token rows and the tile's one or two weight blocks, four or eight
+//              K blocks at a time (neighbours in a row of sa), into shared memory
 //   warps 4-11 drain: a TMEM lane is a token row, so a thread's scale is one value a block, and the sum
 //              costs one multiply-add a value; two warps for each quarter of the lanes, PN / 2 columns each
 // Measured at 8192x8192x16384: 804 us from a cool start (2.7 PFLOP/s), 880 to 900 us back to back, where the power
@@ -534,9 +534,7 @@ constexpr int kPairRegsLow = 88, kPairRegsHigh = 208;
 static_assert(128 * kPairRegsLow + 32 * kPairDrain * kPairRegsHigh <= kPairThreads * (65536 / kPairThreads / 8 * 8),
               "above the launch's registers");
 constexpr int kPairEpi = 2048;                   // of a drain warp: 32 rows x 64 bytes
-constexpr int kScaleBlocks = 4;                  // K blocks of one hand-over of scales
-constexpr int kScalePitch = PTH + 8;             // floats of a block's row of scales: no bank conflicts
-constexpr int kScaleHalf = kScaleBlocks * kScalePitch;
+constexpr int kScalePitch = PTH + 8;             // floats of a block's row of scales
 
 template <int PN>
 struct Pair8Cfg {
@@ -545,9 +543,13 @@ struct Pair8Cfg {
     static constexpr int kStages = PN == 256 ? 6 : 8;
     static constexpr int kBufs = 512 / PN;                    // accumulator buffers: block c is in stage c % kStages
     static_assert(kStages % kBufs == 0, "a stage has its buffer");   // and buffer c % kBufs
+    static constexpr int kScaleBlocks = PN == 256 ? 4 : 8;    // K blocks of one hand-over of scales, as room allows
+                                                              // (256x8192x8192, narrow: 27 us with 4, 25 with 8)
+    static constexpr int kScaleHalf = kScaleBlocks * kScalePitch;   // of one weight block
     static constexpr int kOffEpi = kStages * kStage;
     static constexpr int kOffScale = kOffEpi + kPairDrain * kPairEpi;
-    static constexpr int kOffBar = kOffScale + 2 * 2 * kScaleHalf * 4;
+    static constexpr int kScaleBuf = PN / BK * kScaleHalf;
+    static constexpr int kOffBar = kOffScale + 2 * kScaleBuf * 4;
     static constexpr int kBars = 2 * kStages + kBufs + 4;
     static constexpr int kSmem = 1024 + kOffBar + 8 * kBars + 32 + 4 * (kMaxExperts + 2);
     static_assert(kSmem <= kSmemMax, "above the shared memory of one CTA");
@@ -655,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
                          PairArgs p) {
     using C = Pair8Cfg<PN>;
-    constexpr int kStages = C::kStages, kBufs = C::kBufs;
+    constexpr int kStages = C::kStages, kBufs = C::kBufs, kScaleBlocks = C::kScaleBlocks;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t sraw = smem_u32(smem_raw);
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
@@ -666,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t bar_accempty = bar_done + 8 * kStages;  // used in the even CTA: both CTAs' drain warps
     const uint32_t bar_scfull = bar_accempty + 8 * kBufs;
     const uint32_t bar_scempty = bar_scfull + 16;
-    float* scales = reinterpret_cast<float*>(smem + C::kOffScale);   // [2 buffers][2 weight blocks][K block][row]
+    float* scales = reinterpret_cast<float*>(smem + C::kOffScale);   // [2 buffers][weight block][K block][row]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* cum = reinterpret_cast<int*>(tmem_slot + 2);
@@ -757,8 +759,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         } else if (warp >= 2) {
             // --------------------------------------------------------------------- scales
-            // A lane loads K block lane % 4 of every 16th row; the next four blocks' loads are in
-            // flight while it waits for the buffer.
+            // A lane loads one K block of every 16th (8th) row; the next blocks' loads are in flight while
+            // it waits for the buffer.
             constexpr int kStep = 64 / kScaleBlocks, kRows = PTH / kStep;   // rows of a pass, passes
             const int NB = (p.N + BK - 1) / BK;
             const int b = lane % kScaleBlocks, r0 = (warp - 2) * (kStep / 2) + lane / kScaleBlocks;
@@ -789,11 +791,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         ok = false;
                         break;
                     }
-                    float* out = scales + buf * 2 * kScaleHalf + b * kScalePitch + r0;
+                    float* out = scales + buf * C::kScaleBuf + b * kScalePitch + r0;
 #pragma unroll
                     for (int i = 0; i < kRows; ++i) {
                         out[kStep * i] = a[i] * f0;
-                        if (PN > BK) out[kStep * i + kScaleHalf] = a[i] * f1;
+                        if (PN > BK) out[kStep * i + C::kScaleHalf] = a[i] * f1;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_scfull + 8 * buf);
@@ -807,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int quarter = warp & 3, part = ((warp - 4) >> 2) * C::kHalf;   // its first column
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + part;
         const uint32_t free_bar = mapa_shared(bar_accempty, 0);
-        const float* own = scales + (part / BK) * kScaleHalf + quarter * 32 + lane;
+        const float* own = scales + (part / BK) * C::kScaleHalf + quarter * 32 + lane;
         uint32_t s = 0, phase = 0, sc = 0;     // s: the block's stage; its buffer is s % kBufs
         bool ok = true;
         for (uint32_t u = first; u < units && ok; u += step) {
@@ -833,7 +835,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
                 mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrDrain, &g_fp8_error);
                 tc_fence_after();
-                const float f = own[sbuf * 2 * kScaleHalf + i * kScalePitch];
+                const float f = own[sbuf * C::kScaleBuf + i * kScalePitch];
                 const uint64_t f2 = pack2(f, f);
                 uint32_t v[kPairLd];
 #pragma unroll

@@ -473,53 +473,74 @@ __global__ void __launch_bounds__(kPlanThreads)
 // 16 bytes of a token's output for each thread, its k rows' loads in flight four at a time; the sum in
 // fp32 in the order of the choices. Reads k rows and writes one for each token: bound by memory, 8192 x 4096 with 8
 // rows each 82 us on the device, 92 us back to back (6.6 TB/s, 0.97 of the measured copy).
-template <class T>
+// A thread has U chunks of 16 bytes, a warp 32 U neighbouring ones (of one token or of two): U = 4 for one row a token,
+// 2 for two or three, 1 for more, so that at least four loads are in flight (5961 x 4560, one row a token: 22 us with
+// four chunks, 32 with one; 8192 x 4096 with two rows 33 us, 0.90 of the copy).
+template <class T, int U>
 __global__ void __launch_bounds__(256)
     moe_combine_kernel(const T* __restrict__ h, int64_t rows, uint32_t chunks, const int32_t* __restrict__ slots,
                        const float* __restrict__ w, uint64_t total, int k, T* __restrict__ y) {
-    constexpr int n = Vec16<T>::n, kAhead = 4;
-    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const uint64_t t = i / chunks;
-    const uint32_t c = (uint32_t)(i - t * chunks);
-    float acc[n];
+    constexpr int n = Vec16<T>::n, kAhead = 4 / U;
+    const uint64_t i0 = (((uint64_t)blockIdx.x * 256 + threadIdx.x) / 32) * (32 * U) + (threadIdx.x & 31);
+    float acc[U][n];
+    uint64_t at[U];     // of the token's first choice
+    uint32_t c[U];
+    bool live[U];
 #pragma unroll
-    for (int j = 0; j < n; ++j) acc[j] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += kAhead) {
-        Vec16<T> v[kAhead];
-        float wt[kAhead];
-        bool in[kAhead];
+    for (int u = 0; u < U; ++u) {
+        const uint64_t i = i0 + u * 32;
+        live[u] = i < total;
+        const uint64_t t = !live[u] ? 0 : total >> 32 ? i / chunks : (uint32_t)i / chunks;
+        c[u] = live[u] ? (uint32_t)(i - t * chunks) : 0;
+        at[u] = t * k;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int64_t d = j0 + j < k ? (int64_t)__ldg(slots + t * k + j0 + j) : -1;
-            in[j] = d >= 0 && d < rows;
-            wt[j] = in[j] ? __ldg(w + t * k + j0 + j) : 0.0f;
-            v[j].u = make_uint4(0, 0, 0, 0);
-            if (in[j]) v[j].u = __ldcs(reinterpret_cast<const uint4*>(h) + (uint64_t)d * chunks + c);
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (in[j]) {
-                float f[n];
-                to_floats(v[j], f);
-#pragma unroll
-                for (int q = 0; q < n; ++q) acc[q] = __fmaf_rn(wt[j], f[q], acc[q]);
-            }
+        for (int q = 0; q < n; ++q) acc[u][q] = 0.0f;
     }
-    Vec16<T> o;
+    for (int j0 = 0; j0 < k; j0 += kAhead) {
+        Vec16<T> v[U][kAhead];
+        float wt[U][kAhead];
+        bool in[U][kAhead];
 #pragma unroll
-    for (int q = 0; q < n; ++q) o.t[q] = from_float<T>(acc[q]);
-    reinterpret_cast<uint4*>(y)[i] = o.u;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t d = live[u] && j0 + j < k ? (int64_t)__ldg(slots + at[u] + j0 + j) : -1;
+                in[u][j] = d >= 0 && d < rows;
+                wt[u][j] = in[u][j] ? __ldg(w + at[u] + j0 + j) : 0.0f;
+                v[u][j].u = make_uint4(0, 0, 0, 0);
+                if (in[u][j]) v[u][j].u = __ldcs(reinterpret_cast<const uint4*>(h) + (uint64_t)d * chunks + c[u]);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (in[u][j]) {
+                    float f[n];
+                    to_floats(v[u][j], f);
+#pragma unroll
+                    for (int q = 0; q < n; ++q) acc[u][q] = __fmaf_rn(wt[u][j], f[q], acc[u][q]);
+                }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (live[u]) {
+            Vec16<T> o;
+#pragma unroll
+            for (int q = 0; q < n; ++q) o.t[q] = from_float<T>(acc[u][q]);
+            reinterpret_cast<uint4*>(y)[i0 + u * 32] = o.u;
+        }
 }
 
 template <class T>
 cudaError_t launch_combine(const void* h, int64_t rows, int64_t N, const int32_t* slots, const float* w, int64_t T_,
                            int k, void* y, cudaStream_t stream) {
     const uint64_t chunks = (uint64_t)N / Vec16<T>::n, total = (uint64_t)T_ * chunks;
-    const uint64_t ctas = (total + 255) / 256;
+    const int U = k == 1 ? 4 : k < 4 ? 2 : 1;
+    const uint64_t ctas = (total + 256 * U - 1) / (256 * U);
     if (chunks >= (1ULL << 32) || ctas >= (1ULL << 31)) return cudaErrorNotSupported;
-    moe_combine_kernel<T><<<(unsigned)ctas, 256, 0, stream>>>(static_cast<const T*>(h), rows, (uint32_t)chunks, slots, w,
-                                                             total, k, static_cast<T*>(y));
+    auto* kernel = U == 4 ? moe_combine_kernel<T, 4> : U == 2 ? moe_combine_kernel<T, 2> : moe_combine_kernel<T, 1>;
+    kernel<<<(unsigned)ctas, 256, 0, stream>>>(static_cast<const T*>(h), rows, (uint32_t)chunks, slots, w, total, k,
+                                               static_cast<T*>(y));
     note_launch();
     return cudaGetLastError();
 }
