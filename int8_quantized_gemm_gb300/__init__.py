@@ -699,8 +699,7 @@ def q8_quantize_fp8(x: torch.Tensor, slots=None, rows: int | None = None, q=None
     dev = x.get_device()
     top_k, to = 0, None
     if slots is not None:
-        _need(slots, torch.int32, "slots", 2)
-        top_k = slots.shape[1]
+        top_k = slots.shape[-1]
         to = _dense(slots, torch.int32, (M, top_k), dev, "slots")
         rows = M * top_k if rows is None else rows
     elif rows is not None and rows != M:
@@ -709,8 +708,9 @@ def q8_quantize_fp8(x: torch.Tensor, slots=None, rows: int | None = None, q=None
         rows = M
     q, pq = _out(q, (rows, K), _FP8, x, dev, stream, "q")
     s, ps = _out(s, (rows, -(-K // FP8_BLOCK)), torch.float32, x, dev, stream, "s")
-    _check(load().q8_quantize_fp8(x.data_ptr(), kind, M, K, ldx, to, top_k, rows, pq, ps, _handle(dev, stream)),
-           "q8_quantize_fp8")
+    status = (_lib or load()).q8_quantize_fp8(x.data_ptr(), kind, M, K, ldx, to, top_k, rows, pq, ps, _handle(dev, stream))
+    if status:
+        _check(status, "q8_quantize_fp8")
     return q, s
 
 
@@ -722,8 +722,9 @@ def q8_swiglu_quantize_fp8(h: torch.Tensor, q=None, s=None, stream=None):
     I, dev = cols // 2, h.get_device()
     q, pq = _out(q, (M, I), _FP8, h, dev, stream, "q")
     s, ps = _out(s, (M, -(-I // FP8_BLOCK)), torch.float32, h, dev, stream, "s")
-    _check(load().q8_swiglu_quantize_fp8(h.data_ptr(), kind, M, I, ldh, pq, ps, _handle(dev, stream)),
-           "q8_swiglu_quantize_fp8")
+    status = (_lib or load()).q8_swiglu_quantize_fp8(h.data_ptr(), kind, M, I, ldh, pq, ps, _handle(dev, stream))
+    if status:
+        _check(status, "q8_swiglu_quantize_fp8")
     return q, s
 
 
@@ -740,15 +741,17 @@ def q8_quantize_weight_fp8(w: torch.Tensor, qw=None, sw=None, stream=None):
     scales = (*w.shape[:-2], _cdiv(N, FP8_BLOCK), _cdiv(K, FP8_BLOCK))
     qw, pq = _out(qw, tuple(w.shape), _FP8, w, dev, stream, "qw")
     sw, ps = _out(sw, scales, torch.float32, w, dev, stream, "sw")
-    _check(load().q8_quantize_weight_fp8(w.data_ptr(), FLOAT_TYPES[w.dtype], E, N, K, pq, ps, _handle(dev, stream)),
-           "q8_quantize_weight_fp8")
+    status = (_lib or load()).q8_quantize_weight_fp8(w.data_ptr(), FLOAT_TYPES[w.dtype], E, N, K, pq, ps, _handle(dev, stream))
+    if status:
+        _check(status, "q8_quantize_weight_fp8")
     return qw, sw
 
 
 def _fp8_operands(qa, sa, qw, sw, ndim, out_dtype, out, stream):
     """Addresses and sizes of a product: (device, M, N, K, addresses of qa, sa, qw, sw and out, type, out)."""
-    _need(qa, _FP8, "qa", 2)
-    _need(qw, _FP8, "qw", ndim)
+    for t, name, dims in ((qa, "qa", 2), (qw, "qw", ndim)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not _FP8 or not t.is_cuda or t.dim() != dims or not t.is_contiguous():
+            _need(t, _FP8, name, dims)
     M, K = qa.shape
     shape = qw.shape
     N = shape[-2]
@@ -769,7 +772,9 @@ def _fp8_operands(qa, sa, qw, sw, ndim, out_dtype, out, stream):
 def q8_gemm_fp8(qa, sa, qw, sw, out_dtype=torch.bfloat16, out=None, stream=None):
     """y[m, n] = sum over blocks b of sa[m, b] sw[n / 128, b] (qa . qw over block b), as out_dtype [M, N]."""
     dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 2, out_dtype, out, stream)
-    _check(load().q8_gemm_fp8(pa, psa, pw, psw, M, N, K, py, kind, _handle(dev, stream)), "q8_gemm_fp8")
+    status = (_lib or load()).q8_gemm_fp8(pa, psa, pw, psw, M, N, K, py, kind, _handle(dev, stream))
+    if status:
+        _check(status, "q8_gemm_fp8")
     return out
 
 
@@ -778,8 +783,10 @@ def q8_gemm_fp8_grouped(qa, sa, qw, sw, offsets, out_dtype=torch.bfloat16, out=N
     expert; offsets int32 [E + 1] stay on the device. Rows of no expert are not written."""
     dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 3, out_dtype, out, stream)
     E = qw.shape[0]
-    _check(load().q8_gemm_fp8_grouped(pa, psa, pw, psw, _dense(offsets, torch.int32, (E + 1,), dev, "offsets"), M, E, N, K,
-                                      py, kind, _handle(dev, stream)), "q8_gemm_fp8_grouped")
+    status = (_lib or load()).q8_gemm_fp8_grouped(pa, psa, pw, psw, _dense(offsets, torch.int32, (E + 1,), dev, "offsets"), M, E, N, K,
+                                      py, kind, _handle(dev, stream))
+    if status:
+        _check(status, "q8_gemm_fp8_grouped")
     return out
 
 
@@ -798,22 +805,28 @@ def q8_moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=
     pb = None if bias is None else _dense(bias, torch.float32, (E,), dev, "bias")
     idx, pi = _out(idx, (T, top_k), torch.int32, logits, dev, stream, "idx")
     weights, pw = _out(weights, (T, top_k), torch.float32, logits, dev, stream, "weights")
-    _check(load().q8_moe_route(logits.data_ptr(), kind, T, E, ldl, top_k, SCORES[score], pb, n_group, topk_group,
-                               1 if renorm else 0, scale, pi, pw, _handle(dev, stream)), "q8_moe_route")
+    status = (_lib or load()).q8_moe_route(logits.data_ptr(), kind, T, E, ldl, top_k, SCORES[score], pb, n_group, topk_group,
+                               1 if renorm else 0, scale, pi, pw, _handle(dev, stream))
+    if status:
+        _check(status, "q8_moe_route")
     return idx, weights
 
 
 def q8_moe_plan(idx: torch.Tensor, n_experts: int, offsets=None, slots=None, stream=None):
     """The choices idx int32 [T, k] sorted by expert (stable): (offsets int32 [n_experts + 1], slots int32 [T, k]),
     the first row of each expert and the row of each choice (-1 where idx is outside [0, n_experts))."""
-    _need(idx, torch.int32, "idx", 2)
     if n_experts < 1:
         raise ValueError("n_experts must be positive")
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or not idx.is_cuda:
+        _need(idx, torch.int32, "idx", 2)
     T, k = idx.shape
     dev = idx.get_device()
+    pi = _dense(idx, torch.int32, (T, k), dev, "idx")
     offsets, po = _out(offsets, (n_experts + 1,), torch.int32, idx, dev, stream, "offsets")
     slots, ps = _out(slots, (T, k), torch.int32, idx, dev, stream, "slots")
-    _check(load().q8_moe_plan(idx.data_ptr(), T, k, n_experts, po, ps, _handle(dev, stream)), "q8_moe_plan")
+    status = (_lib or load()).q8_moe_plan(pi, T, k, n_experts, po, ps, _handle(dev, stream))
+    if status:
+        _check(status, "q8_moe_plan")
     return offsets, slots
 
 
@@ -823,11 +836,14 @@ def q8_moe_combine(h: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, 
     rows, N, pitch, kind = _float_rows(h, "h")
     if pitch != N:
         raise ValueError("h must be contiguous")
-    _need(slots, torch.int32, "slots", 2)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        _need(slots, torch.int32, "slots", 2)
     T, k = slots.shape
     dev = h.get_device()
     ps = _dense(slots, torch.int32, (T, k), dev, "slots")
     pw = _dense(weights, torch.float32, (T, k), dev, "weights")
     out, py = _out(out, (T, N), h.dtype, h, dev, stream, "out")
-    _check(load().q8_moe_combine(h.data_ptr(), kind, rows, N, ps, pw, T, k, py, _handle(dev, stream)), "q8_moe_combine")
+    status = (_lib or load()).q8_moe_combine(h.data_ptr(), kind, rows, N, ps, pw, T, k, py, _handle(dev, stream))
+    if status:
+        _check(status, "q8_moe_combine")
     return out
