@@ -943,16 +943,22 @@ cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* q
         // for 64 x 128 tiles of the other kernel over 152 CTAs (or fewer, larger clusters); and about six
         // blocks a tile. Measured, wide pairs / narrow pairs / other kernel, us: 100x512x16384 62 / 41 / 15; 128x8192x8192
         // 34 / 25 / 27; 517x2056x4112 25 / 17 / 27; 512x8192x8192 38 / 44 / 91; 2048x4096x4096 38 / 51 / 77; 8192
-        // rows of 64 experts, 4096x4096, 268 / 311 / 369. The estimate picks the fastest in each.
+        // rows of 64 experts, 4096x4096, 268 / 311 / 369. The estimate picks the fastest in each. Where rows of y are
+        // not whole 16-byte chunks, a pair's store takes 2.4 us more a tile by words and 5 us more by 16-bit values,
+        // which decides for few K blocks (1778x8597x416 fp16 43 / 45 / 32; 7367 rows of 72 experts, 5318x272 bf16,
+        // 126 / 159 / 95, but 5312 columns 79 / 95 / 95).
         int pairs = 0, split = 1, clusters = 0;
         double other = 0.0;
         cudaError_t e = pair_clusters<256>(pairs);
         if (e == cudaSuccess) e = swap_plan<32>(tiles(64), N, K, split, clusters, other);
         if (e != cudaSuccess) return e;
-        auto rounds = [&](int pn) {
-            return (double)(((tiles(PT) * ((N + pn - 1) / pn) + pairs - 1) / pairs) * ((K + BK - 1) / BK + 6));
+        const int64_t row_bytes = N * (t == Q8_F32 ? 4 : 2);
+        const double store = row_bytes % 16 == 0 ? 0.0 : row_bytes % 4 == 0 ? 2.4 : 5.0;   // us a wide tile
+        auto estimate = [&](int pn, double block) {
+            const int64_t rounds = (tiles(PT) * ((N + pn - 1) / pn) + pairs - 1) / pairs;
+            return (double)rounds * (block * (double)((K + BK - 1) / BK + 6) + store * pn / 256);
         };
-        const double wide = 0.47 * rounds(256), narrow = 0.30 * rounds(128);
+        const double wide = estimate(256, 0.47), narrow = estimate(128, 0.30);
         const PairArgs pa{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t};
         if (0.37 * other < wide && 0.37 * other < narrow) return launch_swap<32>(qa, qw, p, tiles(64), stream);
         if (narrow < wide) return launch_pair<128>(qa, qw, pa, tiles(PT), stream);

@@ -169,7 +169,8 @@ def check(y, qa, sa, qw, sw, dtype):
 SHAPES = [(1, 128, 128), (1, 8, 16), (1, 1, 1040), (2, 130, 144), (15, 257, 512), (16, 2056, 4112), (17, 128, 2048),
           (33, 640, 1040), (64, 256, 4096), (65, 136, 256), (128, 384, 640), (129, 264, 400), (256, 256, 1024),
           (300, 520, 528), (517, 1032, 784), (1000, 96, 2064), (2500, 1500, 400), (400, 1500, 2064),
-          (300, 200, 16), (600, 521, 128), (70, 201, 112), (2500, 1503, 272)]
+          (300, 200, 16), (600, 521, 128), (70, 201, 112), (2500, 1503, 272),
+          (2500, 1503, 4112), (2500, 1502, 4112), (517, 1030, 4112), (1400, 1031, 4112)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
