@@ -633,7 +633,7 @@ FP8_BLOCK = 128
 _FP8 = torch.float8_e4m3fn
 # A decode step makes many of these calls, so the marshalling is kept short: raw integers for the pointers,
 # the stream's handle without a Stream object, each tensor looked at once.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # None in a torch without CUDA
 
 
 def _cdiv(a: int, b: int) -> int:
