@@ -555,7 +555,8 @@ struct Pair8Cfg {
     static_assert(kSmem <= kSmemMax, "above the shared memory of one CTA");
     static constexpr uint32_t kIdesc = idesc_f16(PT, PN);
 };
-constexpr int kBand = 8;                         // token tiles that share a sweep over the weights
+constexpr int kBand = 8;                         // token tiles that share a sweep over the weights (8192x8192x16384 back
+                                                 // to back: 4 3 % slower, 32 6 %; 16 the same, and 2 % slower for experts)
 
 struct PairArgs {
     const float* sa;
