@@ -783,8 +783,9 @@ def q8_gemm_fp8_grouped(qa, sa, qw, sw, offsets, out_dtype=torch.bfloat16, out=N
     expert; offsets int32 [E + 1] stay on the device. Rows of no expert are not written."""
     dev, M, N, K, pa, psa, pw, psw, py, kind, out = _fp8_operands(qa, sa, qw, sw, 3, out_dtype, out, stream)
     E = qw.shape[0]
-    status = (_lib or load()).q8_gemm_fp8_grouped(pa, psa, pw, psw, _dense(offsets, torch.int32, (E + 1,), dev, "offsets"), M, E, N, K,
-                                      py, kind, _handle(dev, stream))
+    status = (_lib or load()).q8_gemm_fp8_grouped(pa, psa, pw, psw,
+                                                  _dense(offsets, torch.int32, (E + 1,), dev, "offsets"),
+                                                  M, E, N, K, py, kind, _handle(dev, stream))
     if status:
         _check(status, "q8_gemm_fp8_grouped")
     return out

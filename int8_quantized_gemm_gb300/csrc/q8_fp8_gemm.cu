@@ -7,11 +7,10 @@
 // drain warps read each partial sum and add it, times its scale, to fp32 registers. The MMA of the
 // next block runs meanwhile, on another of the accumulator's buffers.
 #include <cuda.h>
-#include <string.h>
 
 #include "q8_fp8.h"
-#include "q8_internal.h"
 #include "q8_fp8_ptx.cuh"
+#include "q8_internal.h"
 
 namespace q8 {
 namespace {
@@ -664,9 +663,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (sbase - sraw);
     const uint32_t bar_full = sbase + C::kOffBar;             // used in the even CTA: both CTAs' loads
-    const uint32_t bar_done = bar_full + 8 * kStages;      // both CTAs: the pair MMA's commit; the stage may
+    const uint32_t bar_done = bar_full + 8 * kStages;          // both CTAs: the pair MMA's commit; the stage may
                                                                // be filled again, its partial sums be read
-    const uint32_t bar_accempty = bar_done + 8 * kStages;  // used in the even CTA: both CTAs' drain warps
+    const uint32_t bar_accempty = bar_done + 8 * kStages;      // used in the even CTA: both CTAs' drain warps
     const uint32_t bar_scfull = bar_accempty + 8 * kBufs;
     const uint32_t bar_scempty = bar_scfull + 16;
     float* scales = reinterpret_cast<float*>(smem + C::kOffScale);   // [2 buffers][weight block][K block][row]
@@ -743,7 +742,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int kb = 0; kb < KB; ++kb, ++c) {
                     const uint32_t buf = c % kBufs;
                     const bool got =
-                        mbar_wait_cluster(bar_accempty + 8 * buf, ((c / kBufs) & 1) ^ 1, abort_flag, kErrMmaAcc, &g_fp8_error) &&
+                        mbar_wait_cluster(bar_accempty + 8 * buf, ((c / kBufs) & 1) ^ 1, abort_flag, kErrMmaAcc,
+                                          &g_fp8_error) &&
                         mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp8_error);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;

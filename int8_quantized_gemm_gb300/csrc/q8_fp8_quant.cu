@@ -82,7 +82,8 @@ enum Form : int { kDense = 0, kGated = 1, kSlots = 2 };
 // rows in order; kSlots: `wpr` warps for each row, which copies its blocks to the row's slots. kWhole:
 // K is a multiple of 128, so that block b's codes are at 128 b and its scale at b.
 // Bound by memory: 8192 x 16384 fp32 92 us on the device (98 us back to back, 6.9 TB/s); the gated form,
-// 32768 x 2048 bf16, 51 us (54 back to back; issue slots 75 % busy); 1037 x 4096 bf16 to 8 slots 10.5 us, 4.2 TB/s of mostly writes, launch and tail included.
+// 32768 x 2048 bf16, 51 us (54 back to back; issue slots 75 % busy); 1037 x 4096 bf16 to 8 slots 10.5 us, 4.2 TB/s of
+// mostly writes, launch and tail included.
 template <class T, int kForm, bool kWhole>
 __global__ void __launch_bounds__(kThreads)
     quantize_fp8_kernel(const T* __restrict__ x, uint32_t total, uint32_t KB, uint32_t K, int64_t ldx, uint32_t wpr,
