@@ -185,14 +185,15 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return r;
 }
 
-// The fp32 keys of a router with a bias, in place of the logits.
+// The fp32 keys of a router with a bias, in place of the logits. A bias of -inf or NaN masks.
 template <int VPL>
 __device__ __forceinline__ void fast_keys(float (&key)[VPL], const Place& pl, const RouteArgs& a, float m, float inv_z) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const float p = a.softmax ? fast_exp(key[i] - m) * inv_z : fast_rcp(1.0f + fast_exp(-key[i]));
         const float b = i < pl.have ? __ldg(a.bias + pl.base + i) : 0.0f;
-        key[i] = key[i] > -INFINITY ? p + b + 0.0f : -INFINITY;
+        const float k = p + b + 0.0f;
+        key[i] = key[i] > -INFINITY && k > -INFINITY ? k : -INFINITY;   // a NaN is no key: it would count as its neighbour
     }
 }
 
