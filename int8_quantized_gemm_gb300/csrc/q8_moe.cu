@@ -63,8 +63,8 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
 }
 
 // A group's score: its best key, or (sum2) the sum of its two best. Keys are floats (-inf: masked) or ordered
-// doubles (0: masked). Returns whether this lane's group is among the topk_group best; x, y: the scores
-// of the last that is and the first that is not (where there is one).
+// doubles (0: masked). Returns whether this lane's group is among the topk_group best, which are not all; x, y: the
+// scores of the last that is and the first that is not.
 template <int VPL, class K>
 __device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, K& x,
                                            K& y) {
@@ -94,13 +94,11 @@ __device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl,
         const K o = __shfl_sync(kFull, score, g * pl.lpg);
         rank += (o > score || (o == score && g < pl.group)) ? 1 : 0;
     }
-    if (a.topk_group < a.n_group) {
-        const bool counts = pl.group < a.n_group;
-        const unsigned in = __ballot_sync(kFull, counts && rank == a.topk_group - 1);
-        const unsigned out = __ballot_sync(kFull, counts && rank == a.topk_group);
-        x = __shfl_sync(kFull, score, __ffs(in) - 1);
-        y = __shfl_sync(kFull, score, __ffs(out) - 1);
-    }
+    const bool counts = pl.group < a.n_group;
+    const unsigned in = __ballot_sync(kFull, counts && rank == a.topk_group - 1);
+    const unsigned out = __ballot_sync(kFull, counts && rank == a.topk_group);
+    x = __shfl_sync(kFull, score, __ffs(in) - 1);
+    y = __shfl_sync(kFull, score, __ffs(out) - 1);
     return rank < a.topk_group;
 }
 
@@ -110,8 +108,8 @@ template <int VPL>
 __device__ __forceinline__ Doubt choose_fast(float (&key)[VPL], const Place& pl, const RouteArgs& a, bool check,
                                              float eps, float rel, int lane, int& mine) {
     Doubt doubt;
-    if (a.n_group > 1) {
-        float x = INFINITY, y = 0.0f;
+    if (a.topk_group < a.n_group) {   // else every group is kept, and there is nothing to decide or to doubt
+        float x, y;
         doubt.kept = keep_group<VPL, float>(key, pl, a, a.bias != nullptr, x, y);
         // without a bias the scores are logits, and exact
         doubt.group = a.bias != nullptr && x - y <= 2.0f * (eps + rel * fabsf(x));
@@ -252,7 +250,7 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
     for (int i = 0; i < VPL; ++i)
         key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? exact_key(pl.base + i) : 0;
     uint64_t x, y;
-    if (a.n_group > 1 && !keep_group<VPL, uint64_t>(key, pl, a, a.bias != nullptr, x, y))
+    if (a.topk_group < a.n_group && !keep_group<VPL, uint64_t>(key, pl, a, a.bias != nullptr, x, y))
 #pragma unroll
         for (int i = 0; i < VPL; ++i) key[i] = 0;
     int mine = -1;

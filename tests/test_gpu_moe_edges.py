@@ -28,3 +28,37 @@ def test_masking_bias_in_groups(q8, score, E, n_group, topk_group):
     bias[off[::2]] = math.nan
     bias[off[1::2]] = -math.inf
     check_route(q8, torch.randn((600, E), generator=g), 8, bias, score=score, n_group=n_group, topk_group=topk_group)
+
+
+def clock(call, calls=50):
+    """Microseconds a call, the smallest of three rounds."""
+    best = math.inf
+    for _ in range(3):
+        call()
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        start.record()
+        for _ in range(calls):
+            call()
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, start.elapsed_time(end) * 1e3 / calls)
+    return best
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_all_groups_kept(q8, score):
+    """Where every group is kept there is nothing to decide between groups: the same choice as without them, and not
+    every token again in 64 bits (which takes several times as long: 3 is between the two)."""
+    g = torch.Generator().manual_seed(4)
+    logits, bias = torch.randn((16384, 256), generator=g), 0.1 * torch.randn(256, generator=g)
+    check_route(q8, logits[:300], 8, bias, score=score, n_group=8, topk_group=8)
+    check_route(q8, logits[:300], 8, None, score=score, n_group=8, topk_group=8)
+    l, b = logits.cuda(), bias.cuda()
+    idx, w = q8.q8_moe_route(l, 8, score=score, bias=b)
+    out = dict(idx=torch.empty_like(idx), weights=torch.empty_like(w))
+    q8.q8_moe_route(l, 8, score=score, bias=b, n_group=8, topk_group=8, **out)
+    assert torch.equal(out["idx"], idx)
+    one = clock(lambda: q8.q8_moe_route(l, 8, score=score, bias=b, **out))
+    all_kept = clock(lambda: q8.q8_moe_route(l, 8, score=score, bias=b, n_group=8, topk_group=8, **out))
+    assert all_kept < 3.0 * one, (all_kept, one)
