@@ -63,13 +63,13 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
 }
 
 // A group's score: its best key, or (sum2) the sum of its two best. Keys are floats (-inf: masked) or ordered
-// doubles (0: masked). Returns whether this lane's group is among the topk_group best, which are not all; x, y: the
-// scores of the last that is and the first that is not.
+// doubles (0: masked). Returns whether this lane's group is among the topk_group best, its score and its two best keys.
 template <int VPL, class K>
-__device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2, K& x,
-                                           K& y) {
+__device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl, const RouteArgs& a, bool sum2,
+                                           K& score, K& m1, K& m2) {
     const K none = sizeof(K) == 4 ? (K)-INFINITY : (K)0;
-    K m1 = none, m2 = none;
+    m1 = none;
+    m2 = none;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         m2 = max(m2, min(m1, key[i]));
@@ -84,7 +84,7 @@ __device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl,
         m2 = max(min(m1, o1), max(m2, o2));
         m1 = max(m1, o1);
     }
-    K score = m1;
+    score = m1;
     if (sum2 && m2 > none) {
         if constexpr (sizeof(K) == 4) score = m1 + m2;
         else score = ordered(unordered(m1) + unordered(m2));
@@ -94,25 +94,31 @@ __device__ __forceinline__ bool keep_group(const K (&key)[VPL], const Place& pl,
         const K o = __shfl_sync(kFull, score, g * pl.lpg);
         rank += (o > score || (o == score && g < pl.group)) ? 1 : 0;
     }
-    const bool counts = pl.group < a.n_group;
-    const unsigned in = __ballot_sync(kFull, counts && rank == a.topk_group - 1);
-    const unsigned out = __ballot_sync(kFull, counts && rank == a.topk_group);
-    x = __shfl_sync(kFull, score, __ffs(in) - 1);
-    y = __shfl_sync(kFull, score, __ffs(out) - 1);
     return rank < a.topk_group;
 }
 
 // The chosen expert of lane j in `mine` (-1: none) for j < k, from a lane's keys (-inf: masked). check: report
-// decisions closer than eps + rel |key| (group sums: twice that).
+// decisions closer than eps + rel |key|, the error of two keys. A group's score is off by that of its own two, which goes
+// with their sizes and not with the size of their sum: the groups are in doubt where the lowest that the score of one
+// that is kept can be is not above the highest that another's can be.
 template <int VPL>
 __device__ __forceinline__ Doubt choose_fast(float (&key)[VPL], const Place& pl, const RouteArgs& a, bool check,
                                              float eps, float rel, int lane, int& mine) {
     Doubt doubt;
     if (a.topk_group < a.n_group) {   // else every group is kept, and there is nothing to decide or to doubt
-        float x, y;
-        doubt.kept = keep_group<VPL, float>(key, pl, a, a.bias != nullptr, x, y);
-        // without a bias the scores are logits, and exact
-        doubt.group = a.bias != nullptr && x - y <= 2.0f * (eps + rel * fabsf(x));
+        float score, m1, m2;
+        doubt.kept = keep_group<VPL, float>(key, pl, a, a.bias != nullptr, score, m1, m2);
+        if (a.bias) {   // else the scores are logits, and exact
+            const float size = fabsf(m1) + (m2 > -INFINITY ? fabsf(m2) : 0.0f);
+            const float err = eps + rel * fminf(size, kFloatMax);
+            // a sum past the largest fp32 value can be anything from there on: kept finite, it is in doubt against its like
+            const float mid = fminf(fmaxf(score, -kFloatMax), kFloatMax);
+            const bool counts = pl.group < a.n_group, live = m1 > -INFINITY;   // a group without an expert: as low as can be
+            const float lo = !counts || !doubt.kept ? INFINITY : live ? mid - err : -INFINITY;
+            const float hi = !counts || doubt.kept || !live ? -INFINITY : mid + err;
+            const float most = warp_max(hi);
+            doubt.group = most > -INFINITY && -warp_max(-lo) <= most;
+        }
     }
     uint32_t o[VPL];
 #pragma unroll
@@ -249,8 +255,8 @@ __device__ __noinline__ int route_exact(const T* row, const Place pl, const Rout
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         key[i] = i < pl.have && load_logit(row + pl.base + i) > -INFINITY ? exact_key(pl.base + i) : 0;
-    uint64_t x, y;
-    if (a.topk_group < a.n_group && !keep_group<VPL, uint64_t>(key, pl, a, a.bias != nullptr, x, y))
+    uint64_t score, m1, m2;
+    if (a.topk_group < a.n_group && !keep_group<VPL, uint64_t>(key, pl, a, a.bias != nullptr, score, m1, m2))
 #pragma unroll
         for (int i = 0; i < VPL; ++i) key[i] = 0;
     int mine = -1;

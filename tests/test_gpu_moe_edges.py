@@ -62,3 +62,26 @@ def test_all_groups_kept(q8, score):
     one = clock(lambda: q8.q8_moe_route(l, 8, score=score, bias=b, **out))
     all_kept = clock(lambda: q8.q8_moe_route(l, 8, score=score, bias=b, n_group=8, topk_group=8, **out))
     assert all_kept < 3.0 * one, (all_kept, one)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [1e3, 1e4, 1e5, 1e7])
+def test_groups_whose_biases_cancel(q8, score, size):
+    """Two experts a group with biases of opposite sign: the group's score is small, the rounding of its terms is not."""
+    g = torch.Generator().manual_seed(int(size))
+    E = 16
+    bias = size * (1.0 + torch.rand(E // 2, generator=g)).repeat_interleave(2)
+    bias[1::2] *= -1.0
+    check_route(q8, torch.randn((3000, E), generator=g), 4, bias, score=score, n_group=8, topk_group=4)
+
+
+def test_group_scores_past_the_largest_fp32(q8):
+    """Sums of two keys that only 64 bits tell apart; and whole groups that a very low bias puts last."""
+    logits = torch.randn((40, 32), generator=torch.Generator().manual_seed(3))
+    bias = torch.linspace(2.0e38, 3.3e38, 8).repeat_interleave(4)
+    check_route(q8, logits, 4, bias, score="sigmoid", n_group=8, topk_group=3)
+    check_route(q8, logits, 4, -bias, score="sigmoid", n_group=8, topk_group=3)
+    bias = torch.zeros(32)
+    bias[8:16] = torch.finfo(torch.float32).min
+    check_route(q8, logits, 8, bias, score="softmax", n_group=8, topk_group=6)
+    check_route(q8, logits, 8, bias, score="softmax", n_group=8, topk_group=7)
