@@ -637,7 +637,8 @@ q8_status q8_gemm_fp8_grouped(const uint8_t* qa, const float* sa, const uint8_t*
  *  - n_group > 1: the experts form n_group groups of E / n_group neighbours, and only those of the
  *    topk_group best groups can be chosen. A group is ranked by its best expert, or, with a bias, by the sum
  *    of its two best.
- *  - weights = p of the chosen, divided by their sum if renorm (0 where that is 0), times scale.
+ *  - weights = p of the chosen, divided by their sum if renorm (0 where that is 0), times scale. These p are fp32
+ *    values: one below 2^-126 has fewer bits, one below 2^-150 is 0.
  *  - An expert whose logit is -inf or NaN is masked: its score is 0 and it is never chosen. A token
  *    that has too few experts left gets idx -1 and weight 0 in the places that remain. A logit of +inf
  *    counts as the largest fp32 value. A bias of -inf or NaN masks its expert for every token.

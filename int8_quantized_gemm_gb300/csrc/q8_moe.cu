@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(128) moe_route_kernel(RouteArgs a) {
     float p = 0.0f;
     if (mine >= 0) {
         const float l = load_logit(row + mine);
-        p = a.softmax ? expf(l - m) * inv_z : __fdiv_rn(1.0f, 1.0f + expf(-l));
+        // sigmoid: from exp(-|l|), which is at most 1; exp(-l) is past fp32's range for l < -88.7, the score is not
+        const float t = expf(a.softmax ? l - m : -fabsf(l));
+        p = a.softmax ? t * inv_z : __fdiv_rn(l < 0.0f ? t : 1.0f, 1.0f + t);
     }
     if (a.renorm) {
         float sum = p;

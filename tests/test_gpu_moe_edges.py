@@ -85,3 +85,20 @@ def test_group_scores_past_the_largest_fp32(q8):
     bias[8:16] = torch.finfo(torch.float32).min
     check_route(q8, logits, 8, bias, score="softmax", n_group=8, topk_group=6)
     check_route(q8, logits, 8, bias, score="softmax", n_group=8, topk_group=7)
+
+
+def test_sigmoid_of_very_low_logits(q8):
+    """Scores down to fp32's subnormals. Of each: the exponential (2 steps, of 2^-149 where it is subnormal), a sum, a
+    division, half a step each; renormalised, the same again of the sum, and the last division."""
+    g = torch.Generator().manual_seed(6)
+    logits = -86.0 - 8.0 * torch.rand((200, 8), generator=g)
+    want_idx, want = ref.route(logits, 6, "sigmoid", renorm=False)
+    idx, w = q8.q8_moe_route(logits.cuda(), 6, score="sigmoid", renorm=False)
+    off = 4 * 2.0 ** -23 * want + 3 * 2.0 ** -149
+    assert torch.equal(idx.cpu(), want_idx)
+    assert ((w.cpu().double() - want).abs() <= off).all()
+    idx, w = q8.q8_moe_route(logits.cuda(), 6, score="sigmoid")
+    rel = off / want + (off.sum(1) / want.sum(1))[:, None] + 8 * 2.0 ** -24
+    share = want / want.sum(1, keepdim=True)
+    assert torch.equal(idx.cpu(), want_idx)
+    assert ((w.cpu().double() - share).abs() <= share * rel * (1 + 2.0 ** -6)).all()
