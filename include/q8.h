@@ -592,7 +592,8 @@ q8_status q8_quantize_fp8(const void* x, q8_float_type type, int64_t M, int64_t 
 /*
  * Gated activation and quantization in one pass, between the two products of a gated layer:
  *   x[m, i] = h[m, I + i] * g / (1 + exp(-g)),  g = h[m, i],   then q and s of x as q8_quantize_fp8.
- * The activation is computed in fp32, off by a few units of its last place.
+ * The activation is computed in fp32, off by less than 2^-20 of its value; where exp(-|g|) is not a normal fp32 number
+ * (|g| > 87.3), by up to 2^-148 |g h[m, I + i]| more.
  * h    : [M, 2 I] of `type` (gates, then the values they gate), rows ldh elements apart. I % 16 == 0.
  * q, s : [M, I] and [M, ceil(I / 128)], written. Errors as q8_quantize_fp8.
  */

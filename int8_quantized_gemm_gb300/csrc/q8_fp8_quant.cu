@@ -46,25 +46,40 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 
-// Two of u * g / (1 + exp(-g)), exp(-g) = 2^(-g log2 e). The fast exponential and reciprocal are off by a few 2^-22
-// relative for g > -20 (a thousandth of an e4m3 step); below, the value is under 5e-8 |u|. For exp(-g)
-// above 2^126 the reciprocal gives 0, its limit.
+// Two of u * g / (1 + exp(-g)) for |g| <= kGateFast. exp(-g) = 2^h e^-d with h = fl(-g log2 e) and d = g + h ln 2, which is
+// under 2^-16, so that e^-d is 1 - d: without d the rounding of h would cost |g| half steps. Off by less than
+// 2^-20 of the value: the fast exponential 2^-22, ln 2 in 24 bits times h 2^-22, 1 - d and the sum half a step each
+// (2^-24), the fast reciprocal 2^-23, two products half a step each. (32768 x 2048 bf16: 53.7 us without d, 56.0 with it,
+// 67.6 with fp32's own exponential for every gate.)
+constexpr float kGateFast = 87.0f;   // the exponential and its reciprocal are normal numbers
 __device__ __forceinline__ void silu_mul2(float& g0, float& g1, float u0, float u1) {
-    const uint64_t g = pack2(g0, g1);
+    const uint64_t g = pack2(g0, g1), one = pack2(1.0f, 1.0f);
+    const uint64_t h = mul2(g, pack2(-1.4426950408889634f, -1.4426950408889634f));
+    const uint64_t d = fma2(h, pack2(0.6931471805599453f, 0.6931471805599453f), g);
     float e0, e1, r0, r1;
-    unpack2(mul2(g, pack2(-1.4426950408889634f, -1.4426950408889634f)), e0, e1);
+    unpack2(h, e0, e1);
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e0) : "f"(e0));
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e1) : "f"(e1));
-    unpack2(add2(pack2(e0, e1), pack2(1.0f, 1.0f)), e0, e1);
+    unpack2(fma2(pack2(e0, e1), fma2(d, pack2(-1.0f, -1.0f), one), one), e0, e1);
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r0) : "f"(e0));
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r1) : "f"(e1));
     unpack2(mul2(mul2(g, pack2(r0, r1)), pack2(u0, u1)), g0, g1);
+}
+
+// The same for any gate, from t = exp(-|g|), so that nothing overflows before the value does and the tail of a closed gate
+// keeps its bits: u g / (1 + t) for g >= 0, u g t / (1 + t) below (the reciprocal is of a number between 1 and 2). Where t
+// is subnormal (|g| > 87.3) two of its steps, 2^-148 |g u|, come on top.
+__device__ __forceinline__ float silu_mul_far(float g, float u) {
+    const float t = expf(-fabsf(g));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.0f + t));
+    return (g < 0.0f ? g * t : g) * r * u;
 }
 
 // max(m, |a|, |b|), NaN if one is (its bits are then above those of inf).
@@ -82,10 +97,10 @@ enum Form : int { kDense = 0, kGated = 1, kSlots = 2 };
 // rows in order; kSlots: `wpr` warps for each row, which copies its blocks to the row's slots. kWhole:
 // K is a multiple of 128, so that block b's codes are at 128 b and its scale at b.
 // Bound by memory: 8192 x 16384 fp32 92 us on the device (98 us back to back, 6.9 TB/s); the gated form,
-// 32768 x 2048 bf16, 51 us (54 back to back; issue slots 75 % busy); 1037 x 4096 bf16 to 8 slots 10.5 us, 4.2 TB/s of
+// 32768 x 2048 bf16, 56 us back to back (issue slots); 1037 x 4096 bf16 to 8 slots 10.5 us, 4.2 TB/s of
 // mostly writes, launch and tail included.
 template <class T, int kForm, bool kWhole>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kForm == kGated ? 6 : 1)   // gated: 40 registers instead of 48, 56.0 us for 57.6
     quantize_fp8_kernel(const T* __restrict__ x, uint32_t total, uint32_t KB, uint32_t K, int64_t ldx, uint32_t wpr,
                         const int32_t* __restrict__ slots, int top_k, int64_t rows_out, uint8_t* __restrict__ q,
                         float* __restrict__ s) {
@@ -145,10 +160,17 @@ __global__ void __launch_bounds__(kThreads)
         float most = 0.0f;
         to_floats(v[i], f[i]);
         if constexpr (kForm == kGated) {
-            float by[n];
+            float by[n], far = 0.0f;
             to_floats(up[i], by);
 #pragma unroll
-            for (int j = 0; j < n; j += 2) silu_mul2(f[i][j], f[i][j + 1], by[j], by[j + 1]);
+            for (int j = 0; j < n; j += 2) far = max_abs(far, f[i][j], f[i][j + 1]);
+            if (far <= kGateFast) {
+#pragma unroll
+                for (int j = 0; j < n; j += 2) silu_mul2(f[i][j], f[i][j + 1], by[j], by[j + 1]);
+            } else {   // some gate of the lane's is far out, infinite or NaN: rare
+#pragma unroll
+                for (int j = 0; j < n; ++j) f[i][j] = silu_mul_far(f[i][j], by[j]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < n; j += 2) most = max_abs(most, f[i][j], f[i][j + 1]);
