@@ -580,7 +580,8 @@ typedef enum q8_score { Q8_SOFTMAX = 0, Q8_SIGMOID = 1 } q8_score;
  * slots : NULL, or int32 [M, top_k]: row m is written to the rows slots[m, j] of q and s instead of row
  *         m (the tokens of a routed layer, in expert order; q8_moe_plan). Slots outside
  *         [0, rows_out) are skipped. The valid ones have to differ.
- * top_k, rows_out : the slots of a row (1..32) and the rows of q and s; 0 and M when slots is NULL.
+ * top_k, rows_out : the slots of a row (1..32) and the rows of q and s; 0 and M when slots is NULL. With
+ *         M = 0 slots may be NULL whatever these are, and nothing is written.
  * q, s  : e4m3 codes [rows_out, K] and fp32 scales [rows_out, KB], written.
  * Errors: Q8_ERR_UNSUPPORTED for K % 16 != 0, a row pitch that is not a multiple of 16 bytes, more than
  * 32 slots a row, sizes of 2^31 and more, or 2^31 and more blocks.

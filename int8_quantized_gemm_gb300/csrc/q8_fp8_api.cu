@@ -62,8 +62,8 @@ q8_status q8_quantize_fp8(const void* x, q8_float_type type, int64_t M, int64_t 
                           int64_t top_k, int64_t rows_out, uint8_t* q, float* s, q8_stream_t stream) {
     q8_status st = check_rows(x, type, M, K, K, ldx, q, s);
     if (st != Q8_OK) return st;
-    if (slots) {
-        if (top_k < 1 || rows_out < 0 || !aligned(slots, 4)) return Q8_ERR_INVALID_ARG;
+    if (slots || M == 0) {   // the slots of no row may have no address
+        if (top_k < (slots ? 1 : 0) || rows_out < 0 || !aligned(slots, 4)) return Q8_ERR_INVALID_ARG;
         if (top_k > q8::kMaxTopK || !in_range(rows_out)) return Q8_ERR_UNSUPPORTED;
     } else if (top_k != 0 || rows_out != M) {
         return Q8_ERR_INVALID_ARG;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from . import fp8_reference as ref
-from .test_gpu_moe import check_route
+from .test_gpu_moe import check_route, layer
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +102,15 @@ def test_sigmoid_of_very_low_logits(q8):
     share = want / want.sum(1, keepdim=True)
     assert torch.equal(idx.cpu(), want_idx)
     assert ((w.cpu().double() - share).abs() <= share * rel * (1 + 2.0 ** -6)).all()
+
+
+def test_layer_of_no_token(q8):
+    """Every step of a routed layer with zero tokens: empty results, no error."""
+    E, k, H, I = 8, 4, 256, 128
+    w13 = q8.q8_quantize_weight_fp8(torch.randn((E, 2 * I, H), device="cuda"))
+    w2 = q8.q8_quantize_weight_fp8(torch.randn((E, H, I), device="cuda"))
+    x = torch.empty((0, H), dtype=torch.bfloat16, device="cuda")
+    y, idx, w = layer(q8, x, torch.empty((0, E), device="cuda"), None, w13, w2, k, E)
+    assert y.shape == (0, H) and idx.shape == (0, k) and w.shape == (0, k)
+    q, s = q8.q8_quantize_fp8(x, slots=torch.empty((0, k), dtype=torch.int32, device="cuda"), rows=3)
+    assert q.shape == (3, H) and s.shape == (3, 2)
