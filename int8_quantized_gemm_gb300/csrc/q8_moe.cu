@@ -565,9 +565,9 @@ cudaError_t launch_moe_route(const RouteArgs& a, q8_float_type t, cudaStream_t s
 cudaError_t launch_moe_plan(const int32_t* idx, int64_t n, int E, int32_t* offsets, int32_t* slots,
                             cudaStream_t stream) {
     const size_t smem = (size_t)(kPlanWarps + 1) * E * 4;
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) {   // the limit is the device's, so always the same: another thread may be about to launch
+        const cudaError_t e = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (kPlanWarps + 1) * kMaxExperts * 4);
         if (e != cudaSuccess) return e;
     }
     // A CTA for each 2048 entries, up to the portable cluster of 8.

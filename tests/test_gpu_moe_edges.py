@@ -1,5 +1,6 @@
 """Router, plan and layer at the edges of their definition, against plain forms in 64 bits."""
 import math
+import threading
 
 import pytest
 import torch
@@ -114,3 +115,29 @@ def test_layer_of_no_token(q8):
     assert y.shape == (0, H) and idx.shape == (0, k) and w.shape == (0, k)
     q, s = q8.q8_quantize_fp8(x, slots=torch.empty((0, k), dtype=torch.int32, device="cuda"), rows=3)
     assert q.shape == (3, H) and s.shape == (3, 2)
+
+
+def test_plans_of_two_sizes_from_two_threads(q8):
+    """The launch's shared memory limit is the same whatever the number of experts, so that one thread's call does not
+    take the room from another's. The library is called without the binding, so that the calls overlap."""
+    lib, wrong = q8.load(), []
+
+    def work(E):
+        idx = torch.randint(0, E, (8, 4), generator=torch.Generator().manual_seed(E)).to(torch.int32)
+        want_o, want_s = ref.plan(idx, E)
+        mine, stream = idx.cuda(), torch.cuda.Stream()
+        offsets = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+        slots = torch.empty((8, 4), dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        args = (mine.data_ptr(), 8, 4, E, offsets.data_ptr(), slots.data_ptr(), stream.cuda_stream)
+        status = [lib.q8_moe_plan(*args) for _ in range(20000)]
+        stream.synchronize()
+        if any(status) or not torch.equal(offsets.cpu(), want_o) or not torch.equal(slots.cpu(), want_s):
+            wrong.append((E, sum(s != 0 for s in status)))
+
+    threads = [threading.Thread(target=work, args=(E,)) for E in (380, 512, 400, 511)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
