@@ -614,7 +614,7 @@ q8_status q8_quantize_weight_fp8(const void* w, q8_float_type type, int64_t E, i
  * The inner sums are the tensor core's, in fp32; the sum over blocks is one fp32 multiply-add a block;
  * y is rounded once, to `type`. The order of every sum depends on the sizes alone, so that the same
  * call gives the same bits. y : [M, N], dense. K = 0 gives zeros.
- * Errors: Q8_ERR_UNSUPPORTED for K % 16 != 0 or sizes of 2^31 and more.
+ * Errors: Q8_ERR_UNSUPPORTED for K % 16 != 0, M and N from 2^31 - 1024 on, or K from 2^31 - 128 on.
  */
 q8_status q8_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw, int64_t M, int64_t N,
                       int64_t K, void* y, q8_float_type type, q8_stream_t stream);
@@ -625,7 +625,8 @@ q8_status q8_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, con
  * device (no synchronisation; the call can be captured in a graph); an expert may have no row.
  * offsets : int32 [E + 1], not falling, offsets[0] >= 0. Values past `rows` are cut to it; rows before
  *           offsets[0] or from offsets[E] on are not written. Overlapping ranges are not defined.
- * rows    : the rows of qa, sa and y. E <= 512, K >= 16 (else Q8_ERR_UNSUPPORTED).
+ * rows    : the rows of qa, sa and y. E <= 512, K >= 16 (else Q8_ERR_UNSUPPORTED). Limits of M, N and K above hold for
+ *           rows, E N and K.
  */
 q8_status q8_gemm_fp8_grouped(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
                               const int32_t* offsets, int64_t rows, int64_t E, int64_t N, int64_t K, void* y,

@@ -38,8 +38,10 @@ q8_status check_rows(const void* x, q8_float_type t, int64_t M, int64_t cols, in
 q8_status gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw, const int32_t* offsets,
                    int64_t rows, int64_t E, int64_t N, int64_t K, void* y, q8_float_type t, q8_stream_t stream) {
     if (rows < 0 || E < 0 || N < 0 || K < 0 || !valid_type(t)) return Q8_ERR_INVALID_ARG;
-    if (K % 16 != 0 || !in_range(rows) || !in_range(K) || E > q8::kMaxExperts) return Q8_ERR_UNSUPPORTED;
-    // TMA coordinates of the weight rows, and of a tile that ends past them, are 32-bit
+    if (K % 16 != 0 || E > q8::kMaxExperts) return Q8_ERR_UNSUPPORTED;
+    // The kernels count rows and K in 32 bits, and so are TMA's coordinates: the end of a tile that begins inside has to
+    // be a number too (rows of a tile up to 256, and as many again of the tokens; 128 K of a block).
+    if (rows > INT32_MAX - 1024 || K > INT32_MAX - q8::kFp8Block) return Q8_ERR_UNSUPPORTED;
     if (!in_range(N) || (E > 0 && N > (INT32_MAX - 1024) / E)) return Q8_ERR_UNSUPPORTED;
     if (rows == 0 || N == 0 || E == 0) return Q8_OK;
     if (!y || !aligned(y, 16)) return Q8_ERR_INVALID_ARG;

@@ -2,7 +2,7 @@
 runs before any CUDA call, so these need no GPU (the pointers are never read)."""
 import pytest
 
-from .test_fp8_abi import FAKE, OK, INVALID, QUANT, UNSUPPORTED, call, lib  # noqa: F401  (lib is the fixture)
+from .test_fp8_abi import FAKE, GEMM, GROUPED, INVALID, OK, QUANT, UNSUPPORTED, call, lib  # noqa: F401  (lib is the fixture)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -18,4 +18,20 @@ from .test_fp8_abi import FAKE, OK, INVALID, QUANT, UNSUPPORTED, call, lib  # no
 def test_no_rows_to_quantize_into_slots(lib, change, status):  # noqa: F811
     before = lib.q8_launch_count()
     assert call(lib, "q8_quantize_fp8", QUANT, M=0, x=None, q=None, s=None, **change) == status
+    assert lib.q8_launch_count() == before
+
+
+@pytest.mark.parametrize("name,defaults,change", [
+    ("q8_gemm_fp8", GEMM, dict(K=(1 << 31) - 16)),            # the block after the last would end past 2^31
+    ("q8_gemm_fp8", GEMM, dict(K=(1 << 31) - 112)),
+    ("q8_gemm_fp8", GEMM, dict(M=(1 << 31) - 1)),             # and so would the rows of a tile
+    ("q8_gemm_fp8", GEMM, dict(M=(1 << 31) - 200)),
+    ("q8_gemm_fp8", GEMM, dict(N=(1 << 31) - 1)),
+    ("q8_gemm_fp8_grouped", GROUPED, dict(K=(1 << 31) - 112)),
+    ("q8_gemm_fp8_grouped", GROUPED, dict(rows=(1 << 31) - 16)),
+    ("q8_gemm_fp8_grouped", GROUPED, dict(E=2, N=(1 << 30) - 8)),
+])
+def test_products_next_to_32_bits_are_refused(lib, name, defaults, change):  # noqa: F811
+    before = lib.q8_launch_count()
+    assert call(lib, name, defaults, **change) == UNSUPPORTED
     assert lib.q8_launch_count() == before
