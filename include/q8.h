@@ -624,7 +624,8 @@ q8_status q8_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw, con
  * expert e and use qw[e], sw[e] of qw[E, N, K], sw[E, ceil(N / 128), KB]. The offsets are read on the
  * device (no synchronisation; the call can be captured in a graph); an expert may have no row.
  * offsets : int32 [E + 1], not falling, offsets[0] >= 0. Values past `rows` are cut to it; rows before
- *           offsets[0] or from offsets[E] on are not written. Overlapping ranges are not defined.
+ *           offsets[0] or from offsets[E] on are not written. Where offsets fall, ranges overlap and their rows
+ *           are not defined; the call does no more work than disjoint ranges take.
  * rows    : the rows of qa, sa and y. E <= 512, K >= 16 (else Q8_ERR_UNSUPPORTED). Limits of M, N and K above hold for
  *           rows, E N and K.
  */

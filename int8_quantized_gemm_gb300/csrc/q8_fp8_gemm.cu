@@ -64,10 +64,13 @@ struct SwapArgs {
     int split;                // CTAs of a cluster, sharing a tile's K blocks
     void* y;
     q8_float_type type;
+    uint32_t most;            // units there can be
 };
 
 // Token tiles before each group, and the rows of a group, from the offsets. Ranges are cut to
-// [0, rows], so that no offset, whatever its value, leads outside of qa and y.
+// [0, rows], so that no offset, whatever its value, leads outside of qa and y. Offsets that fall make ranges overlap, and
+// up to E times the tiles that disjoint ranges have: `units` cuts the work to what those can have, which the host has
+// checked to be below 2^31 (so that no unit's number wraps and no kernel runs for the sum of all overlaps).
 struct Groups {
     const int32_t* offsets;
     const int* cum;   // shared: tiles before group e
@@ -94,6 +97,11 @@ struct Groups {
         range(e, lo, hi);
         row = lo + (t - cum[e]) * tn;
         n = min(tn, hi - row);
+    }
+    // tiles (token tiles times the NT weight tiles) to work on
+    __device__ __forceinline__ uint32_t units(int NT, uint32_t most) const {
+        const uint64_t all = (uint64_t)(uint32_t)cum[E] * (uint32_t)NT;
+        return all < most ? (uint32_t)all : most;
     }
     // one warp: the prefix sums
     __device__ __forceinline__ void scan(int* out, int lane) const {
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const uint32_t units = (uint32_t)cum[p.E] * NT;
+    const uint32_t units = groups.units(NT, p.most);
 
     if (warp == 0) {
         // ---------------------------------------------------------------------------- TMA
@@ -487,6 +495,7 @@ cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_
     double cost = 0.0;
     cudaError_t e = swap_plan<CW>(tiles, p.N, p.K, p.split, clusters, cost);
     if (e != cudaSuccess) return e;
+    p.most = (uint32_t)(tiles * ((p.N + TW - 1) / TW));
     const int reduce = p.split > 1 ? C::reduce_bytes(p.split) : 0;
     const int room = kSmemMax - 1024 - kTailBytes - C::kScale - reduce;
     p.stages = room / C::kStage < kMaxStages ? room / C::kStage : kMaxStages;
@@ -564,6 +573,7 @@ struct PairArgs {
     int rows, E, N, K;
     void* y;
     q8_float_type type;
+    uint32_t most;   // units there can be
 };
 
 // Units in bands of kBand token tiles, the weight tiles swept inside a band, so that the tiles that run
@@ -701,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     const int NT = (p.N + PN - 1) / PN, KB = (p.K + BK - 1) / BK;
     const int tiles = cum[p.E];
-    const uint32_t units = (uint32_t)tiles * NT, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const uint32_t units = groups.units(NT, p.most), first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPairRegsLow));
@@ -916,7 +926,7 @@ cudaError_t pair_clusters(int& clusters) {
 }
 
 template <int PN>
-cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, const PairArgs& p, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, PairArgs p, int64_t tiles, cudaStream_t stream) {
     using C = Pair8Cfg<PN>;
     int clusters = 0;
     const cudaError_t e = pair_clusters<PN>(clusters);
@@ -927,6 +937,7 @@ cudaError_t launch_pair(const uint8_t* qa, const uint8_t* qw, const PairArgs& p,
         return cudaErrorInvalidValue;
     const int64_t units = tiles * ((p.N + PN - 1) / PN);
     if (units < clusters) clusters = (int)units;
+    p.most = (uint32_t)units;
     gemm_fp8_pair_kernel<PN><<<2 * clusters, kPairThreads, C::kSmem, stream>>>(ma, mw, p);
     note_launch();
     return cudaGetLastError();
@@ -942,7 +953,7 @@ cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* q
     auto tiles = [&](int tn) { return offsets ? rows / tn + (E < rows ? E : rows) : (rows + tn - 1) / tn; };
     // The kernels count tiles in 32 bits, whatever the offsets are (each group at most all rows).
     if (tiles(16) * NT >= (1LL << 31) - 1024 || (rows / 16 + 1) * E >= (1LL << 31)) return cudaErrorNotSupported;
-    const SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, 0, 1, y, t};
+    const SwapArgs p{sa, sw, offsets, (int)rows, E, (int)N, (int)K, 0, 1, y, t, 0};
     if (per > 64) {
         // What a round of tiles costs a K block: 0.47 us for 256 x 256 tiles over 76 pairs, 0.30 us for 256 x 128, 0.37 us
         // for 64 x 128 tiles of the other kernel over 152 CTAs (or fewer, larger clusters); and about six
@@ -964,7 +975,7 @@ cudaError_t launch_gemm_fp8(const uint8_t* qa, const float* sa, const uint8_t* q
             return (double)rounds * (block * (double)((K + BK - 1) / BK + 6) + store * pn / 256);
         };
         const double wide = estimate(256, 0.47), narrow = estimate(128, 0.30);
-        const PairArgs pa{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t};
+        const PairArgs pa{sa, sw, offsets, (int)rows, E, (int)N, (int)K, y, t, 0};
         if (0.37 * other < wide && 0.37 * other < narrow) return launch_swap<32>(qa, qw, p, tiles(64), stream);
         if (narrow < wide) return launch_pair<128>(qa, qw, pa, tiles(PT), stream);
         return launch_pair<256>(qa, qw, pa, tiles(PT), stream);
