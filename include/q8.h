@@ -685,10 +685,12 @@ const char* q8_status_string(q8_status status);
  * gave up: one byte per kernel family (bits 0..7: the single-CTA tcgen05 kernel,
  * and bit 7 the fused RMSNorm quantizer's wait for a row copy; bits 8..15: the
  * tcgen05 decode kernel; bits 16..23: the warp-MMA decode kernels; bits 24..31:
- * the CTA-pair kernel and the float8 products), within a byte one bit per role (1 TMA producer,
+ * the CTA-pair kernel and the float8 products, bit 31 set where a float8 product is among
+ * them), within a byte one bit per role (1 TMA producer,
  * 2 converters / compute warps waiting for loaded data, 4 converters waiting
  * for a free stage, 8 MMA issuer waiting for converted data, 16 MMA issuer
- * waiting for a free accumulator, 32 accumulator drain, 64 the odd CTA's relay).
+ * waiting for a free accumulator, 32 accumulator drain, 64 the odd CTA's relay;
+ * of a float8 product 4 its scale warps, 64 the exchange of a cluster's partial sums).
  * Synchronises the device. Reading it resets it to 0. A nonzero value means the
  * outputs of the kernel that set it are invalid.
  */

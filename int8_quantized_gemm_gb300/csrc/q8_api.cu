@@ -542,7 +542,7 @@ q8_status q8_device_error(uint32_t* code_out) {
     if (e == cudaSuccess) e = q8::read_and_clear_quant_error(&qz);
     if (e == cudaSuccess) e = q8::read_and_clear_gemm_fp8_error(&f8);
     if (e != cudaSuccess) return Q8_ERR_CUDA;
-    *code_out = (a | qz) | (b << 8) | (c << 16) | ((d | f8) << 24);
+    *code_out = q8::device_error_code(a, qz, b, c, d, f8);
     return *code_out ? Q8_ERR_TIMEOUT : Q8_OK;
 }
 

@@ -153,4 +153,12 @@ cudaError_t read_and_clear_gemv_mma_error(uint32_t* code);
 cudaError_t read_and_clear_gemm_tc2_error(uint32_t* code);
 cudaError_t read_and_clear_quant_error(uint32_t* code);
 
+// The code that q8_device_error reports, from the error words of the single-CTA tcgen05 kernel, the quantizers, the two
+// decode kernels, the CTA-pair kernel and the float8 products. The last two share a byte of role bits; its highest bit
+// says that a float8 product is among those that gave up.
+inline uint32_t device_error_code(uint32_t tc, uint32_t quant, uint32_t gemv_tc, uint32_t gemv_mma, uint32_t tc2,
+                                  uint32_t fp8) {
+    return tc | quant | gemv_tc << 8 | gemv_mma << 16 | (tc2 | fp8 | (fp8 ? 0x80u : 0u)) << 24;
+}
+
 }  // namespace q8
