@@ -79,3 +79,54 @@ def test_grouped_overlapping_ranges_end(q8, rows, N, K):
         want, mag = ref.product(qa[at], sa[at], qw[e], sw[e])
         assert ((y[at].cpu().double() - want).abs() <= ref.product_tolerance(want, mag, K, torch.float32)).all()
     assert q8.q8_device_error() == 0
+
+
+# ------------------------------------------------------------------------------- results, slots
+
+def pool_stream(t):
+    """The stream whose memory pool of PyTorch's allocator the tensor lies in."""
+    for segment in torch.cuda.memory_snapshot():
+        if segment["address"] <= t.data_ptr() < segment["address"] + segment["total_size"]:
+            return segment["stream"]
+    raise AssertionError("not memory of the allocator")
+
+
+def test_results_are_allocated_for_the_stream_that_writes_them(q8):
+    """A result's memory comes from the pool of the call's stream: from another's, it could be handed out again to work that
+    is not ordered after the call."""
+    def calls(stream):
+        x = torch.randn((40, 256), device="cuda").to(torch.bfloat16)
+        logits = torch.randn((40, 8), device="cuda")
+        w = torch.randn((8, 256, 256), device="cuda")
+        torch.cuda.synchronize()
+        kept = [x, logits, w]
+        idx, weights = q8.q8_moe_route(logits, 2, stream=stream)
+        offsets, slots = q8.q8_moe_plan(idx, 8, stream=stream)
+        qw, sw = q8.q8_quantize_weight_fp8(w, stream=stream)
+        qa, sa = q8.q8_quantize_fp8(x, slots=slots, stream=stream)
+        qd, sd = q8.q8_quantize_fp8(x, stream=stream)
+        h = q8.q8_gemm_fp8_grouped(qa, sa, qw, sw, offsets, stream=stream)
+        y = q8.q8_gemm_fp8(qd, sd, qw[0], sw[0], stream=stream)
+        qh, sh = q8.q8_swiglu_quantize_fp8(h, stream=stream)
+        out = q8.q8_moe_combine(h, slots, weights, stream=stream)
+        torch.cuda.synchronize()
+        return kept, (idx, weights, offsets, slots, qw, sw, qa, sa, qd, sd, h, y, qh, sh, out)
+
+    side = torch.cuda.Stream()
+    kept, results = calls(side)
+    assert {pool_stream(t) for t in results} == {side.cuda_stream}
+    assert side.cuda_stream not in {pool_stream(t) for t in kept}
+    kept, results = calls(None)
+    assert {pool_stream(t) for t in results} == {pool_stream(kept[0])} != {side.cuda_stream}
+
+
+@pytest.mark.parametrize("M,K,k", [(1, 16, 32), (9, 400, 3), (70, 2064, 8)])
+def test_quantize_fp16_to_slots(q8, M, K, k):
+    """Every slot of a row holds the row's codes and scales, bit for bit."""
+    x = ref.tokens(M, K, seed=M).to(torch.float16)
+    slots = torch.randperm(M * k, generator=torch.Generator().manual_seed(M)).to(torch.int32).view(M, k)
+    q, s = q8.q8_quantize_fp8(x.cuda(), slots=slots.cuda())
+    wq, ws = ref.quantize(x.float())
+    for j in range(k):
+        at = slots[:, j].long()
+        assert torch.equal(q.view(torch.uint8).cpu()[at], wq.view(torch.uint8)) and torch.equal(s.cpu()[at], ws)
