@@ -699,7 +699,9 @@ def q8_quantize_fp8(x: torch.Tensor, slots=None, rows: int | None = None, q=None
     dev = x.get_device()
     top_k, to = 0, None
     if slots is not None:
-        top_k = slots.shape[-1]
+        if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+            _need(slots, torch.int32, "slots", 2)
+        top_k = slots.shape[1]
         to = _dense(slots, torch.int32, (M, top_k), dev, "slots")
         rows = M * top_k if rows is None else rows
     elif rows is not None and rows != M:

@@ -130,3 +130,12 @@ def test_quantize_fp16_to_slots(q8, M, K, k):
     for j in range(k):
         at = slots[:, j].long()
         assert torch.equal(q.view(torch.uint8).cpu()[at], wq.view(torch.uint8)) and torch.equal(s.cpu()[at], ws)
+
+
+def test_slots_that_are_no_matrix_of_indices(q8):
+    x = torch.zeros((4, 128), device="cuda")
+    one = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for slots, error in (([0, 1, 2, 3], TypeError), (one, ValueError), (one[0], ValueError), (one.view(4, 1).long(), TypeError),
+                         (one.view(4, 1).cpu(), ValueError), (one.view(2, 2), ValueError)):
+        with pytest.raises(error):
+            q8.q8_quantize_fp8(x, slots=slots)
