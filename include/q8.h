@@ -611,7 +611,8 @@ q8_status q8_quantize_weight_fp8(const void* w, q8_float_type type, int64_t E, i
 /*
  * Product of float8 matrices with block scales:
  *   y[m, n] = sum_b sa[m, b] sw[n / 128, b] sum_{k in block b} qa[m, k] qw[n, k].
- * The inner sums are the tensor core's, in fp32; the sum over blocks is one fp32 multiply-add a block;
+ * The inner sums are the tensor core's, in fp32; the sum over blocks is one fp32 multiply-add a block, with
+ * sa sw rounded to fp32 first (a product of scales past its range is infinite, one below 2^-126 has fewer bits);
  * y is rounded once, to `type`. The order of every sum depends on the sizes alone, so that the same
  * call gives the same bits. y : [M, N], dense. K = 0 gives zeros.
  * Errors: Q8_ERR_UNSUPPORTED for K % 16 != 0, M and N from 2^31 - 1024 on, or K from 2^31 - 128 on.

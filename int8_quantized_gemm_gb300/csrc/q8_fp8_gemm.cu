@@ -528,12 +528,13 @@ cudaError_t launch_swap(const uint8_t* qa, const uint8_t* qw, SwapArgs p, int64_
 //              K blocks at a time (neighbours in a row of sa), into shared memory
 //   warps 4-11 drain: a TMEM lane is a token row, so a thread's scale is one value a block, and the sum
 //              costs one multiply-add a value; two warps for each quarter of the lanes, PN / 2 columns each
-// Measured at 8192x8192x16384: 804 us from a cool start (2.7 PFLOP/s), 880 to 900 us back to back, where the power
-// cap holds the SM clock at 1.69 GHz (with all-zero codes 2.03 GHz and 764 us). The loads and MMAs alone (sums read
-// once a tile: wrong results) take 674 us, with every block's hand-over but no sums 756: what is left is
+// Measured at 8192x8192x16384: 804 us from a cool start (2.7 PFLOP/s), 875 to 885 us back to back, where the power
+// cap holds the SM clock at 1.69 GHz (with all-zero codes 2.03 GHz and 764 us). The MMAs are 0.92 M of some 1.5 M clocks
+// either way, so the cap costs a sixth of the time, and the tensor pipe stands still for 40 % of it. The loads and MMAs
+// alone (sums read once a tile: wrong results) take 674 us, with every block's hand-over but no sums 756: what is left is
 // the round trip MMA, commit, TMEM read, arrive, next MMA on two buffers (TMEM holds no third of 256 columns;
-// four of 128 in halves of a tile cost the MMA alone 838). A second issuer warp, spinning without
-// suspension, and 16 drain warps of 64 columns each were slower.
+// four of 128 in halves of a tile cost the MMA alone 838), in which a drain warp's reads and sums take turns. A second
+// issuer warp, spinning without suspension, and 16 drain warps of 64 columns each were slower.
 constexpr int PT = 256, PTH = 128;
 constexpr int kPairDrain = 8;                    // drain warps
 constexpr int kPairThreads = 128 + 32 * kPairDrain;

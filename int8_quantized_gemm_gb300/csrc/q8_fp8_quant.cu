@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(kThreads, kForm == kGated ? 6 : 1)   // gated:
     }
 }
 
-// One 128 x 128 block for a CTA: two sweeps over it (the second hits L2), offline.
+// One 128 x 128 block for a CTA: two sweeps over it (the second hits L2), offline, so with loads of single values: 0.65 of
+// the measured copy bandwidth (64 x 4096 x 4096 bf16 733 us, floor 475; 8192 x 16384 fp32 145 us, floor 99).
 template <class T>
 __global__ void __launch_bounds__(kThreads)
     quantize_weight_fp8_kernel(const T* __restrict__ w, int64_t N, int64_t K, uint8_t* __restrict__ q,

@@ -25,9 +25,9 @@ constexpr float kFloatMax = 3.402823466e38f;
 // fp32 keys' error bound and the replaced bits (about one token in a thousand on Gaussian logits with
 // a bias), the warp decides again in fp64: among the few experts about the border where only their
 // order is in doubt, over all of them where the choice of the groups is. The scores of the weights are fp32.
-// Bound by issue slots (about 1000 instructions a token at 256 experts): 8192 tokens take 10 us without a bias, 17 to
-// 21 us with one and groups, of which the last few tokens' fp64 (64 clocks an instruction) are 7 to 10; one
-// token 3.9 us, mostly launch.
+// Bound by issue slots (about 1000 instructions a token at 256 experts): 8192 tokens take 9 to 11 us without a bias, 12 to
+// 21 us (sigmoid) or up to 28 (softmax, whose bound is wider) with one and groups, of which the last few tokens' fp64
+// (64 clocks an instruction) are 7 and more; one token 3.9 us, mostly launch.
 struct Place {      // where a lane's experts are
     int base, have; // first expert, how many (<= VPL, may be 0)
     int group, first, lpg;
