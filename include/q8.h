@@ -564,8 +564,8 @@ q8_status q8_selftest_wait_timeout(q8_gemm_kernel kernel, const int8_t* qa, cons
  * value is passed on, never turned into a finite one.
  */
 
-/* Type of float tensors read or written by these operators. */
-typedef enum q8_float_type { Q8_F32 = 0, Q8_BF16 = 1, Q8_F16 = 2 } q8_float_type;
+/* Type of float tensors read or written by these operators; Q8_E4M3 only where it is named. */
+typedef enum q8_float_type { Q8_F32 = 0, Q8_BF16 = 1, Q8_F16 = 2, Q8_E4M3 = 3 } q8_float_type;
 
 /* Scores of a router: softmax over the experts, or a sigmoid of each. */
 typedef enum q8_score { Q8_SOFTMAX = 0, Q8_SIGMOID = 1 } q8_score;
@@ -635,6 +635,83 @@ q8_status q8_gemm_fp8_grouped(const uint8_t* qa, const float* sa, const uint8_t*
                               q8_float_type type, q8_stream_t stream);
 
 /*
+ * Operands of 4-bit floating point (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with a scale for each block of 16 or
+ * 32 along K, for linear layers and the products of routed experts.
+ *
+ * Codes are bytes [rows, K / 2]: K 2i in the low four bits of byte i, K 2i + 1 in the high ones; bit 3 of a code is its sign.
+ * K is a multiple of 32. Two formats, named by `block`:
+ *   16: e4m3 block scales c and an fp32 scale s for each row;  a code q stands for  q c s.
+ *   32: block scales that are powers of two, 2^(byte - 127), byte 255 NaN;  a code stands for  q c.
+ * Block scales, one byte each:
+ *   of activations, sf[rows, P]: block b of a row at b; P = 256 / block * ceil(K / 256) bytes, of which the last, past K, are
+ *       written as zeros and not read;
+ *   of weights, sfw[E, ceil(N / 128), P / 4, 32, 4, 4]: block b of row n at [n / 128][b / 4][n % 32][n % 128 / 32][b % 4], the
+ *       order in which the tensor core takes them; zeros where there is no row n or no block b.
+ * All of these arrays are 16-byte aligned. NaN and infinities are passed on, as by the float8 operators.
+ */
+
+/*
+ * Dynamic activation quantization to 4 bits, each operation rounded to nearest even in fp32, each scale and code once to its type:
+ *   block 16, over a row a = max(max |x|, 1e-30), over a block b = max |x|:
+ *       s = a / 2688,  c = e4m3(b * (448 / a)),  q = e2m1(x * ((2688 / a) / c)), 0 where c = 0.
+ *       A row with a NaN or an infinity gets s = NaN (its codes and block scales are not defined).
+ *   block 32: c = 2^e, the smallest with e >= -127 and b <= 6 c,  q = e2m1(x / c). c is NaN for a block with a NaN or an infinity.
+ *
+ * x, type, M, K, ldx, slots, top_k, rows_out : as q8_quantize_fp8 (rows 16-byte aligned; rows through slots).
+ * q, sf, s : codes [rows_out, K / 2], block scales [rows_out, P], row scales fp32 [rows_out], written (s: block 16 only; else it
+ *            may be NULL and is not used).
+ * Errors: Q8_ERR_INVALID_ARG (also another block), Q8_ERR_UNSUPPORTED for K % 32 != 0, a row pitch that is not a multiple of
+ * 16 bytes, more than 32 slots a row, sizes of 2^31 and more.
+ */
+q8_status q8_quantize_fp4(const void* x, q8_float_type type, int block, int64_t M, int64_t K, int64_t ldx,
+                          const int32_t* slots, int64_t top_k, int64_t rows_out, uint8_t* q, uint8_t* sf, float* s,
+                          q8_stream_t stream);
+
+/*
+ * Gated activation and quantization in one pass: x = h[m, I + i] * g / (1 + exp(-g)), g = h[m, i], as exact as in
+ * q8_swiglu_quantize_fp8, then q, sf and s of x as q8_quantize_fp4.
+ * h : [M, 2 I] of `type`, rows ldh elements apart. I % 32 == 0. Errors as q8_quantize_fp4.
+ */
+q8_status q8_swiglu_quantize_fp4(const void* h, q8_float_type type, int block, int64_t M, int64_t I, int64_t ldh, uint8_t* q,
+                                 uint8_t* sf, float* s, q8_stream_t stream);
+
+/*
+ * Weight quantization (offline): the rule of q8_quantize_fp4 for the rows of E matrices [N, K] (E = 1: one layer), dense, of
+ * `type`. qw [E, N, K / 2], sfw in the weights' order (above), sw fp32 [E, N] (block 16).
+ */
+q8_status q8_quantize_weight_fp4(const void* w, q8_float_type type, int block, int64_t E, int64_t N, int64_t K, uint8_t* qw,
+                                 uint8_t* sfw, float* sw, q8_stream_t stream);
+
+/*
+ * What codes stand for: y[m, k] = (q c) s in fp32, rounded to `type`. sf NULL: c = 1; s NULL: s = 1. tile_rows: 0 for block
+ * scales of activations; N for those of weights [rows / N, N, K]. type Q8_E4M3: the codes' own values (each of them an
+ * e4m3 number), with sf and s NULL. rows up to 2^40, rows * K / 16 up to 2^39 - 2^31.
+ */
+q8_status q8_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const float* s, int block, int64_t rows, int64_t K,
+                            int64_t tile_rows, void* y, q8_float_type type, q8_stream_t stream);
+
+/*
+ * Product of 4-bit matrices with block scales:
+ *   y[m, n] = sa[m] sw[n] sum_b sfa[m, b] sfw[n, b] sum_{k in block b} qa[m, k] qw[n, k].
+ * The sums over all of K are the tensor core's, in fp32; they are multiplied by sa and then by sw in fp32, and rounded once, to
+ * `type`. The order of every sum depends on the sizes alone, so that the same call gives the same bits.
+ * sa fp32 [M], sw fp32 [N] : NULL stands for ones, whatever the block. y : [M, N], dense. K = 0 gives zeros.
+ * Errors: Q8_ERR_UNSUPPORTED for K % 32 != 0, M and N from 2^31 - 1024 on, K from 2^31 - 512 on, weights whose block scales (padded
+ * to 128 rows and 256 K) are about 2^42 / block and more.
+ */
+q8_status q8_gemm_fp4(const uint8_t* qa, const uint8_t* sfa, const float* sa, const uint8_t* qw, const uint8_t* sfw,
+                      const float* sw, int block, int64_t M, int64_t N, int64_t K, void* y, q8_float_type type,
+                      q8_stream_t stream);
+
+/*
+ * The same product for routed experts: rows offsets[e] .. offsets[e + 1] - 1 of qa, sfa, sa and y belong to expert e and use
+ * qw[e], sfw[e], sw[e]. offsets, rows, E and what happens at their borders: as q8_gemm_fp8_grouped.
+ */
+q8_status q8_gemm_fp4_grouped(const uint8_t* qa, const uint8_t* sfa, const float* sa, const uint8_t* qw, const uint8_t* sfw,
+                              const float* sw, const int32_t* offsets, int block, int64_t rows, int64_t E, int64_t N,
+                              int64_t K, void* y, q8_float_type type, q8_stream_t stream);
+
+/*
  * Routing to experts. For each token, from its logits l[E]: the scores are p = softmax(l) or
  * sigmoid(l); top_k experts are chosen and written in falling order, ties to the lowest index.
  *  - Without a bias experts are ordered by l, with one by p + bias (compared as 64 bits give it); the bias
@@ -686,12 +763,12 @@ const char* q8_status_string(q8_status status);
  * gave up: one byte per kernel family (bits 0..7: the single-CTA tcgen05 kernel,
  * and bit 7 the fused RMSNorm quantizer's wait for a row copy; bits 8..15: the
  * tcgen05 decode kernel; bits 16..23: the warp-MMA decode kernels; bits 24..31:
- * the CTA-pair kernel and the float8 products, bit 31 set where a float8 product is among
+ * the CTA-pair kernel and the float8 and 4-bit products, bit 31 set where one of these products is among
  * them), within a byte one bit per role (1 TMA producer,
  * 2 converters / compute warps waiting for loaded data, 4 converters waiting
  * for a free stage, 8 MMA issuer waiting for converted data, 16 MMA issuer
  * waiting for a free accumulator, 32 accumulator drain, 64 the odd CTA's relay;
- * of a float8 product 4 its scale warps, 64 the exchange of a cluster's partial sums).
+ * of a float8 or 4-bit product 4 its scale warps, 64 the exchange of a cluster's partial sums).
  * Synchronises the device. Reading it resets it to 0. A nonzero value means the
  * outputs of the kernel that set it are invalid.
  */

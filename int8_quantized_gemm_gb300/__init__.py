@@ -26,6 +26,15 @@ Float8 (e4m3) operands with a scale for each block of 128, and layers of routed 
   q8_moe_route(logits, top_k, ...)        -> idx, weights
   q8_moe_plan(idx, n_experts)             -> offsets, slots
   q8_moe_combine(h, slots, weights)       -> y
+
+4-bit floating point (e2m1) operands with a scale for each block of 16 (e4m3, under one fp32 scale a row) or 32 K (a power of two):
+
+  q8_quantize_fp4(x, block=16, slots=None)      -> q, sf, s     (s is None for block 32)
+  q8_swiglu_quantize_fp4(h, block=16)           -> q, sf, s     (gated activation + quantize)
+  q8_quantize_weight_fp4(w, block=16)           -> qw, sfw, sw  ([N, K] or [E, N, K]; scales in the tensor core's order)
+  q8_dequantize_fp4(q, sf, s)                   -> y            (what the codes stand for)
+  q8_gemm_fp4(qa, sfa, sa, qw, sfw, sw)         -> y
+  q8_gemm_fp4_grouped(qa, sfa, sa, qw, sfw, sw, offsets) -> y   (row ranges of experts)
 """
 from __future__ import annotations
 
@@ -41,7 +50,8 @@ __all__ = [
     "q8_gemm_epilogue", "q8_gemm_s32", "q8_linear", "q8_quantize_weight_int4", "q8_colsum_int4", "q8_gemm_w4a8",
     "q8_gemm_w4a8_s32", "q8_quantize_weight_mx", "q8_gemm_mx", "q8_quantize_act_f16", "q8_quantize_act_dual", "q8_gemm_f16a", "q8_gemm_f16a_s32", "q8_linear_host", "q8_linear_host_workspace", "q8_gemm_workspace", "q8_gemm_pick", "q8_launch_count", "q8_device_error",
     "q8_selftest_wait_timeout", "KERNELS", "q8_quantize_fp8", "q8_swiglu_quantize_fp8", "q8_quantize_weight_fp8",
-    "q8_gemm_fp8", "q8_gemm_fp8_grouped", "q8_moe_route", "q8_moe_plan", "q8_moe_combine",
+    "q8_gemm_fp8", "q8_gemm_fp8_grouped", "q8_moe_route", "q8_moe_plan", "q8_moe_combine", "q8_quantize_fp4",
+    "q8_swiglu_quantize_fp4", "q8_quantize_weight_fp4", "q8_dequantize_fp4", "q8_gemm_fp4", "q8_gemm_fp4_grouped",
 ]
 
 LIB_PATH = _build.LIB
@@ -115,7 +125,14 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.q8_moe_route.argtypes = [p, i32, i64, i64, i64, i64, i32, p, i64, i64, i32, ctypes.c_float, p, p, p]
     lib.q8_moe_plan.argtypes = [p, i64, i64, i64, p, p, p]
     lib.q8_moe_combine.argtypes = [p, i32, i64, i64, p, p, i64, i64, p, p]
-    for name in ("q8_quantize_fp8", "q8_swiglu_quantize_fp8", "q8_quantize_weight_fp8", "q8_gemm_fp8",
+    lib.q8_quantize_fp4.argtypes = [p, i32, i32, i64, i64, i64, p, i64, i64, p, p, p, p]
+    lib.q8_swiglu_quantize_fp4.argtypes = [p, i32, i32, i64, i64, i64, p, p, p, p]
+    lib.q8_quantize_weight_fp4.argtypes = [p, i32, i32, i64, i64, i64, p, p, p, p]
+    lib.q8_dequantize_fp4.argtypes = [p, p, p, i32, i64, i64, i64, p, i32, p]
+    lib.q8_gemm_fp4.argtypes = [p, p, p, p, p, p, i32, i64, i64, i64, p, i32, p]
+    lib.q8_gemm_fp4_grouped.argtypes = [p, p, p, p, p, p, p, i32, i64, i64, i64, i64, p, i32, p]
+    for name in ("q8_quantize_fp4", "q8_swiglu_quantize_fp4", "q8_quantize_weight_fp4", "q8_dequantize_fp4", "q8_gemm_fp4",
+                 "q8_gemm_fp4_grouped", "q8_quantize_fp8", "q8_swiglu_quantize_fp8", "q8_quantize_weight_fp8", "q8_gemm_fp8",
                  "q8_gemm_fp8_grouped", "q8_moe_route", "q8_moe_plan", "q8_moe_combine",
                  "q8_quantize_act", "q8_rmsnorm_quantize_act", "q8_quantize_weight", "q8_colsum", "q8_gemm_dequant",
                  "q8_gemm_dequant_ex", "q8_gemm_dequant_ws", "q8_gemm_epilogue_ex", "q8_gemm_s32_ex", "q8_quantize_weight_int4",
@@ -849,4 +866,195 @@ def q8_moe_combine(h: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, 
     status = (_lib or load()).q8_moe_combine(h.data_ptr(), kind, rows, N, ps, pw, T, k, py, _handle(dev, stream))
     if status:
         _check(status, "q8_moe_combine")
+    return out
+
+
+# --------------------------------------------------------- 4-bit floating point, scales of 16 or 32 K
+
+FP4_SPAN = 256      # rows of block scales are whole spans of 256 K
+_SCALE_TYPES = {16: torch.float8_e4m3fn, 32: torch.float8_e8m0fnu}
+_BLOCKS = {v: k for k, v in _SCALE_TYPES.items()}
+_VALUE_TYPES = {**FLOAT_TYPES, torch.float8_e4m3fn: 3}
+
+
+def _fp4_pitch(K: int, block: int) -> int:
+    """Block scales of a row, those that fill up its last span among them."""
+    return -(-K // FP4_SPAN) * (FP4_SPAN // block)
+
+
+def _fp4_codes(rows: int, K: int, block: int, q, sf, s, like: torch.Tensor, device: int, stream):
+    """Results of a quantizer of `rows` rows: (q, sf, s) and their addresses."""
+    kind = _SCALE_TYPES.get(block)
+    if kind is None:
+        raise ValueError("block must be 16 or 32")
+    if K % 32:
+        raise ValueError("the number of columns must be a multiple of 32")
+    q, pq = _out(q, (rows, K // 2), torch.uint8, like, device, stream, "q")
+    sf, psf = _out(sf, (rows, _fp4_pitch(K, block)), kind, like, device, stream, "sf")
+    if block == 32:
+        if s is not None:
+            raise ValueError("s goes with block 16")
+        return q, sf, None, pq, psf, None
+    s, ps = _out(s, (rows,), torch.float32, like, device, stream, "s")
+    return q, sf, s, pq, psf, ps
+
+
+def q8_quantize_fp4(x: torch.Tensor, block: int = 16, slots=None, rows: int | None = None, q=None, sf=None, s=None, stream=None):
+    """4-bit codes of x[M, K] (fp32, bf16 or fp16; rows may be strided; K a multiple of 32). block 16: e4m3 scales of 16 K under an
+    fp32 scale a row; block 32: powers of two of 32 K. slots int32 [M, k]: row m goes to the rows slots[m] of the result instead
+    (skipped where outside), which has `rows` rows (default M * k). Returns (q uint8 [rows, K / 2], two codes a byte, sf
+    [rows, 256 / block * ceil(K / 256)] float8_e4m3fn or float8_e8m0fnu, s fp32 [rows] or None)."""
+    M, K, ldx, kind = _float_rows(x, "x")
+    dev = x.get_device()
+    top_k, to = 0, None
+    if slots is not None:
+        if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+            _need(slots, torch.int32, "slots", 2)
+        top_k = slots.shape[1]
+        to = _dense(slots, torch.int32, (M, top_k), dev, "slots")
+        rows = M * top_k if rows is None else rows
+    elif rows is not None and rows != M:
+        raise ValueError("rows goes with slots")
+    else:
+        rows = M
+    q, sf, s, pq, psf, ps = _fp4_codes(rows, K, block, q, sf, s, x, dev, stream)
+    status = (_lib or load()).q8_quantize_fp4(x.data_ptr(), kind, block, M, K, ldx, to, top_k, rows, pq, psf, ps,
+                                              _handle(dev, stream))
+    if status:
+        _check(status, "q8_quantize_fp4")
+    return q, sf, s
+
+
+def q8_swiglu_quantize_fp4(h: torch.Tensor, block: int = 16, q=None, sf=None, s=None, stream=None):
+    """Codes and scales (as q8_quantize_fp4) of silu(h[:, :I]) * h[:, I:], h[M, 2 I] (rows may be strided)."""
+    M, cols, ldh, kind = _float_rows(h, "h")
+    if cols % 2:
+        raise ValueError("h must have an even number of columns")
+    I, dev = cols // 2, h.get_device()
+    q, sf, s, pq, psf, ps = _fp4_codes(M, I, block, q, sf, s, h, dev, stream)
+    status = (_lib or load()).q8_swiglu_quantize_fp4(h.data_ptr(), kind, block, M, I, ldh, pq, psf, ps, _handle(dev, stream))
+    if status:
+        _check(status, "q8_swiglu_quantize_fp4")
+    return q, sf, s
+
+
+def _fp4_tiles(N: int, K: int, block: int):
+    """Shape of the block scales of a weight matrix: tiles of 128 rows x 4 scales."""
+    return _cdiv(N, 128), _fp4_pitch(K, block) // 4, 32, 4, 4
+
+
+def q8_quantize_weight_fp4(w: torch.Tensor, block: int = 16, qw=None, sfw=None, sw=None, stream=None):
+    """4-bit codes of w[N, K] or of the matrices w[E, N, K] (offline): (qw uint8 [.., N, K / 2], sfw [.., ceil(N / 128),
+    64 / block * ceil(K / 256), 32, 4, 4], sw fp32 [.., N] or None). Scale b of row n is at
+    sfw[n // 128, b // 4, n % 32, n % 128 // 32, b % 4]."""
+    if not isinstance(w, torch.Tensor) or w.dtype not in FLOAT_TYPES:
+        raise TypeError("w must be a float32, bfloat16 or float16 tensor")
+    _need(w, w.dtype, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    kind = _SCALE_TYPES.get(block)
+    if kind is None:
+        raise ValueError("block must be 16 or 32")
+    N, K = w.shape[-2:]
+    if K % 32:
+        raise ValueError("the number of columns must be a multiple of 32")
+    lead, dev = tuple(w.shape[:-2]), w.get_device()
+    E = lead[0] if lead else 1
+    qw, pq = _out(qw, (*lead, N, K // 2), torch.uint8, w, dev, stream, "qw")
+    sfw, psf = _out(sfw, (*lead, *_fp4_tiles(N, K, block)), kind, w, dev, stream, "sfw")
+    ps = None
+    if block == 16:
+        sw, ps = _out(sw, (*lead, N), torch.float32, w, dev, stream, "sw")
+    elif sw is not None:
+        raise ValueError("sw goes with block 16")
+    status = (_lib or load()).q8_quantize_weight_fp4(w.data_ptr(), FLOAT_TYPES[w.dtype], block, E, N, K, pq, psf, ps,
+                                                     _handle(dev, stream))
+    if status:
+        _check(status, "q8_quantize_weight_fp4")
+    return qw, sfw, sw
+
+
+def q8_dequantize_fp4(q: torch.Tensor, sf=None, s=None, out_dtype=torch.bfloat16, out=None, stream=None):
+    """What codes stand for, [.., K]: q (q8_quantize_fp4's [rows, K / 2] or q8_quantize_weight_fp4's) times its block scales sf (of the
+    same kind) times its row scales s; without a scale it counts as 1. out_dtype float32, bfloat16 or float16; without scales
+    also float8_e4m3fn, which holds every code."""
+    if not isinstance(q, torch.Tensor) or q.dtype is not torch.uint8 or not q.is_cuda or q.dim() not in (2, 3):
+        _need(q, torch.uint8, "q")
+        raise ValueError("q must be [rows, K / 2] or [E, N, K / 2]")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    kind = _VALUE_TYPES.get(out_dtype)
+    if kind is None:
+        raise TypeError("out_dtype must be torch.float32, torch.bfloat16, torch.float16 or torch.float8_e4m3fn")
+    if kind == 3 and (sf is not None or s is not None):
+        raise ValueError("float8 holds the codes alone, without scales")
+    lead, N, K, dev = tuple(q.shape[:-2]), q.shape[-2], 2 * q.shape[-1], q.get_device()
+    rows, block, tile_rows, psf, ps = (lead[0] * N if lead else N), 16, 0, None, None
+    if sf is not None:
+        block = _BLOCKS.get(sf.dtype) if isinstance(sf, torch.Tensor) else None
+        if block is None:
+            raise TypeError("sf must be float8_e4m3fn (blocks of 16) or float8_e8m0fnu (blocks of 32)")
+        if sf.dim() == 2 and not lead:
+            psf = _dense(sf, sf.dtype, (N, _fp4_pitch(K, block)), dev, "sf")
+        else:
+            psf, tile_rows = _dense(sf, sf.dtype, (*lead, *_fp4_tiles(N, K, block)), dev, "sf"), N
+    if s is not None:
+        ps = _dense(s, torch.float32, (*lead, N), dev, "s")
+    out, py = _out(out, (*lead, N, K), out_dtype, q, dev, stream, "out")
+    status = (_lib or load()).q8_dequantize_fp4(q.data_ptr(), psf, ps, block, rows, K, tile_rows, py, kind, _handle(dev, stream))
+    if status:
+        _check(status, "q8_dequantize_fp4")
+    return out
+
+
+def _fp4_operands(qa, sfa, sa, qw, sfw, sw, ndim, out_dtype, out, stream):
+    """Addresses and sizes of a product: (device, M, N, K, block, addresses of qa, sfa, sa, qw, sfw, sw and out, type, out)."""
+    for t, name, dims in ((qa, "qa", 2), (qw, "qw", ndim)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or not t.is_cuda or t.dim() != dims or not t.is_contiguous():
+            _need(t, torch.uint8, name, dims)
+    block = _BLOCKS.get(sfa.dtype) if isinstance(sfa, torch.Tensor) else None
+    if block is None:
+        raise TypeError("sfa must be float8_e4m3fn (blocks of 16) or float8_e8m0fnu (blocks of 32)")
+    M, half = qa.shape
+    shape = qw.shape
+    N, K = shape[-2], 2 * half
+    if shape[-1] != half:
+        raise ValueError("qa and qw disagree on K")
+    kind = FLOAT_TYPES.get(out_dtype)
+    if kind is None:
+        raise TypeError("out_dtype must be torch.float32, torch.bfloat16 or torch.float16")
+    dev = qa.get_device()
+    if qw.get_device() != dev:
+        raise ValueError(f"qw is on {qw.device}, not on cuda:{dev}")
+    lead, pitch = tuple(shape[:-2]), _fp4_pitch(K, block)
+    psfa = _dense(sfa, sfa.dtype, (M, pitch), dev, "sfa")
+    psfw = _dense(sfw, sfa.dtype, (*lead, -(-N // 128), pitch // 4, 32, 4, 4), dev, "sfw")
+    psa = None if sa is None else _dense(sa, torch.float32, (M,), dev, "sa")
+    psw = None if sw is None else _dense(sw, torch.float32, (*lead, N), dev, "sw")
+    out, py = _out(out, (M, N), out_dtype, qa, dev, stream, "out")
+    return dev, M, N, K, block, qa.data_ptr(), psfa, psa, qw.data_ptr(), psfw, psw, py, kind, out
+
+
+def q8_gemm_fp4(qa, sfa, sa, qw, sfw, sw, out_dtype=torch.bfloat16, out=None, stream=None):
+    """y[m, n] = sa[m] sw[n] sum over blocks b of sfa[m, b] sfw[n, b] (qa . qw over block b), as out_dtype [M, N]. The operands are
+    those of q8_quantize_fp4 and q8_quantize_weight_fp4, with the same block; sa or sw None stands for ones."""
+    dev, M, N, K, block, pa, psfa, psa, pw, psfw, psw, py, kind, out = _fp4_operands(qa, sfa, sa, qw, sfw, sw, 2, out_dtype, out,
+                                                                                     stream)
+    status = (_lib or load()).q8_gemm_fp4(pa, psfa, psa, pw, psfw, psw, block, M, N, K, py, kind, _handle(dev, stream))
+    if status:
+        _check(status, "q8_gemm_fp4")
+    return out
+
+
+def q8_gemm_fp4_grouped(qa, sfa, sa, qw, sfw, sw, offsets, out_dtype=torch.bfloat16, out=None, stream=None):
+    """The product of q8_gemm_fp4 with qw[e], sfw[e], sw[e] (of qw[E, N, K / 2]) for the rows offsets[e] .. offsets[e + 1] - 1 of each
+    expert; offsets int32 [E + 1] stay on the device. Rows of no expert are not written."""
+    dev, M, N, K, block, pa, psfa, psa, pw, psfw, psw, py, kind, out = _fp4_operands(qa, sfa, sa, qw, sfw, sw, 3, out_dtype, out,
+                                                                                     stream)
+    E = qw.shape[0]
+    status = (_lib or load()).q8_gemm_fp4_grouped(pa, psfa, psa, pw, psfw, psw,
+                                                  _dense(offsets, torch.int32, (E + 1,), dev, "offsets"), block, M, E, N, K, py,
+                                                  kind, _handle(dev, stream))
+    if status:
+        _check(status, "q8_gemm_fp4_grouped")
     return out

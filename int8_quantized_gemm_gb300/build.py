@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libq8.so")
 SOURCES = ["q8_api.cu", "q8_quant.cu", "q8_gemm_mma.cu", "q8_gemm_tc.cu", "q8_gemv_tc.cu", "q8_gemv_mma.cu", "q8_gemm_tc2.cu",
-           "q8_host.cu", "q8_fp8_api.cu", "q8_fp8_quant.cu", "q8_fp8_gemm.cu", "q8_moe.cu"]
+           "q8_host.cu", "q8_fp8_api.cu", "q8_fp8_quant.cu", "q8_fp8_gemm.cu", "q8_moe.cu",
+           "q8_fp4_api.cu", "q8_fp4_quant.cu", "q8_fp4_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,12 +41,9 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, "q8_internal.h"),
-                                                      os.path.join(CSRC, "q8_tc_ptx.cuh"),
-                                                      os.path.join(CSRC, "q8_fp8.h"),
-                                                      os.path.join(CSRC, "q8_fp8_ptx.cuh"),
-                                                      os.path.join(ROOT, "include", "q8.h"),
-                                                      os.path.abspath(__file__)]
+    headers = ["q8_internal.h", "q8_tc_ptx.cuh", "q8_fp8.h", "q8_fp8_ptx.cuh", "q8_tiles.cuh", "q8_silu.cuh", "q8_fp4.h",
+               "q8_fp4_ptx.cuh"]
+    deps = [os.path.join(CSRC, s) for s in SOURCES + headers] + [os.path.join(ROOT, "include", "q8.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
