@@ -260,3 +260,208 @@ def test_gemm(q8, M, N, K, block):
     for dtype in DTYPES:
         y = q8.q8_gemm_fp4(*device(a, block), *device(w, block, True), out_dtype=dtype)
         check(y, a[0], w[0], K, dtype)
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+def test_gemm_scales_of_ones(q8, block):
+    """Row scales may be left out, on either side, for either format."""
+    M, N, K = 70, 200, 416
+    a, w = ref.operand(M, K, block, seed=4), ref.operand(N, K, block, seed=5)
+    (qa, sfa, sa), (qw, sfw, sw) = device(a, block), device(w, block, True)
+    va, vw = a[0] if sa is None else a[0] / a[4].double()[:, None], w[0] if sw is None else w[0] / w[4].double()[:, None]
+    check(q8.q8_gemm_fp4(qa, sfa, None, qw, sfw, None, out_dtype=torch.float32), va, vw, K, torch.float32)
+    ones = torch.linspace(0.5, 2.0, M).cuda(), torch.linspace(-1.0, 1.0, N).cuda()
+    got = q8.q8_gemm_fp4(qa, sfa, ones[0], qw, sfw, None, out_dtype=torch.float32)
+    check(got, va * ones[0].cpu().double()[:, None], vw, K, torch.float32)
+    got = q8.q8_gemm_fp4(qa, sfa, None, qw, sfw, ones[1], out_dtype=torch.float32)
+    check(got, va, vw * ones[1].cpu().double()[:, None], K, torch.float32)
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+@pytest.mark.parametrize("M", [3, 40, 130, 600])
+def test_gemm_broken_rows_stay_apart(q8, M, block):
+    """A NaN in a token's or a weight's scales reaches its own row or column of y only; scales past K are not read."""
+    N, K = 300, 288
+    a, w = ref.operand(M, K, block, seed=6), ref.operand(N, K, block, seed=7)
+    rows, tiles = a[2].clone(), w[3].clone()
+    nan = 0x7F if block == 16 else 0xFF
+    rows[:, K // block:] = nan
+    sa = None if block == 32 else a[4].clone()
+    if block == 16:
+        sa[M // 2] = math.nan
+    else:
+        rows[M // 2, 1] = nan
+    tiles[1, 1, 7, 2, 1] = nan                       # weight row 128 + 64 + 7, block 5
+    q, sf, s = device(w, block, True)
+    y = q8.q8_gemm_fp4(a[1].cuda(), rows.view(ref.SCALE[block]).cuda(), None if sa is None else sa.cuda(), q,
+                       tiles.view(ref.SCALE[block]).cuda(), s, out_dtype=torch.float32).cpu()
+    want = torch.zeros((M, N), dtype=torch.bool)
+    want[M // 2], want[:, 199] = True, True
+    assert torch.equal(torch.isnan(y), want)
+    fine, cols = torch.arange(M) != M // 2, torch.arange(N) != 199
+    check(y[fine][:, cols], a[0][fine], w[0][cols], K, torch.float32)
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+@pytest.mark.parametrize("M", [5, 100, 520])
+def test_gemm_large_and_small_values(q8, M, block):
+    """Rows of very different sizes: the products' scales neither overflow nor lose bits on the way."""
+    N, K = 136, 1056
+    x, v = ref.tokens(M, K, seed=8), ref.tokens(N, K, seed=9)
+    x *= 2.0 ** torch.linspace(-60.0, 60.0, M).round()[:, None]
+    v *= 2.0 ** torch.linspace(40.0, -40.0, N).round()[:, None]
+    ops = []
+    for t in (x, v):
+        codes, sf, s = ref.quantize(t, block)
+        ops.append((ref.values(codes, sf, s, block), ref.pack(codes), ref.pad(sf, K, block), ref.tile(sf, K, block), s))
+    y = q8.q8_gemm_fp4(*device(ops[0], block), *device(ops[1], block, True), out_dtype=torch.float32)
+    check(y, ops[0][0], ops[1][0], K, torch.float32)
+
+
+def test_gemm_nothing_to_do(q8):
+    for block in BLOCKS:
+        a, w = ref.operand(4, 64, block, seed=1), ref.operand(8, 64, block, seed=2)
+        (qa, sfa, sa), (qw, sfw, sw) = device(a, block), device(w, block, True)
+        assert q8.q8_gemm_fp4(qa[:0], sfa[:0], None if sa is None else sa[:0], qw, sfw, sw).shape == (0, 8)
+        y = q8.q8_gemm_fp4(qa, sfa, sa, qw[:0], sfw[:0], None if sw is None else sw[:0])
+        assert y.shape == (4, 0)
+        out = torch.full((4, 8), 3.0, dtype=torch.float16, device="cuda")
+        q8.q8_gemm_fp4(qa[:, :0].contiguous(), sfa[:, :0].contiguous(), sa, qw[:, :0].contiguous(),
+                       sfw[:, :0].contiguous(), sw, out_dtype=torch.float16, out=out)
+        assert (out == 0).all()
+        q, sf, s = q8.q8_quantize_fp4(torch.empty((0, 64), device="cuda"), block=block)
+        assert q.shape == (0, 32) and sf.shape == (0, 256 // block)
+
+
+def offsets_of(counts, first=0):
+    return torch.tensor([first] + [first + sum(counts[:i + 1]) for i in range(len(counts))], dtype=torch.int32)
+
+
+GROUPS = [
+    ([3, 0, 5, 1], 130, 288),                    # a few rows; an expert without any
+    ([0, 0, 1], 64, 32),
+    ([17, 1, 0, 33, 2, 64], 264, 544),           # one tile and more of the smallest
+    ([70, 130, 0, 1, 90], 257, 800),
+    ([300, 1, 513, 0, 129], 392, 1312),          # CTA pairs; tiles that end in the next expert
+    ([1000, 24], 640, 2080),
+]
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+@pytest.mark.parametrize("counts,N,K", GROUPS)
+def test_grouped(q8, counts, N, K, block):
+    """Every expert's rows with its own matrix, rows before the first and behind the last left as they were."""
+    first, E = 5, len(counts)
+    rows = first + sum(counts) + 7
+    off = offsets_of(counts, first)
+    a = ref.operand(rows, K, block, seed=N)
+    ws = [ref.operand(N, K, block, seed=N + e + 1, scale=0.02) for e in range(E)]
+    qw = torch.stack([w[1] for w in ws]).cuda()
+    sfw = torch.stack([w[3] for w in ws]).view(ref.SCALE[block]).cuda()
+    sw = torch.stack([w[4] for w in ws]).cuda() if block == 16 else None
+    for dtype in DTYPES:
+        out = torch.full((rows, N), -7.0, dtype=dtype, device="cuda")
+        y = q8.q8_gemm_fp4_grouped(*device(a, block), qw, sfw, sw, off.cuda(), out_dtype=dtype, out=out)
+        assert y is out and (y[:first] == -7).all() and (y[int(off[-1]):] == -7).all()
+        for e in range(E):
+            at = slice(int(off[e]), int(off[e + 1]))
+            if counts[e]:
+                check(y[at], a[0][at], ws[e][0], K, dtype)
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+def test_grouped_offsets_of_any_value(q8, block):
+    """Offsets past the rows are cut, falling ones end the call; nothing outside y is touched."""
+    E, N, K, rows = 4, 72, 288, 50
+    a = ref.operand(rows, K, block, seed=1)
+    ws = [ref.operand(N, K, block, seed=e + 2) for e in range(E)]
+    qw = torch.stack([w[1] for w in ws]).cuda()
+    sfw = torch.stack([w[3] for w in ws]).view(ref.SCALE[block]).cuda()
+    sw = torch.stack([w[4] for w in ws]).cuda() if block == 16 else None
+    big = torch.full((rows + 200, N), 9.0, device="cuda")
+    for off in ([0, 10, 60, 1 << 30, 1 << 30], [-5, 10, 20, 45, 50], [40, 10, 50, 0, 50], [50, 50, 50, 50, 50]):
+        out = big[100:100 + rows]
+        q8.q8_gemm_fp4_grouped(*device(a, block), qw, sfw, sw, torch.tensor(off, dtype=torch.int32).cuda(),
+                               out_dtype=torch.float32, out=out)
+        assert (big[:100] == 9).all() and (big[100 + rows:] == 9).all()
+    y = q8.q8_gemm_fp4_grouped(*device(a, block), qw, sfw, sw, torch.tensor([0, 10, 60, 70, 90], dtype=torch.int32).cuda(),
+                               out_dtype=torch.float32)
+    check(y[:10], a[0][:10], ws[0][0], K, torch.float32)
+    check(y[10:], a[0][10:], ws[1][0], K, torch.float32)
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+@pytest.mark.parametrize("M", [2, 96, 700])
+def test_same_bits_again(q8, M, block):
+    """The same call gives the same bits, on another stream, from a graph, and with another call's kernels beside it."""
+    N, K = 520, 2080
+    a, w = device(ref.operand(M, K, block, seed=1), block), device(ref.operand(N, K, block, seed=2), block, True)
+    want = q8.q8_gemm_fp4(*a, *w)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        x, y = q8.q8_gemm_fp4(*a, *w, stream=other), q8.q8_gemm_fp4(*a, *w)
+        torch.cuda.synchronize()
+        assert torch.equal(x, want) and torch.equal(y, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z = q8.q8_gemm_fp4(*a, *w)
+    for _ in range(3):
+        z.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z, want)
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+@pytest.mark.parametrize("T", [1, 9, 300])
+def test_layer_of_experts(q8, T, block):
+    """The operators as a layer uses them, captured in a graph and replayed with other tokens, against 64 bits on the codes that the
+    quantizers gave: both products within their bounds."""
+    E, k, H, I = 6, 2, 288, 160
+    g = torch.Generator().manual_seed(T)
+    w13 = torch.randn((E, 2 * I, H), generator=g).cuda() * H ** -0.5
+    w2 = torch.randn((E, H, I), generator=g).cuda() * I ** -0.5
+    p13, p2 = q8.q8_quantize_weight_fp4(w13, block=block), q8.q8_quantize_weight_fp4(w2, block=block)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16).cuda()
+    logits = torch.randn((T, E), generator=g).cuda()
+
+    def layer():
+        idx, weights = q8.q8_moe_route(logits, k)
+        offsets, slots = q8.q8_moe_plan(idx, E)
+        qa = q8.q8_quantize_fp4(x, block=block, slots=slots)
+        h = q8.q8_gemm_fp4_grouped(*qa, *p13, offsets, out_dtype=torch.float32)
+        qh = q8.q8_swiglu_quantize_fp4(h, block=block)
+        z = q8.q8_gemm_fp4_grouped(*qh, *p2, offsets, out_dtype=torch.float32)
+        return offsets, slots, weights, qa, h, qh, z, q8.q8_moe_combine(z, slots, weights)
+
+    layer()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        offsets, slots, weights, qa, h, qh, z, y = layer()
+    for turn in range(2):
+        x.copy_(torch.randn((T, H), generator=g).to(torch.bfloat16))
+        logits.copy_(torch.randn((T, E), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        off = offsets.tolist()
+        codes, sf, s = ref.quantize(x.float().cpu(), block)
+        for t in range(T):
+            for d in slots[t].tolist():
+                assert torch.equal(qa[0][d].cpu(), ref.pack(codes)[t])
+
+        def value(q, sf, s):
+            K = 2 * q.shape[-1]
+            return ref.values(ref.unpack(q.cpu()), raw(sf)[:, :K // block].contiguous(), None if s is None else s.cpu(), block)
+        va, vh = value(*qa), value(*qh)
+        for e in range(E):
+            at = slice(off[e], off[e + 1])
+            if off[e] < off[e + 1]:
+                check(h[at], va[at], q8.q8_dequantize_fp4(p13[0][e], p13[1][e], None if p13[2] is None else p13[2][e],
+                                                          out_dtype=torch.float32).cpu().double(), H, torch.float32)
+                check(z[at], vh[at], q8.q8_dequantize_fp4(p2[0][e], p2[1][e], None if p2[2] is None else p2[2][e],
+                                                          out_dtype=torch.float32).cpu().double(), I, torch.float32)
+        want = (weights.cpu().double()[:, :, None] * z.cpu().double()[slots.cpu().long()]).sum(1)
+        size = (weights.cpu().double()[:, :, None] * z.cpu().double()[slots.cpu().long()].abs()).sum(1)
+        assert ((y.cpu().double() - want).abs() <= 4 * 2.0 ** -24 * size + 1e-30).all()
