@@ -694,18 +694,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + part;
         const uint32_t free_bar = mapa_shared(bar_accempty, 0);
         float* cols = reinterpret_cast<float*>(smem + C::kOffCol) + (warp - 4) * C::kHalf;
-        const uint32_t cols_at = sbase + C::kOffCol + (warp - 4) * C::kHalf * 4;
         const uint32_t epi = sbase + C::kOffEpi + (warp - 4) * kPairEpi;
         uint32_t buf = 0, bphase = 0;
-        for (uint32_t u = first; u < units; u += step) {
+        const int r0 = rank * PTH + quarter * 32;      // the warp's first row in a tile
+        // A tile's place and this lane's part of its scales: the row's, and every 32nd of the warp's columns. They are fetched
+        // while the tile before is written out.
+        struct {
+            int row, live, col0;
+            float f, w[C::kHalf / 32];
+        } next;
+        auto fetch = [&](uint32_t u) {
             int t, nt, e, row, n;
             pair_unit(u, tiles, NT, t, nt);
             groups.tile(t, e, row, n);
-            const int r0 = rank * PTH + quarter * 32;      // the warp's first row in the tile
-            const int live = min(32, n - r0), col0 = nt * PN + part;
-            const float f = p.sa && lane < live ? __ldg(p.sa + row + r0 + lane) : 1.0f;
+            next.row = row + r0;
+            next.live = min(32, n - r0);
+            next.col0 = nt * PN + part;
+            next.f = p.sa && lane < next.live ? __ldg(p.sa + next.row + lane) : 1.0f;
             if (p.sw)
-                for (int c = lane; c < C::kHalf; c += 32) cols[c] = col0 + c < p.N ? __ldg(p.sw + (int64_t)e * p.N + col0 + c) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < C::kHalf / 32; ++i) {
+                    const int c = next.col0 + 32 * i + lane;
+                    next.w[i] = c < p.N ? __ldg(p.sw + (int64_t)e * p.N + c) : 0.0f;
+                }
+        };
+        if (first < units) fetch(first);
+        for (uint32_t u = first; u < units; u += step) {
+            const int row = next.row, live = next.live, col0 = next.col0;
+            const uint64_t f2 = pack2(next.f, next.f);
+            if (p.sw) {
+#pragma unroll
+                for (int i = 0; i < C::kHalf / 32; ++i) cols[32 * i + lane] = next.w[i];
+                __syncwarp();
+            }
             if (!warp_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain)) break;
             tc_fence_after();
             uint64_t acc[C::kHalf / 2];
@@ -716,24 +737,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(free_bar + 8 * buf);
             if (++buf == kBufs) { buf = 0; bphase ^= 1; }
-            const uint64_t f2 = pack2(f, f);
+            if (u + step < units) fetch(u + step);
 #pragma unroll
-            for (int j = 0; j < C::kHalf / 2; j += 2) {
-                acc[j] = mul2(pack2(__uint_as_float(v[j / 32][2 * j % 64]), __uint_as_float(v[j / 32][2 * j % 64 + 1])), f2);
-                acc[j + 1] = mul2(pack2(__uint_as_float(v[j / 32][2 * j % 64 + 2]), __uint_as_float(v[j / 32][2 * j % 64 + 3])), f2);
-                if (p.sw) {
-                    const float4 w = lds_f4(cols_at + j * 8);
-                    acc[j] = mul2(acc[j], pack2(w.x, w.y));
-                    acc[j + 1] = mul2(acc[j + 1], pack2(w.z, w.w));
+            for (int h = 0; h < C::kHalf / 32; ++h) {
+                float4 w[8];
+                if (p.sw)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w[j] = reinterpret_cast<const float4*>(cols + 32 * h)[j];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t* from = &v[h / 2][h % 2 * 32 + 2 * j];
+                    uint64_t x = mul2(pack2(__uint_as_float(from[0]), __uint_as_float(from[1])), f2);
+                    if (p.sw) x = mul2(x, j % 2 ? pack2(w[j / 2].z, w[j / 2].w) : pack2(w[j / 2].x, w[j / 2].y));
+                    acc[16 * h + j] = x;
                 }
             }
             if (live > 0 && col0 < p.N) {
                 if (p.type == Q8_BF16)
-                    store_rows(static_cast<__nv_bfloat16*>(p.y), row + r0, live, col0, p.N, acc, epi, lane);
+                    store_rows(static_cast<__nv_bfloat16*>(p.y), row, live, col0, p.N, acc, epi, lane);
                 else if (p.type == Q8_F16)
-                    store_rows(static_cast<__half*>(p.y), row + r0, live, col0, p.N, acc, epi, lane);
+                    store_rows(static_cast<__half*>(p.y), row, live, col0, p.N, acc, epi, lane);
                 else
-                    store_rows(static_cast<float*>(p.y), row + r0, live, col0, p.N, acc, epi, lane);
+                    store_rows(static_cast<float*>(p.y), row, live, col0, p.N, acc, epi, lane);
             }
             __syncwarp();   // the column scales have been read
         }
