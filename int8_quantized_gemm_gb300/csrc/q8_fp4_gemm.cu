@@ -10,6 +10,8 @@
 // them into tiles on the way to shared memory.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "q8_fp4.h"
 #include "q8_fp4_ptx.cuh"
 #include "q8_internal.h"
@@ -79,7 +81,9 @@ struct TokenScales {
     }
 };
 
-// One of two scale warps (which = 0, 1: every other stage): the stages kb0 .. kb1 - 1 of one tile. `s`, `phase`: the ring's state at
+// One of two scale warps (which = 0, 1: every other stage, so that each has two stages' time for the way from a free stage to a full
+// one; pairs of stages a warp, which share a sector of the rows' scales, were 15 % slower with 128 tokens): the stages kb0 .. kb1 - 1
+// of one tile. `s`, `phase`: the ring's state at
 // kb0, moved on; `free_bar`: base of the barriers that a stage is free; `put(s)`: address of stage s's tiles; `done(s)`: arrival.
 // Two stages of its own are loaded ahead. False when a wait gave up.
 template <int kBlock, int J, class Put, class Done>
@@ -135,6 +139,40 @@ constexpr int kBufs = 2;               // accumulator buffers: the next tile's M
 constexpr int kMaxStages = 8;
 constexpr int kTailBytes = 8 * (2 * kMaxStages + 2 * kBufs + 2) + 32 + 4 * (kMaxExperts + 2);
 
+constexpr int kSwapEpi = 2048 + 256;   // of a drain warp: 2 KB of values on their way out, the scales of up to 64 tokens
+
+// acc[j]: weight row (column of y) col0 + lane, token t0 + j, as store_tokens; y's rows are whole 16-byte chunks. 2 KB of tokens
+// x 32 columns at a time are turned round in shared memory, so that a token's columns leave 16 bytes a lane (2050 rows of 32 experts,
+// 4096 x 2048: 89 -> 35 us with 128 tokens a tile, 57 -> 35 with 64).
+template <class T, int CW>
+__device__ __forceinline__ void store_tokens_staged(T* y, int64_t row, int t0, int n, int col0, int N, const float (&acc)[CW],
+                                                    uint32_t buf, int split, int rank, int lane) {
+    constexpr int kRow = 32 * sizeof(T), kTokens = 2048 / kRow < CW ? 2048 / kRow : CW;   // bytes of a token, tokens of a step
+    constexpr int kLanes = kRow / 16, kPass = 32 / kLanes;                               // lanes of a token, tokens of a pass
+    const int col = col0 + lane % kLanes * (16 / (int)sizeof(T));
+#pragma unroll
+    for (int c = 0; c < CW / kTokens; ++c) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+            const T v = from_float<T>(acc[c * kTokens + j]);
+            if constexpr (sizeof(T) == 2)
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 2), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
+            else
+                asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 4), "r"(__float_as_uint(acc[c * kTokens + j])) : "memory");
+        }
+        __syncwarp();
+        if (col < N) {
+#pragma unroll
+            for (int i = 0; i < (kTokens + kPass - 1) / kPass; ++i) {
+                const int r = i * kPass + lane / kLanes, t = t0 + c * kTokens + r;
+                if (r < kTokens && t < n && (split == 1 || ((t / 4) & (split - 1)) == rank))
+                    *reinterpret_cast<uint4*>(y + (row + t) * N + col) = lds128(buf + r * kRow + lane % kLanes * 16);
+            }
+        }
+    }
+}
+
 struct SwapArgs {
     const uint8_t* sfa;
     const float* sa;
@@ -181,7 +219,8 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     const uint32_t sbase = (sraw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (sbase - sraw);
     const uint32_t off_reduce = p.stages * C::kStage;
-    const uint32_t off_bar = off_reduce + reduce_bytes;
+    const uint32_t off_epi = off_reduce + reduce_bytes;
+    const uint32_t off_bar = off_epi + kDrainWarps * kSwapEpi;
     const uint32_t bar_full = sbase + off_bar;
     const uint32_t bar_empty = bar_full + 8 * kMaxStages;
     const uint32_t bar_accfull = bar_empty + 8 * kMaxStages;
@@ -313,12 +352,22 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
         // -------------------------------------------------------------------------- drain
         const int quarter = warp & 3, t0 = ((warp - 4) >> 2) * CW;   // its first token
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + t0;
+        const uint32_t epi = sbase + off_epi + (warp - 4) * kSwapEpi;
+        float* token_scales = reinterpret_cast<float*>(smem + off_epi + (warp - 4) * kSwapEpi + 2048);
         uint32_t buf = 0, bphase = 0, done = 0;
         for (uint32_t u = first; u < units; u += step, ++done) {
             int e, row, n;
             groups.tile((int)(u / (uint32_t)NT), e, row, n);
             const int col = (int)(u % (uint32_t)NT) * TW + quarter * 32 + lane;   // this thread's weight row
             const float scale = p.sw && col < p.N ? __ldg(p.sw + (int64_t)e * p.N + col) : 1.0f;
+            if (p.sa) {
+#pragma unroll
+                for (int i = 0; i < (CW + 31) / 32; ++i) {
+                    const int j = 32 * i + lane;
+                    if (j < CW) token_scales[j] = t0 + j < n ? __ldg(p.sa + row + t0 + j) : 0.0f;
+                }
+                __syncwarp();
+            }
             if (!warp_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain)) break;
             tc_fence_after();
             float acc[CW];
@@ -371,16 +420,30 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                 if (lane < S4) mbar_arrive_remote(mapa_shared(bar_free, lane));
             }
 #pragma unroll
-            for (int j = 0; j < CW; ++j) {
-                const float f = p.sa && t0 + j < n ? __ldg(p.sa + row + t0 + j) : 1.0f;
-                acc[j] = __fmul_rn(__fmul_rn(acc[j], f), scale);
+            for (int j = 0; j < CW; j += 4) {
+                if (p.sa) {
+                    const float4 f = *reinterpret_cast<const float4*>(token_scales + j);
+                    acc[j] = __fmul_rn(acc[j], f.x);
+                    acc[j + 1] = __fmul_rn(acc[j + 1], f.y);
+                    acc[j + 2] = __fmul_rn(acc[j + 2], f.z);
+                    acc[j + 3] = __fmul_rn(acc[j + 3], f.w);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j + i] = __fmul_rn(acc[j + i], scale);
             }
-            if (p.type == Q8_BF16)
-                store_tokens(static_cast<__nv_bfloat16*>(p.y), row, t0, n, col, p.N, acc, p.split, rank, lane);
-            else if (p.type == Q8_F16)
-                store_tokens(static_cast<__half*>(p.y), row, t0, n, col, p.N, acc, p.split, rank, lane);
-            else
-                store_tokens(static_cast<float*>(p.y), row, t0, n, col, p.N, acc, p.split, rank, lane);
+            __syncwarp();   // the tokens' scales have been read
+            if (t0 < n) {
+                auto store = [&](auto* y) {
+                    using T = typename std::remove_pointer<decltype(y)>::type;
+                    if (p.N * sizeof(T) % 16 == 0)
+                        store_tokens_staged<T>(y, row, t0, n, col - lane, p.N, acc, epi, p.split, rank, lane);
+                    else
+                        store_tokens(y, row, t0, n, col, p.N, acc, p.split, rank, lane);
+                };
+                if (p.type == Q8_BF16) store(static_cast<__nv_bfloat16*>(p.y));
+                else if (p.type == Q8_F16) store(static_cast<__half*>(p.y));
+                else store(static_cast<float*>(p.y));
+            }
         }
     }
 
@@ -471,14 +534,14 @@ cudaError_t launch_swap(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     p.most = (uint32_t)(tiles * ((g.N + TW - 1) / TW));
     const int reduce = p.split > 1 ? C::reduce_bytes(p.split) : 0;
-    const int room = kSmemMax - 1024 - kTailBytes - reduce;
+    const int room = kSmemMax - 1024 - kTailBytes - kDrainWarps * kSwapEpi - reduce;
     p.stages = room / C::kStage < kMaxStages ? room / C::kStage : kMaxStages;
     CUtensorMap ma, mw, ms;
     if (!make_maps<kBlock>(g, C::kBox, TW, ma, mw, ms)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
     cfg.blockDim = dim3(kSwapThreads, 1, 1);
-    cfg.dynamicSmemBytes = 1024 + p.stages * C::kStage + reduce + kTailBytes;
+    cfg.dynamicSmemBytes = 1024 + p.stages * C::kStage + reduce + kDrainWarps * kSwapEpi + kTailBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -491,23 +554,23 @@ cudaError_t launch_swap(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 }
 
 // ------------------------------------------------------------------ tokens on the MMA's M side, CTA pairs
-// For many tokens: a cluster of two CTAs shares a tile of 256 token rows x PN = 256 or 128 weight rows
+// For many tokens: a cluster of two CTAs shares a tile of 256 token rows x 256 weight rows
 // (cta_group::2; each CTA loads half of both, and the scales of its own token rows and of all weight rows of the tile, and
 // holds its 128 token rows' accumulators). Per CTA:
-//   warp 0     TMA: tokens [128 x 256 codes], weights [PN / 2 x 256 codes], the weights' scales of each stage, completing on the
+//   warp 0     TMA: tokens [128 x 256 codes], weights [128 x 256 codes], the weights' scales of each stage, completing on the
 //              even CTA's barrier
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
 //   warps 2, 3 scales of the CTA's token rows, every other stage each
-//   warps 4-11 drain: a TMEM lane is a token row; two warps for each quarter of the lanes, PN / 2 columns each
-constexpr int PT = 256, PTH = 128;
+//   warps 4-11 drain: a TMEM lane is a token row; two warps for each quarter of the lanes, 128 columns each
+constexpr int PT = 256, PTH = 128, PN = 256;   // tile: tokens, tokens of a CTA, weight rows
 constexpr int kPairDrain = 8;                    // drain warps
 constexpr int kPairThreads = 128 + 32 * kPairDrain;
 constexpr int kPairRegsLow = 88, kPairRegsHigh = 208;
 static_assert(128 * kPairRegsLow + 32 * kPairDrain * kPairRegsHigh <= kPairThreads * (65536 / kPairThreads / 8 * 8),
               "above the launch's registers");
-constexpr int kPairEpi = 2048;                   // of a drain warp: 32 rows x 64 bytes
+constexpr int kPairEpi = 4096;                   // of a drain warp: 32 rows x 128 bytes
 
-template <int PN, int kBlock>
+template <int kBlock>
 struct PairCfg {
     using S = Scales<kBlock>;
     static constexpr int kHalf = PN / 2;                      // weight rows of a CTA; columns of a drain warp
@@ -517,15 +580,15 @@ struct PairCfg {
     static constexpr int kStage = kOffSfa + S::kBytes;
     static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
     static constexpr int kLoad = kOffSfa;                     // bytes of a CTA's loads
-    static constexpr int kStages = PN == 256 ? 5 : 7;
-    static constexpr int kBufs = PN == 256 ? 1 : 2;           // accumulator buffers, beside the scales' columns
+    static constexpr int kStages = 5;
+    static constexpr int kBufs = 1;                           // accumulator buffers, beside the scales' columns
     static constexpr uint32_t kId0 = idesc_fp4(PT, PN, kBlock, 0), kId2 = idesc_fp4(PT, PN, kBlock, 2);
     static constexpr int kScaleCols = S::kCols + PN / TW * S::kCols;    // tokens, then weights
     static constexpr int kTmemScales = kBufs * PN;
     static_assert(kTmemScales + 2 * kScaleCols <= 512, "above the tensor memory");
     static constexpr int kOffEpi = kStages * kStage;
-    static constexpr int kOffCol = kOffEpi + kPairDrain * kPairEpi;     // the column scales of each drain warp
-    static constexpr int kOffBar = kOffCol + kPairDrain * kHalf * 4;
+    static constexpr int kOffCol = kOffEpi + kPairDrain * kPairEpi;     // the tile's column scales
+    static constexpr int kOffBar = kOffCol + PN * 4;
     static constexpr int kBars = 2 * kStages + 2 * kBufs;
     static constexpr int kSmem = 1024 + kOffBar + 8 * kBars + 32 + 4 * (kMaxExperts + 2);
     static_assert(kSmem <= kSmemMax, "above the shared memory of one CTA");
@@ -540,8 +603,43 @@ struct PairArgs {
     uint32_t pitch;
     void* y;
     q8_float_type type;
+    bool tma_out;    // rows of y are whole 16-byte chunks
     uint32_t most;   // units there can be
 };
+
+// A drain warp's 32 whole rows x 2 NC columns (one row a lane) to y: 128 bytes of each row at a time are staged in shared memory
+// (128-byte swizzle) and leave by TMA, which cuts off columns past N.
+template <class T, int NC>
+__device__ __forceinline__ void store_rows_tma(const CUtensorMap* map, int row0, int col0, int N, const uint64_t (&acc)[NC],
+                                               uint32_t buf, int lane) {
+    constexpr int kCols = 128 / sizeof(T);         // columns of a step
+#pragma unroll
+    for (int c = 0; c < 2 * NC / kCols; ++c) {
+        if (lane == 0) bulk_wait_read_all();      // the step before has left the buffer
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 2) {
+                    const float2 f = unpack2(acc[c * 32 + j * 4 + i]);
+                    w[i] = pack16<T>(f.x, f.y);
+                } else {
+                    const float2 f = unpack2(acc[c * 16 + j * 2 + i / 2]);
+                    w[i] = __float_as_uint(i & 1 ? f.y : f.x);
+                }
+            }
+            sts128(buf + lane * 128 + ((j ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && col0 + c * kCols < N) {
+            tma_store_2d(map, buf, col0 + c * kCols, row0);
+            bulk_commit();
+        }
+    }
+}
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
@@ -549,11 +647,26 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
-template <int PN, int kBlock>
+// The four drain warps of one half of the columns; all of them learn whether one has given up.
+__device__ __forceinline__ void part_sync(int id) { asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool part_any(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\n"
+        "setp.ne.u32 p, %2, 0;\n"
+        "bar.red.or.pred q, %1, 128, p;\n"
+        "selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"(v ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+template <int kBlock>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
-                         const __grid_constant__ CUtensorMap tmap_sf, PairArgs p) {
-    using C = PairCfg<PN, kBlock>;
+                         const __grid_constant__ CUtensorMap tmap_sf, const __grid_constant__ CUtensorMap tmap_y, PairArgs p) {
+    using C = PairCfg<kBlock>;
     using S = Scales<kBlock>;
     constexpr int kStages = C::kStages, kBufs = C::kBufs;
     extern __shared__ uint8_t smem_raw[];
@@ -693,15 +806,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int quarter = warp & 3, part = ((warp - 4) >> 2) * C::kHalf;   // its first column
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + part;
         const uint32_t free_bar = mapa_shared(bar_accempty, 0);
-        float* cols = reinterpret_cast<float*>(smem + C::kOffCol) + (warp - 4) * C::kHalf;
+        float* cols = reinterpret_cast<float*>(smem + C::kOffCol) + part;   // of the four warps of these columns
         const uint32_t epi = sbase + C::kOffEpi + (warp - 4) * kPairEpi;
         uint32_t buf = 0, bphase = 0;
         const int r0 = rank * PTH + quarter * 32;      // the warp's first row in a tile
-        // A tile's place and this lane's part of its scales: the row's, and every 32nd of the warp's columns. They are fetched
-        // while the tile before is written out.
+        // A tile's place and this thread's part of its scales, the row's and one of the columns'. They are fetched while the
+        // tile before is written out.
+        const int own = quarter * 32 + lane;           // its column scale
         struct {
             int row, live, col0;
-            float f, w[C::kHalf / 32];
+            float f, w;
         } next;
         auto fetch = [&](uint32_t u) {
             int t, nt, e, row, n;
@@ -712,22 +826,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             next.col0 = nt * PN + part;
             next.f = p.sa && lane < next.live ? __ldg(p.sa + next.row + lane) : 1.0f;
             if (p.sw)
-#pragma unroll
-                for (int i = 0; i < C::kHalf / 32; ++i) {
-                    const int c = next.col0 + 32 * i + lane;
-                    next.w[i] = c < p.N ? __ldg(p.sw + (int64_t)e * p.N + c) : 0.0f;
-                }
+                next.w = own < C::kHalf && next.col0 + own < p.N ? __ldg(p.sw + (int64_t)e * p.N + next.col0 + own) : 0.0f;
         };
         if (first < units) fetch(first);
         for (uint32_t u = first; u < units; u += step) {
             const int row = next.row, live = next.live, col0 = next.col0;
             const uint64_t f2 = pack2(next.f, next.f);
-            if (p.sw) {
-#pragma unroll
-                for (int i = 0; i < C::kHalf / 32; ++i) cols[32 * i + lane] = next.w[i];
-                __syncwarp();
-            }
-            if (!warp_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain)) break;
+            if (p.sw && own < C::kHalf) cols[own] = next.w;   // read after part_any
+            // A warp that gives up leaves with the three that share its column scales: they wait for one another.
+            const bool ok = warp_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain);
+            if (p.sw ? part_any(1 + part / C::kHalf, !ok) : !ok) break;
             tc_fence_after();
             uint64_t acc[C::kHalf / 2];
             uint32_t v[C::kHalf / 64][64];
@@ -752,16 +860,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     acc[16 * h + j] = x;
                 }
             }
+            if (p.sw) part_sync(1 + part / C::kHalf);   // the column scales have been read
+            auto store = [&](auto* y) {
+                using T = typename std::remove_pointer<decltype(y)>::type;
+                if (live == 32 && p.tma_out) {
+                    store_rows_tma<T>(&tmap_y, row, col0, p.N, acc, epi, lane);
+                } else {
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+                    store_rows(y, row, live, col0, p.N, acc, epi, lane);
+                }
+            };
             if (live > 0 && col0 < p.N) {
-                if (p.type == Q8_BF16)
-                    store_rows(static_cast<__nv_bfloat16*>(p.y), row, live, col0, p.N, acc, epi, lane);
-                else if (p.type == Q8_F16)
-                    store_rows(static_cast<__half*>(p.y), row, live, col0, p.N, acc, epi, lane);
-                else
-                    store_rows(static_cast<float*>(p.y), row, live, col0, p.N, acc, epi, lane);
+                if (p.type == Q8_BF16) store(static_cast<__nv_bfloat16*>(p.y));
+                else if (p.type == Q8_F16) store(static_cast<__half*>(p.y));
+                else store(static_cast<float*>(p.y));
             }
-            __syncwarp();   // the column scales have been read
         }
+        if (lane == 0) bulk_wait_all();   // shared memory outlives the stores from it
     }
 
     __syncthreads();
@@ -775,11 +891,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
-// Once per device: the shared-memory limit, and the clusters of two that run at once.
-template <int PN, int kBlock>
-cudaError_t pair_clusters(int& clusters) {
-    using C = PairCfg<PN, kBlock>;
-    static int cached[64] = {0};
+// Once per kernel and device: the shared-memory limit, and the clusters of two that run at once.
+template <class Kernel>
+cudaError_t clusters_of_two(Kernel* kernel, int smem, int (&cached)[64], int& clusters) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -787,14 +901,13 @@ cudaError_t pair_clusters(int& clusters) {
         clusters = cached[dev];
         return cudaSuccess;
     }
-    auto* kernel = gemm_fp4_pair_kernel<PN, kBlock>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     clusters = device_sm_count() / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.dynamicSmemBytes = smem;
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
@@ -803,19 +916,363 @@ cudaError_t pair_clusters(int& clusters) {
     return cudaSuccess;
 }
 
-template <int PN, int kBlock>
+template <int kBlock>
+cudaError_t pair_clusters(int& clusters) {
+    static int cached[64] = {0};
+    return clusters_of_two(gemm_fp4_pair_kernel<kBlock>, PairCfg<kBlock>::kSmem, cached, clusters);
+}
+
+template <int kBlock>
 cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream) {
-    using C = PairCfg<PN, kBlock>;
+    using C = PairCfg<kBlock>;
     int clusters = 0;
-    const cudaError_t e = pair_clusters<PN, kBlock>(clusters);
+    const cudaError_t e = pair_clusters<kBlock>(clusters);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mw, ms;
     if (!make_maps<kBlock>(g, PTH, C::kHalf, ma, mw, ms)) return cudaErrorInvalidValue;
     const int64_t units = tiles * ((g.N + PN - 1) / PN);
     if (units < clusters) clusters = (int)units;
+    const bool tma_out = g.N * (g.type == Q8_F32 ? 4 : 2) % 16 == 0;
+    CUtensorMap my = ma;
+    if (tma_out && !make_tma_map_out(&my, g.y, g.type == Q8_F32 ? kMapF32 : kMapBF16, g.rows, g.N)) return cudaErrorInvalidValue;
     const PairArgs p{g.sfa, g.sa, g.sw, g.offsets, (int)g.rows, (int)g.E, (int)g.N, (int)g.K, (uint32_t)fp4_pitch(g.K, kBlock),
-                     g.y, g.type, (uint32_t)units};
-    gemm_fp4_pair_kernel<PN, kBlock><<<2 * clusters, kPairThreads, C::kSmem, stream>>>(ma, mw, ms, p);
+                     g.y, g.type, tma_out, (uint32_t)units};
+    gemm_fp4_pair_kernel<kBlock><<<2 * clusters, kPairThreads, C::kSmem, stream>>>(ma, mw, ms, my, p);
+    note_launch();
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ weights on the MMA's M side, CTA pairs
+// For some tens of tokens a matrix: a cluster of two CTAs shares a tile of 256 weight rows x up to 128 token rows
+// (cta_group::2; each CTA loads half of both, the scales of its own weight rows and of all tokens of the tile, and
+// holds its 128 weight rows' accumulators). The MMA's N is the tile's tokens rounded up to 16, so that the last tile of an expert
+// costs what its tokens do. Per CTA:
+//   warp 0     TMA: weights [128 x 256 codes] with their scales, tokens [N / 2 x 256 codes] of each stage, completing on the even
+//              CTA's barrier
+//   warp 1     even CTA: pair MMA issuer; TMEM in both
+//   warps 2, 3 scales of the tile's tokens, every other stage each
+//   warps 4-11 drain: a TMEM lane is a weight row (a column of y); two warps for each quarter of the lanes, 64 tokens each
+constexpr int TWP = 256, TNP = 128;               // weight rows of a tile, token rows at most
+
+template <int kBlock>
+struct WideCfg {
+    using S = Scales<kBlock>;
+    static constexpr int kHalf = TNP / 2;                     // token rows of a CTA at most; tokens of a drain warp
+    static constexpr int kBox = 32;                           // token rows of a TMA box
+    static constexpr int kOffTokens = TW * kRowBytes;
+    static constexpr int kOffSfw = kOffTokens + kHalf * kRowBytes;
+    static constexpr int kOffSfa = kOffSfw + S::kBytes;
+    static constexpr int kStage = kOffSfa + S::kBytes;
+    static_assert(kStage % 1024 == 0 && kHalf % kBox == 0, "swizzled tiles start on 1024 bytes");
+    static constexpr int kStages = 6;
+    static constexpr int kBufs = 2;                           // accumulator buffers, beside the scales' columns
+    static constexpr uint32_t kId0 = idesc_fp4(TWP, 0, kBlock, 0), kId2 = idesc_fp4(TWP, 0, kBlock, 2);   // N is added
+    static constexpr int kScaleCols = 2 * S::kCols;           // weights, then tokens
+    static constexpr int kTmemScales = kBufs * TNP;
+    static_assert(kTmemScales + 2 * kScaleCols <= 512, "above the tensor memory");
+    static constexpr int kOffEpi = kStages * kStage;
+    static constexpr int kOffTok = kOffEpi + kPairDrain * kPairEpi;     // the tokens' row scales
+    static constexpr int kOffBar = kOffTok + TNP * 4;
+    static constexpr int kBars = 2 * kStages + 2 * kBufs;
+    static constexpr int kSmem = 1024 + kOffBar + 8 * kBars + 32 + 4 * (kMaxExperts + 2);
+    static_assert(kSmem <= kSmemMax, "above the shared memory of one CTA");
+};
+
+// acc[j]: weight row (column of y) col0 + lane, token t0 + j; y's rows are whole 16-byte chunks. 2 KB of tokens x 32 columns at a
+// time are turned round in shared memory (two buffers) and leave by TMA, the last tokens of an expert 16 bytes a lane.
+template <class T, int NC>
+__device__ __forceinline__ void store_columns(const CUtensorMap* map, T* y, int row, int live, int col0, int N,
+                                              const float (&acc)[NC], uint32_t buf, int lane) {
+    constexpr int kRow = 32 * sizeof(T), kTokens = 2048 / kRow;      // bytes of a token, tokens of a step
+    constexpr int kLanes = kRow / 16, kPass = 32 / kLanes;           // lanes of a token, tokens of a pass
+    if (col0 >= N) return;
+#pragma unroll
+    for (int c = 0; c < NC / kTokens; ++c) {
+        if (c * kTokens >= live) break;
+        const uint32_t at = buf + (c & 1) * 2048;
+        if (lane == 0) {   // the buffer has left: of the tile before, or of the step before the last
+            if (c == 0) bulk_wait_read_all();
+            else asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+            const T v = from_float<T>(acc[c * kTokens + j]);
+            if constexpr (sizeof(T) == 2)
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(at + j * kRow + lane * 2), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
+            else
+                asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(at + j * kRow + lane * 4), "r"(__float_as_uint(acc[c * kTokens + j])) : "memory");
+        }
+        if (live - c * kTokens >= kTokens) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(map, at, col0, row + c * kTokens);
+                bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            const int col = col0 + lane % kLanes * (16 / (int)sizeof(T));
+            for (int r = lane / kLanes; r < live - c * kTokens; r += kPass)
+                if (col < N)
+                    *reinterpret_cast<uint4*>(y + (int64_t)(row + c * kTokens + r) * N + col) =
+                        lds128(at + r * kRow + lane % kLanes * 16);
+        }
+    }
+}
+
+template <int kBlock>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    gemm_fp4_wide_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                         const __grid_constant__ CUtensorMap tmap_sf, const __grid_constant__ CUtensorMap tmap_y, PairArgs p) {
+    using C = WideCfg<kBlock>;
+    using S = Scales<kBlock>;
+    constexpr int kStages = C::kStages, kBufs = C::kBufs;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t sraw = smem_u32(smem_raw);
+    const uint32_t sbase = (sraw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (sbase - sraw);
+    const uint32_t bar_full = sbase + C::kOffBar;             // used in the even CTA: both CTAs' loads and scales
+    const uint32_t bar_done = bar_full + 8 * kStages;          // both CTAs: the pair MMA's commit
+    const uint32_t bar_accfull = bar_done + 8 * kStages;       // both CTAs: a tile's last commit
+    const uint32_t bar_accempty = bar_accfull + 8 * kBufs;     // used in the even CTA: both CTAs' drain warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * C::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* cum = reinterpret_cast<int*>(tmem_slot + 2);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar_full + 8 * s, 3);      // the loads and a scale warp of each CTA
+            mbar_init(bar_done + 8 * s, 1);
+        }
+        for (int b = 0; b < kBufs; ++b) {
+            mbar_init(bar_accfull + 8 * b, 1);
+            mbar_init(bar_accempty + 8 * b, 2 * kPairDrain);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_sf)) : "memory");
+    }
+    const Groups groups{p.offsets, cum, p.rows, p.E, TNP};
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    if (warp == 2) groups.scan(cum, lane);
+    tc_fence_before();
+    cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int NT = (p.N + TWP - 1) / TWP, NB = (p.N + TW - 1) / TW, KB = (p.K + kFp4Span - 1) / kFp4Span;
+    const int tiles = cum[p.E];
+    const uint32_t units = groups.units(NT, p.most), first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPairRegsLow));
+        if (warp == 0) {
+            // ------------------------------------------------------------------------ TMA
+            const uint32_t full0 = mapa_shared(bar_full, 0);
+            uint32_t s = 0, phase = 1;
+            bool ok = true;
+            for (uint32_t u = first; u < units && ok; u += step) {
+                int t, nt, e, row, n;
+                pair_unit(u, tiles, NT, t, nt);
+                groups.tile(t, e, row, n);
+                const int half = ((n + 15) >> 4) << 3, boxes = (half + C::kBox - 1) / C::kBox;   // tokens of a CTA
+                const int arow = row + rank * half;
+                // A half without a weight row is loaded from past the end of the tensor: zeros
+                const int wrow = nt * TWP + rank * TW < p.N ? e * p.N + nt * TWP + rank * TW : p.E * p.N;
+                const int sfrow = (e * NB + nt * 2 + rank) * KB * (S::kAtoms * 4);
+                const uint32_t bytes = 2 * (C::kOffTokens + S::kBytes + boxes * C::kBox * kRowBytes);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!warp_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + s * C::kStage;
+                    if (elect_one()) {
+                        if (rank == 0) mbar_expect_tx(bar_full + 8 * s, bytes);
+                        tma_load_2d_pair(dst, &tmap_w, kb * kRowBytes, wrow, full0 + 8 * s);
+                        tma_load_2d_pair(dst + C::kOffSfw, &tmap_sf, 0, sfrow + kb * (S::kAtoms * 4), full0 + 8 * s);
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d_pair(dst + C::kOffTokens + b * C::kBox * kRowBytes, &tmap_a, kb * kRowBytes,
+                                             arow + b * C::kBox, full0 + 8 * s);
+                    }
+                    __syncwarp();
+                    if (++s == kStages) { s = 0; phase ^= 1; }
+                }
+            }
+        } else if (warp == 1 && rank == 0) {
+            // ------------------------------------------------------------------------ MMA
+            uint32_t s = 0, phase = 0, buf = 0, bphase = 1, c = 0;
+            bool ok = true;
+            for (uint32_t u = first; u < units && ok; u += step) {
+                int t, nt, e, row, n;
+                pair_unit(u, tiles, NT, t, nt);
+                groups.tile(t, e, row, n);
+                const uint32_t width = (uint32_t)((n + 15) >> 4) << 18;   // N = n rounded up to 16
+                const uint32_t id0 = C::kId0 + width, id2 = C::kId2 + width;
+                if (!warp_wait_cluster(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc)) break;
+                const uint32_t d = tmem_base + buf * TNP;
+                for (int kb = 0; kb < KB; ++kb, ++c) {
+                    if (!warp_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = sbase + s * C::kStage;
+                    const uint64_t w = smem_desc_sw128(at), a = smem_desc_sw128(at + C::kOffTokens);
+                    const uint64_t sfw = smem_desc_scales(at + C::kOffSfw), sfa = smem_desc_scales(at + C::kOffSfa);
+                    const uint32_t tw = tmem_base + C::kTmemScales + (c & 1) * C::kScaleCols, ta = tw + S::kCols;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < S::kAtoms; ++k) {
+                            copy_scales<2>(tw + 4 * k, sfw + 32 * k);
+                            copy_scales<2>(ta + 4 * k, sfa + 32 * k);
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const int k = kBlock == 16 ? kk : kk / 2;
+                            mma_fp4<kBlock, 2>(d, w + 2 * kk, a + 2 * kk, kBlock == 32 && kk % 2 ? id2 : id0, tw + 4 * k,
+                                               ta + 4 * k, kb || kk ? 1u : 0u);
+                        }
+                        mma_commit_pair(bar_done + 8 * s, 3);
+                        if (kb == KB - 1) mma_commit_pair(bar_accfull + 8 * buf, 3);
+                    }
+                    __syncwarp();
+                    if (++s == kStages) { s = 0; phase ^= 1; }
+                }
+                if (++buf == kBufs) { buf = 0; bphase ^= 1; }
+            }
+        } else if (warp >= 2) {
+            // --------------------------------------------------------------------- scales
+            const uint32_t full0 = mapa_shared(bar_full, 0);
+            uint32_t s = 0, phase = 1, count = 0;
+            bool ok = true;
+            for (uint32_t u = first; u < units && ok; u += step) {
+                int t, nt, e, row, n;
+                pair_unit(u, tiles, NT, t, nt);
+                groups.tile(t, e, row, n);
+                ok = feed_scales<kBlock, TNP / 32>(
+                    p.sfa, row, n, p.pitch, p.K / kBlock, 0, KB, count, warp - 2, kStages, s, phase, bar_done, abort_flag, lane,
+                    [&](uint32_t st) { return sbase + st * C::kStage + C::kOffSfa; },
+                    [&](uint32_t st) { mbar_arrive_remote(full0 + 8 * st); });
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------------------- drain
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kPairRegsHigh));
+        const int quarter = warp & 3, t0 = ((warp - 4) >> 2) * C::kHalf, id = 1 + t0 / C::kHalf;   // its first token
+        const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + t0;
+        const uint32_t free_bar = mapa_shared(bar_accempty, 0);
+        float* token_scales = reinterpret_cast<float*>(smem + C::kOffTok) + t0;   // of the four warps of these tokens
+        const uint32_t epi = sbase + C::kOffEpi + (warp - 4) * kPairEpi;
+        const int own = quarter * 32 + lane;           // its token's scale; its weight row in the CTA's half
+        uint32_t buf = 0, bphase = 0;
+        // A tile's place and this thread's part of its scales. They are fetched while the tile before is written out.
+        struct {
+            int row, live, col0;
+            float f, w;
+        } next;
+        auto fetch = [&](uint32_t u) {
+            int t, nt, e, row, n;
+            pair_unit(u, tiles, NT, t, nt);
+            groups.tile(t, e, row, n);
+            next.row = row + t0;
+            next.live = min(C::kHalf, n - t0);
+            next.col0 = nt * TWP + rank * TW + quarter * 32;
+            const int col = next.col0 + lane;
+            next.w = p.sw && col < p.N ? __ldg(p.sw + (int64_t)e * p.N + col) : 1.0f;
+            if (p.sa) next.f = own < next.live ? __ldg(p.sa + next.row + own) : 0.0f;
+        };
+        if (first < units) fetch(first);
+        for (uint32_t u = first; u < units; u += step) {
+            const int row = next.row, live = next.live, col0 = next.col0;
+            const float scale = next.w;
+            if (p.sa && own < C::kHalf) token_scales[own] = next.f;   // read after part_any
+            // A warp that gives up leaves with the three that share its tokens' scales: they wait for one another.
+            const bool ok = warp_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain);
+            if (p.sa ? part_any(id, !ok) : !ok) break;
+            tc_fence_after();
+            float acc[C::kHalf];
+            if (live > 0) {
+                uint32_t v[C::kHalf];
+                tmem_load(tlane + buf * TNP, v);
+#pragma unroll
+                for (int j = 0; j < C::kHalf; ++j) acc[j] = __uint_as_float(v[j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(free_bar + 8 * buf);
+            if (++buf == kBufs) { buf = 0; bphase ^= 1; }
+            if (u + step < units) fetch(u + step);
+            if (live > 0) {
+#pragma unroll
+                for (int h = 0; h < C::kHalf / 32; ++h) {
+                    float4 w[8];
+                    if (p.sa)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[j] = reinterpret_cast<const float4*>(token_scales + 32 * h)[j];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float x = acc[32 * h + j];
+                        if (p.sa) x = __fmul_rn(x, j % 4 == 0 ? w[j / 4].x : j % 4 == 1 ? w[j / 4].y : j % 4 == 2 ? w[j / 4].z : w[j / 4].w);
+                        acc[32 * h + j] = __fmul_rn(x, scale);
+                    }
+                }
+            }
+            if (p.sa) part_sync(id);   // the tokens' scales have been read
+            auto store = [&](auto* y) {
+                using T = typename std::remove_pointer<decltype(y)>::type;
+                if (p.tma_out) store_columns<T>(&tmap_y, y, row, live, col0, p.N, acc, epi, lane);
+                else store_tokens(y, row, 0, live, col0 + lane, p.N, acc, 1, 0, lane);
+            };
+            if (live > 0) {
+                if (p.type == Q8_BF16) store(static_cast<__nv_bfloat16*>(p.y));
+                else if (p.type == Q8_F16) store(static_cast<__half*>(p.y));
+                else store(static_cast<float*>(p.y));
+            }
+        }
+        if (lane == 0) bulk_wait_all();   // shared memory outlives the stores from it
+    }
+
+    __syncthreads();
+    if (*abort_flag) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1LL << 22)) __nanosleep(1000);
+    }
+    tc_fence_before();
+    cluster_sync();   // neither CTA frees TMEM or leaves while the other may still use its part
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+template <int kBlock>
+cudaError_t wide_clusters(int& clusters) {
+    static int cached[64] = {0};
+    return clusters_of_two(gemm_fp4_wide_kernel<kBlock>, WideCfg<kBlock>::kSmem, cached, clusters);
+}
+
+template <int kBlock>
+cudaError_t launch_wide(const Fp4Product& g, int64_t tiles, cudaStream_t stream) {
+    using C = WideCfg<kBlock>;
+    int clusters = 0;
+    const cudaError_t e = wide_clusters<kBlock>(clusters);
+    if (e != cudaSuccess) return e;
+    CUtensorMap ma, mw, ms;
+    if (!make_maps<kBlock>(g, C::kBox, TW, ma, mw, ms)) return cudaErrorInvalidValue;
+    const int64_t units = tiles * ((g.N + TWP - 1) / TWP);
+    if (units < clusters) clusters = (int)units;
+    const int size = g.type == Q8_F32 ? 4 : 2;
+    const bool tma_out = g.N * size % 16 == 0;
+    CUtensorMap my = ma;
+    if (tma_out && !make_tma_map_box(&my, g.y, size, g.rows, g.N, 32, 64 / size)) return cudaErrorInvalidValue;
+    const PairArgs p{g.sfa, g.sa, g.sw, g.offsets, (int)g.rows, (int)g.E, (int)g.N, (int)g.K, (uint32_t)fp4_pitch(g.K, kBlock),
+                     g.y, g.type, tma_out, (uint32_t)units};
+    gemm_fp4_wide_kernel<kBlock><<<2 * clusters, kPairThreads, C::kSmem, stream>>>(ma, mw, ms, my, p);
     note_launch();
     return cudaGetLastError();
 }
@@ -823,31 +1280,30 @@ cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 template <int kBlock>
 cudaError_t launch(const Fp4Product& p, cudaStream_t stream) {
     const int64_t per = (p.rows + p.E - 1) / p.E;   // rows of a group, on average
-    const int64_t NT = (p.N + TW - 1) / TW;
+    const int64_t NT = (p.N + TW - 1) / TW, KB = (p.K + kFp4Span - 1) / kFp4Span;
     auto tiles = [&](int tn) { return p.offsets ? p.rows / tn + (p.E < p.rows ? p.E : p.rows) : (p.rows + tn - 1) / tn; };
     // The kernels count tiles in 32 bits, whatever the offsets are (each group at most all rows).
     if (tiles(16) * NT >= (1LL << 31) - 1024 || (p.rows / 16 + 1) * p.E >= (1LL << 31)) return cudaErrorNotSupported;
-    if (per > 64) {
-        int pairs = 0, split = 1, clusters = 0;
-        double other = 0.0;
-        cudaError_t e = pair_clusters<256, kBlock>(pairs);
-        if (e == cudaSuccess) e = swap_plan<64, kBlock>(tiles(128), p.N, p.K, split, clusters, other);
-        if (e != cudaSuccess) return e;
-        auto estimate = [&](int pn, double stage) {
-            const int64_t rounds = (tiles(PT) * ((p.N + pn - 1) / pn) + pairs - 1) / pairs;
-            return (double)rounds * stage * (double)((p.K + kFp4Span - 1) / kFp4Span + 6);
-        };
-        const double wide = estimate(256, 0.30), narrow = estimate(128, 0.20);
-        if (0.25 * other < wide && 0.25 * other < narrow) return launch_swap<64, kBlock>(p, tiles(128), stream);
-        if (narrow < wide) return launch_pair<128, kBlock>(p, tiles(PT), stream);
-        return launch_pair<256, kBlock>(p, tiles(PT), stream);
-    }
     // Groups of unequal size: a tile four times the average leaves few of them more than one.
     const int64_t most = p.offsets ? 4 * per : per;
     if (most <= 16) return launch_swap<8, kBlock>(p, tiles(16), stream);
     if (most <= 32) return launch_swap<16, kBlock>(p, tiles(32), stream);
-    if (most <= 64) return launch_swap<32, kBlock>(p, tiles(64), stream);
-    return launch_swap<64, kBlock>(p, tiles(128), stream);
+    // What a round of tiles takes, in us, as measured: 0.28 a stage and 1.0 for 256 x 128 tiles over 76 pairs, 0.31 and 1.6 for 256 x
+    // 256; a group's last tile is half full on average. Weights that are not in L2 take their time to be read whatever the tile, and the
+    // smaller one waits less for them.
+    int narrow = 0, wide = 0;
+    cudaError_t e = wide_clusters<kBlock>(narrow);
+    if (e == cudaSuccess) e = pair_clusters<kBlock>(wide);
+    if (e != cudaSuccess) return e;
+    auto rounds = [&](int tn, int pairs) {
+        const int64_t t = p.offsets ? p.rows / tn + (p.E < p.rows ? p.E : p.rows) / 2 + 1 : (p.rows + tn - 1) / tn;
+        return (double)((t * ((p.N + PN - 1) / PN) + pairs - 1) / pairs);
+    };
+    const double memory = (double)(p.E < p.rows ? p.E : p.rows) * (double)p.N * (double)p.K * (0.5 + 1.0 / kBlock) / 6.5e6;
+    const double small = rounds(TNP, narrow) * (0.28 * (double)KB + 1.0) + 5.0;
+    const double large = rounds(PT, wide) * (0.31 * (double)KB + 1.6) + 6.0;
+    if (small <= (large > memory ? large : memory)) return launch_wide<kBlock>(p, tiles(TNP), stream);
+    return launch_pair<kBlock>(p, tiles(PT), stream);
 }
 
 }  // namespace

@@ -434,6 +434,19 @@ bool make_tma_map_out(CUtensorMap* map, void* base, int kind, int64_t rows, int6
     return r == CUDA_SUCCESS;
 }
 
+bool make_tma_map_box(CUtensorMap* map, void* base, int size, int64_t rows, int64_t cols, int box_cols, int box_rows) {
+    auto enc = get_encode();
+    if (!enc || (size != 2 && size != 4) || cols * size % 16 != 0 || (reinterpret_cast<uintptr_t>(base) & 15) != 0) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(cols * size)};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, size == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, base, dims, strides, box,
+                     estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 int device_sm_count() { return sm_count_impl(); }
 
 bool gemm_tc_supports(int64_t M, int64_t N, int64_t K) {

@@ -250,7 +250,7 @@ def check(got, a, w, K, dtype):
 
 SIZES = [(1, 8, 32), (1, 128, 256), (3, 130, 288), (16, 264, 2048), (17, 1000, 544), (33, 257, 96), (64, 512, 1024),
          (65, 129, 4128), (100, 384, 320), (128, 256, 512), (129, 391, 800), (200, 264, 1088), (257, 520, 1312), (300, 1026, 64),
-         (517, 2056, 2080), (1000, 700, 4096)]
+         (517, 2056, 2080), (1000, 700, 4096), (2600, 2599, 544), (2561, 4001, 96), (3333, 2600, 1312)]
 
 
 @pytest.mark.parametrize("block", BLOCKS)
@@ -344,6 +344,8 @@ GROUPS = [
     ([70, 130, 0, 1, 90], 257, 800),
     ([300, 1, 513, 0, 129], 392, 1312),          # CTA pairs; tiles that end in the next expert
     ([1000, 24], 640, 2080),
+    ([3000, 1, 700, 0, 2000], 2050, 544),        # 256 x 256 tiles
+    ([129, 2800, 2311], 2001, 800),
 ]
 
 
