@@ -40,4 +40,33 @@ struct Fp4Product {
 cudaError_t launch_gemm_fp4(const Fp4Product& p, int block, cudaStream_t stream);
 cudaError_t read_and_clear_gemm_fp4_error(uint32_t* code);
 
+#ifdef __CUDACC__
+// The kernels of these operators may start while the one before them on the stream still runs (programmatic stream
+// serialization): each touches global memory only after depend_wait(), which returns once that kernel has completed and its writes
+// can be seen, and then lets the next one start. What overlaps is the set-up and the launch (128x8192x8192 13.4 -> 12.5 us, 2050 rows
+// of 32 experts 34.3 -> 32.8, called one after another).
+__device__ __forceinline__ void depend_wait() {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+// cluster: CTAs of a cluster, 0 where the kernel names them itself or has none.
+template <class... KArgs, class... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,
+                             Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 }  // namespace q8

@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
         }
     }
     if (warp == 1) tmem_alloc(smem_u32(tmem_slot), C::kTmem);
+    depend_wait();
     if (warp == 2) groups.scan(cum, lane);
     tc_fence_before();
     if (p.split > 1) cluster_sync();
@@ -538,17 +539,9 @@ cudaError_t launch_swap(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
     p.stages = room / C::kStage < kMaxStages ? room / C::kStage : kMaxStages;
     CUtensorMap ma, mw, ms;
     if (!make_maps<kBlock>(g, C::kBox, TW, ma, mw, ms)) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * p.split), 1, 1);
-    cfg.blockDim = dim3(kSwapThreads, 1, 1);
-    cfg.dynamicSmemBytes = 1024 + p.stages * C::kStage + reduce + kDrainWarps * kSwapEpi + kTailBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)p.split, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gemm_fp4_swap_kernel<CW, kBlock>, ma, mw, ms, p, reduce);
+    e = launch_dependent(gemm_fp4_swap_kernel<CW, kBlock>, dim3((unsigned)(clusters * p.split)), dim3(kSwapThreads),
+                         1024 + p.stages * C::kStage + reduce + kDrainWarps * kSwapEpi + kTailBytes, p.split, stream, ma, mw, ms, p,
+                         reduce);
     note_launch();
     return e;
 }
@@ -700,6 +693,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     const Groups groups{p.offsets, cum, p.rows, p.E, PT};
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    depend_wait();
     if (warp == 2) groups.scan(cum, lane);
     tc_fence_before();
     cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
@@ -926,7 +920,7 @@ template <int kBlock>
 cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream) {
     using C = PairCfg<kBlock>;
     int clusters = 0;
-    const cudaError_t e = pair_clusters<kBlock>(clusters);
+    cudaError_t e = pair_clusters<kBlock>(clusters);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mw, ms;
     if (!make_maps<kBlock>(g, PTH, C::kHalf, ma, mw, ms)) return cudaErrorInvalidValue;
@@ -937,9 +931,10 @@ cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
     if (tma_out && !make_tma_map_out(&my, g.y, g.type == Q8_F32 ? kMapF32 : kMapBF16, g.rows, g.N)) return cudaErrorInvalidValue;
     const PairArgs p{g.sfa, g.sa, g.sw, g.offsets, (int)g.rows, (int)g.E, (int)g.N, (int)g.K, (uint32_t)fp4_pitch(g.K, kBlock),
                      g.y, g.type, tma_out, (uint32_t)units};
-    gemm_fp4_pair_kernel<kBlock><<<2 * clusters, kPairThreads, C::kSmem, stream>>>(ma, mw, ms, my, p);
+    e = launch_dependent(gemm_fp4_pair_kernel<kBlock>, dim3((unsigned)(2 * clusters)), dim3(kPairThreads), C::kSmem, 0, stream, ma,
+                         mw, ms, my, p);
     note_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 // ------------------------------------------------------------------ weights on the MMA's M side, CTA pairs
@@ -1059,6 +1054,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     const Groups groups{p.offsets, cum, p.rows, p.E, TNP};
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    depend_wait();
     if (warp == 2) groups.scan(cum, lane);
     tc_fence_before();
     cluster_sync();   // barriers of both CTAs initialised, TMEM allocated in both
@@ -1260,7 +1256,7 @@ template <int kBlock>
 cudaError_t launch_wide(const Fp4Product& g, int64_t tiles, cudaStream_t stream) {
     using C = WideCfg<kBlock>;
     int clusters = 0;
-    const cudaError_t e = wide_clusters<kBlock>(clusters);
+    cudaError_t e = wide_clusters<kBlock>(clusters);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mw, ms;
     if (!make_maps<kBlock>(g, C::kBox, TW, ma, mw, ms)) return cudaErrorInvalidValue;
@@ -1272,9 +1268,10 @@ cudaError_t launch_wide(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
     if (tma_out && !make_tma_map_box(&my, g.y, size, g.rows, g.N, 32, 64 / size)) return cudaErrorInvalidValue;
     const PairArgs p{g.sfa, g.sa, g.sw, g.offsets, (int)g.rows, (int)g.E, (int)g.N, (int)g.K, (uint32_t)fp4_pitch(g.K, kBlock),
                      g.y, g.type, tma_out, (uint32_t)units};
-    gemm_fp4_wide_kernel<kBlock><<<2 * clusters, kPairThreads, C::kSmem, stream>>>(ma, mw, ms, my, p);
+    e = launch_dependent(gemm_fp4_wide_kernel<kBlock>, dim3((unsigned)(2 * clusters)), dim3(kPairThreads), C::kSmem, 0, stream, ma,
+                         mw, ms, my, p);
     note_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 template <int kBlock>

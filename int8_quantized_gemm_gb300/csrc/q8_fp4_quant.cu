@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p,
     constexpr int n = Vec32<T>::n, kLanes = kBlock / n;      // lanes that share a block: 1, 2 or 4
     constexpr int kUnroll = sizeof(T) == 4 ? 4 : 2;
     __shared__ uint32_t part[kMaxThreads / 32];
+    depend_wait();
     const uint32_t tx = threadIdx.x, lane = tx & 31;
     const int64_t slot_row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     // kTiles: rows in tiles of 128 of each matrix, past its end too (their scales are zero)
@@ -292,9 +293,9 @@ cudaError_t launch(Args a, int block, cudaStream_t stream) {
     if (ctas >= (1LL << 31)) return cudaErrorNotSupported;
     const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && a.ldx * sizeof(T) % 32 == 0;
     auto* kernel = block == 16 ? quantize_fp4_kernel<T, kForm, 16> : quantize_fp4_kernel<T, kForm, 32>;
-    kernel<<<(unsigned)ctas, dim3(tx, ty), 0, stream>>>(a, wide);
+    const cudaError_t e = launch_dependent(kernel, dim3((unsigned)ctas), dim3(tx, ty), 0, 0, stream, a, wide);
     note_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 template <int kForm>
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
                                                              const float* __restrict__ s, int block, uint64_t total,
                                                              uint32_t per_row, uint32_t pitch, uint32_t tile_rows,
                                                              T* __restrict__ y) {
+    depend_wait();
     const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= total) return;
     const uint2 c = __ldg(reinterpret_cast<const uint2*>(q) + i);
@@ -378,10 +380,10 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __re
 }
 
 template <class T>
-void dequantize(const uint8_t* q, const uint8_t* sf, const float* s, int block, uint64_t total, int64_t K, int64_t tile_rows,
+cudaError_t dequantize(const uint8_t* q, const uint8_t* sf, const float* s, int block, uint64_t total, int64_t K, int64_t tile_rows,
                 void* y, cudaStream_t stream) {
-    dequantize_fp4_kernel<T><<<(unsigned)((total + 255) / 256), 256, 0, stream>>>(
-        q, sf, s, block, total, (uint32_t)(K / 16), (uint32_t)fp4_pitch(K, block), (uint32_t)tile_rows, static_cast<T*>(y));
+    return launch_dependent(dequantize_fp4_kernel<T>, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, 0, stream, q, sf, s, block,
+                            total, (uint32_t)(K / 16), (uint32_t)fp4_pitch(K, block), (uint32_t)tile_rows, static_cast<T*>(y));
 }
 
 }  // namespace
@@ -410,12 +412,12 @@ cudaError_t launch_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const flo
                                   int64_t tile_rows, void* y, q8_float_type type, bool e4m3, cudaStream_t stream) {
     const uint64_t total = (uint64_t)rows * (uint64_t)(K / 16);
     if (total > 255ull << 31) return cudaErrorNotSupported;
-    if (e4m3) dequantize<uint8_t>(q, sf, s, block, total, K, tile_rows, y, stream);
-    else if (type == Q8_F32) dequantize<float>(q, sf, s, block, total, K, tile_rows, y, stream);
-    else if (type == Q8_BF16) dequantize<__nv_bfloat16>(q, sf, s, block, total, K, tile_rows, y, stream);
-    else dequantize<__half>(q, sf, s, block, total, K, tile_rows, y, stream);
+    const cudaError_t e = e4m3             ? dequantize<uint8_t>(q, sf, s, block, total, K, tile_rows, y, stream)
+                          : type == Q8_F32  ? dequantize<float>(q, sf, s, block, total, K, tile_rows, y, stream)
+                          : type == Q8_BF16 ? dequantize<__nv_bfloat16>(q, sf, s, block, total, K, tile_rows, y, stream)
+                                            : dequantize<__half>(q, sf, s, block, total, K, tile_rows, y, stream);
     note_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace q8

@@ -467,3 +467,37 @@ def test_layer_of_experts(q8, T, block):
         want = (weights.cpu().double()[:, :, None] * z.cpu().double()[slots.cpu().long()]).sum(1)
         size = (weights.cpu().double()[:, :, None] * z.cpu().double()[slots.cpu().long()].abs()).sum(1)
         assert ((y.cpu().double() - want).abs() <= 4 * 2.0 ** -24 * size + 1e-30).all()
+
+
+@pytest.mark.parametrize("block", BLOCKS)
+@pytest.mark.parametrize("M", [4, 24, 100, 3000])
+def test_kernels_that_start_early_wait(q8, M, block):
+    """Operands, scales, offsets and the result are rewritten right before and after each call on one stream, without a synchronisation
+    between them: every kernel sees what the one before it wrote."""
+    N, K, E = 1040, 1056, 3
+    xs = [ref.tokens(M, K, seed=i).cuda() for i in range(3)]
+    vs = [(ref.tokens(E * N, K, seed=10 + i) * 0.02).view(E, N, K).cuda() for i in range(3)]
+    offs = [torch.tensor(o, dtype=torch.int32).cuda() for o in ([0, M // 2, M // 2, M], [0, 0, M // 4, M], [0, M, M, M])]
+    want = []
+    for x, v, off in zip(xs, vs, offs):
+        a, w = q8.q8_quantize_fp4(x, block=block), q8.q8_quantize_weight_fp4(v, block=block)
+        torch.cuda.synchronize()
+        y = q8.q8_gemm_fp4_grouped(*a, *w, off, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        want.append((y, q8.q8_dequantize_fp4(a[0], a[1], a[2], out_dtype=torch.float32)))
+        torch.cuda.synchronize()
+    q, sf, s = q8.q8_quantize_fp4(xs[0], block=block)
+    qw, sfw, sw = q8.q8_quantize_weight_fp4(vs[0], block=block)
+    off, y, back = offs[0].clone(), torch.empty((M, N), device="cuda"), torch.empty((M, K), device="cuda")
+    for turn in range(12):
+        i = turn % 3
+        off.copy_(offs[i])
+        q8.q8_quantize_weight_fp4(vs[i], block=block, qw=qw, sfw=sfw, sw=sw)
+        q8.q8_quantize_fp4(xs[i], block=block, q=q, sf=sf, s=s)
+        q8.q8_gemm_fp4_grouped(q, sf, s, qw, sfw, sw, off, out_dtype=torch.float32, out=y)
+        q8.q8_dequantize_fp4(q, sf, s, out_dtype=torch.float32, out=back)
+        got = y.clone(), back.clone()
+        q8.q8_gemm_fp4_grouped(q, sf, s, qw, sfw, sw, off, out_dtype=torch.float32, out=y)
+        again = y.clone()
+        y.fill_(-1.0)
+        assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1]) and torch.equal(again, want[i][0])
