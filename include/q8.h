@@ -685,7 +685,7 @@ q8_status q8_quantize_weight_fp4(const void* w, q8_float_type type, int block, i
 /*
  * What codes stand for: y[m, k] = (q c) s in fp32, rounded to `type`. sf NULL: c = 1; s NULL: s = 1. tile_rows: 0 for block
  * scales of activations; N for those of weights [rows / N, N, K]. type Q8_E4M3: the codes' own values (each of them an
- * e4m3 number), with sf and s NULL. rows up to 2^40, rows * K / 16 up to 2^39 - 2^31.
+ * e4m3 number), with sf and s NULL. rows up to 2^40, rows * K / 32 up to 2^39 - 2^31.
  */
 q8_status q8_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const float* s, int block, int64_t rows, int64_t K,
                             int64_t tile_rows, void* y, q8_float_type type, q8_stream_t stream);

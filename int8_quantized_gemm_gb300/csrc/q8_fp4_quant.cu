@@ -115,16 +115,24 @@ struct Args {
     float* s;
 };
 
-// A row is held by blockDim.x threads, kUnroll vectors of 32 bytes each, all loads first; blockDim.y rows a CTA. Blocks of 16
-// need the row's maximum before the first code: rows of up to 512 threads' vectors (16384 elements) stay in registers, longer
-// ones are read a second time, from L2.
+// A row is held by blockDim.x threads, kUnroll vectors of 32 bytes each, all loads first; blockDim.y rows a CTA, some in a warp where
+// they are short. Blocks of 16 need the row's maximum before the first code: rows of up to 512 threads' vectors (32768 elements of 16
+// bits, 16384 of 32) stay in registers, as they were read; longer ones are read a second time, from L2.
+// Bound by memory. On the device, of the measured copy bandwidth: 8192 x 16384 fp32 91 us (0.99), bf16 51.5 (0.98; two vectors
+// a thread 66); 16384 x 4096 bf16 26.8 (0.95); the gated form, 32768 x 2048 bf16, 47.4 (0.95) with CTAs of 64 threads (48.0 with 128,
+// 49.5 with 256) and two vectors a thread (one 58); its fp32 form keeps one (42.6 us for 16384 x 2048, two 47, four 73: registers).
+template <class T, int kForm>
+struct Unroll { static constexpr int n = kForm == kGated ? (sizeof(T) == 4 ? 1 : 2) : 4; };
+
 template <class T, int kForm, int kBlock>
 __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p, bool wide) {
     constexpr int n = Vec32<T>::n, kLanes = kBlock / n;      // lanes that share a block: 1, 2 or 4
-    constexpr int kUnroll = sizeof(T) == 4 ? 4 : 2;
+    constexpr int kUnroll = Unroll<T, kForm>::n;
     __shared__ uint32_t part[kMaxThreads / 32];
     depend_wait();
-    const uint32_t tx = threadIdx.x, lane = tx & 31;
+    const uint32_t tx = threadIdx.x;
+    const int width = blockDim.x < 32 ? (int)blockDim.x : 32;     // lanes of a row in a warp: a power of two
+    const uint32_t lane = tx & 31;                                // within the row's lanes
     const int64_t slot_row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     // kTiles: rows in tiles of 128 of each matrix, past its end too (their scales are zero)
     int64_t row = slot_row;
@@ -140,9 +148,10 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p,
     const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.ldx;
     const uint32_t chunk = blockDim.x * kUnroll;
 
-    float f[kUnroll][n];
+    Vec32<T> v[kUnroll];                                          // as they were read,
+    float g[kForm == kGated ? kUnroll : 1][n];                    // or the activation
     auto load = [&](uint32_t v0) {
-        Vec32<T> v[kUnroll], u[kForm == kGated ? kUnroll : 1];
+        Vec32<T> u[kForm == kGated ? kUnroll : 1];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const uint32_t at = v0 + i * blockDim.x + tx;
@@ -154,58 +163,73 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p,
                 if constexpr (kForm == kGated) u[i].zero();
             }
         }
+        if constexpr (kForm == kGated) {
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            to_floats(v[i], f[i]);
-            if constexpr (kForm == kGated) {
+            for (int i = 0; i < kUnroll; ++i) {
                 float by[n], far = 0.0f;
+                to_floats(v[i], g[i]);
                 to_floats(u[i], by);
 #pragma unroll
-                for (int j = 0; j < n; j += 2) far = max_abs(far, f[i][j], f[i][j + 1]);
+                for (int j = 0; j < n; j += 2) far = max_abs(far, g[i][j], g[i][j + 1]);
                 if (far <= kGateFast) {
 #pragma unroll
-                    for (int j = 0; j < n; j += 2) silu_mul2(f[i][j], f[i][j + 1], by[j], by[j + 1]);
+                    for (int j = 0; j < n; j += 2) silu_mul2(g[i][j], g[i][j + 1], by[j], by[j + 1]);
                 } else {   // some gate of the thread's is far out, infinite or NaN: rare
 #pragma unroll
-                    for (int j = 0; j < n; ++j) f[i][j] = silu_mul_far(f[i][j], by[j]);
+                    for (int j = 0; j < n; ++j) g[i][j] = silu_mul_far(g[i][j], by[j]);
                 }
             }
+        }
+    };
+    auto values = [&](int i, float (&f)[n]) {
+        if constexpr (kForm == kGated) {
+#pragma unroll
+            for (int j = 0; j < n; ++j) f[j] = g[i][j];
+        } else {
+            to_floats(v[i], f);
         }
     };
     float most[kUnroll];   // of a thread's vector, then of its block
     auto maxima = [&]() {
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
+            float f[n];
+            values(i, f);
             most[i] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < n; j += 2) most[i] = max_abs(most[i], f[i][j], f[i][j + 1]);
+            for (int j = 0; j < n; j += 2) most[i] = max_abs(most[i], f[j], f[j + 1]);
         }
     };
 
     float r448 = 0.0f, r2688 = 0.0f, s = 0.0f;
     if constexpr (kBlock == 16) {
-        uint32_t m = 0;
+        float top = 0.0f;
         for (uint32_t v0 = 0; v0 < p.vecs; v0 += chunk) {
             load(v0);
             maxima();
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) m = max(m, __float_as_uint(most[i]));
+            for (int i = 0; i < kUnroll; ++i) top = max_abs(top, most[i], 0.0f);
         }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (blockDim.x > 32) {
-            const uint32_t warps = blockDim.x / 32;
-            uint32_t* own = part + threadIdx.y * warps;
-            if (lane == 0) own[tx / 32] = m;
-            __syncthreads();
-            m = lane < warps ? own[lane] : 0;
+        uint32_t m = __float_as_uint(top);
+        if (blockDim.x < 32) {
+            for (int d = 1; d < width; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        } else {
             m = __reduce_max_sync(0xffffffffu, m);
+            if (blockDim.x > 32) {
+                const uint32_t warps = blockDim.x / 32;
+                uint32_t* own = part + threadIdx.y * warps;
+                if (lane == 0) own[tx / 32] = m;
+                __syncthreads();
+                m = lane < warps ? own[lane] : 0;
+                m = __reduce_max_sync(0xffffffffu, m);
+            }
         }
         float a = __uint_as_float(m >= 0x7f800000u ? 0x7fffffffu : m);
         a = a < kFp8Tiny ? kFp8Tiny : a;   // a NaN stays
         const float d = __fdiv_rn(lane == 0 ? a : lane == 1 ? kFp8Max : kFp4RowMax, lane == 0 ? kFp4RowMax : a);
-        s = __shfl_sync(0xffffffffu, d, 0);
-        r448 = __shfl_sync(0xffffffffu, d, 1);
-        r2688 = __shfl_sync(0xffffffffu, d, 2);
+        s = __shfl_sync(0xffffffffu, d, 0, width);
+        r448 = __shfl_sync(0xffffffffu, d, 1, width);
+        r2688 = __shfl_sync(0xffffffffu, d, 2, width);
     }
 
     int to = -1;           // kSlots: lane j has the row's slot j
@@ -228,12 +252,13 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p,
                 most[i] = max_abs(most[i], o, 0.0f);
             }
             uint32_t c;
-            float up;
+            float up, f[n];
             if constexpr (kBlock == 16) scale16(most[i], r448, r2688, c, up);
             else scale32(most[i], c, up);
+            values(i, f);
             uint32_t code[n / 8];
 #pragma unroll
-            for (int j = 0; j < n / 8; ++j) code[j] = codes8(f[i] + 8 * j, up);
+            for (int j = 0; j < n / 8; ++j) code[j] = codes8(f + 8 * j, up);
             auto put = [&](int64_t dst) {
                 uint8_t* qd = p.q + (size_t)dst * (p.K / 2) + (size_t)at * (n / 2);
                 if constexpr (n == 16) *reinterpret_cast<uint2*>(qd) = make_uint2(code[0], code[n / 8 - 1]);
@@ -282,13 +307,14 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p,
 
 template <class T, int kForm>
 cudaError_t launch(Args a, int block, cudaStream_t stream) {
-    constexpr int n = Vec32<T>::n, kUnroll = sizeof(T) == 4 ? 4 : 2;
+    constexpr int n = Vec32<T>::n, kUnroll = Unroll<T, kForm>::n;
     a.vecs = a.K / n;
     const int64_t rows = kForm == kTiles ? a.rows_out : a.M;
     const uint32_t want = (a.vecs + kUnroll - 1) / kUnroll;
     uint32_t tx = (want + 31) / 32 * 32;
+    if (kForm != kSlots && want <= 16) tx = want <= 4 ? 4 : want <= 8 ? 8 : 16;   // several rows a warp; the slots take all of it
     if (tx > kMaxThreads) tx = kMaxThreads;
-    const uint32_t ty = tx >= 256 ? 1 : 256 / tx;
+    const uint32_t ty = tx >= 64 ? 1 : 64 / tx;
     const int64_t ctas = (rows + ty - 1) / ty;
     if (ctas >= (1LL << 31)) return cudaErrorNotSupported;
     const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && a.ldx * sizeof(T) % 32 == 0;
@@ -326,64 +352,100 @@ __device__ __forceinline__ void floats8(uint32_t c, float (&f)[8]) {
     }
 }
 
-// 16 codes a thread: they share one scale of either kind.
-template <class T>
-__global__ void __launch_bounds__(256) dequantize_fp4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
-                                                             const float* __restrict__ s, int block, uint64_t total,
-                                                             uint32_t per_row, uint32_t pitch, uint32_t tile_rows,
-                                                             T* __restrict__ y) {
-    depend_wait();
-    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(q) + i);
-    if constexpr (sizeof(T) == 1) {
-        *(reinterpret_cast<uint4*>(y) + i) =
-            make_uint4(e4m3x4(c.x), e4m3x4(c.x >> 16), e4m3x4(c.y), e4m3x4(c.y >> 16));
+// 32 bytes to y: at once where its rows start on them.
+__device__ __forceinline__ void put32(void* y, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(y), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
     } else {
-        float f[8], g[8];
-        floats8(c.x, f);
-        floats8(c.y, g);
-        if (sf || s) {
-            const uint64_t row = i / per_row;
-            const uint32_t b = (uint32_t)(i - row * per_row) * 16 / block;
-            float scale = 1.0f;
-            if (sf) {
-                size_t at = row * pitch + b;
-                if (tile_rows) {
-                    const uint64_t e = row / tile_rows;
-                    const uint32_t r = (uint32_t)(row - e * tile_rows);
-                    at = ((e * ((tile_rows + 127) / 128) + r / 128) * (pitch / 4) + b / 4) * 512 + (r % 32) * 16 +
-                         r % 128 / 32 * 4 + b % 4;
+        reinterpret_cast<uint4*>(y)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(y)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// 32 codes at a time, two of them a thread with both loads first: one scale of blocks of 32, two of blocks of 16. Bound by memory:
+// DEQ
+constexpr int kBack = 256, kBackUnroll = 2;
+template <class T>
+__global__ void __launch_bounds__(kBack) dequantize_fp4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
+                                                               const float* __restrict__ s, int block, uint64_t total,
+                                                               uint32_t per_row, uint32_t pitch, uint32_t tile_rows,
+                                                               T* __restrict__ y, bool wide) {
+    depend_wait();
+    const uint64_t first = (uint64_t)blockIdx.x * (kBack * kBackUnroll) + threadIdx.x;
+    uint4 c[kBackUnroll];
+#pragma unroll
+    for (int r = 0; r < kBackUnroll; ++r)
+        c[r] = first + r * kBack < total ? __ldg(reinterpret_cast<const uint4*>(q) + first + r * kBack) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < kBackUnroll; ++r) {
+        const uint64_t i = first + r * kBack;
+        if (i >= total) return;
+        const uint32_t w[4] = {c[r].x, c[r].y, c[r].z, c[r].w};
+        if constexpr (sizeof(T) == 1) {
+            uint32_t out[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                out[2 * j] = e4m3x4(w[j]);
+                out[2 * j + 1] = e4m3x4(w[j] >> 16);
+            }
+            put32(y + i * 32, out, wide);
+        } else {
+            float scale[2] = {1.0f, 1.0f}, by = 1.0f;
+            if (sf || s) {
+                const uint64_t row = i / per_row;
+                const uint32_t k = (uint32_t)(i - row * per_row) * 32;
+                if (sf) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t b = (k + 16 * h) / block;
+                        size_t at = row * pitch + b;
+                        if (tile_rows) {
+                            const uint64_t e = row / tile_rows;
+                            const uint32_t n = (uint32_t)(row - e * tile_rows);
+                            at = ((e * ((tile_rows + 127) / 128) + n / 128) * (pitch / 4) + b / 4) * 512 + (n % 32) * 16 +
+                                 n % 128 / 32 * 4 + b % 4;
+                        }
+                        const uint32_t v = __ldg(sf + at);
+                        // 2^-127 is subnormal: its bit is below the exponent's
+                        scale[h] = block == 16 ? of_e4m3(v) : v == 255u ? __uint_as_float(0x7fffffffu)
+                                                                         : __uint_as_float(v ? v << 23 : 0x400000u);
+                    }
                 }
-                const uint32_t v = __ldg(sf + at);
-                // 2^-127 is subnormal: its bit is below the exponent's
-                scale = block == 16 ? of_e4m3(v) : v == 255u ? __uint_as_float(0x7fffffffu)
-                                                              : __uint_as_float(v ? v << 23 : 0x400000u);
+                if (s) by = __ldg(s + row);
             }
-            const float by = s ? __ldg(s + row) : 1.0f;
+            constexpr int kPer = 32 / sizeof(T);       // values of a store
+            uint32_t out[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f[j] = __fmul_rn(__fmul_rn(f[j], scale), by);
-                g[j] = __fmul_rn(__fmul_rn(g[j], scale), by);
+            for (int j = 0; j < 4; ++j) {
+                float f[8];
+                floats8(w[j], f);
+#pragma unroll
+                for (int l = 0; l < 8; ++l) {
+                    const float v = __fmul_rn(__fmul_rn(f[l], scale[j / 2]), by);
+                    if constexpr (sizeof(T) == 4) {
+                        out[l] = __float_as_uint(v);
+                    } else {
+                        const T t = from_float<T>(v);
+                        const uint32_t bits = *reinterpret_cast<const uint16_t*>(&t);
+                        uint32_t& word = out[(j % 2) * 4 + l / 2];
+                        word = l % 2 ? word | bits << 16 : bits;
+                    }
+                }
+                if (sizeof(T) == 4 || j % 2) put32(y + i * 32 + (sizeof(T) == 4 ? j : j / 2) * kPer, out, wide);
             }
         }
-        T out[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            out[j] = from_float<T>(f[j]);
-            out[8 + j] = from_float<T>(g[j]);
-        }
-        uint4* to = reinterpret_cast<uint4*>(y + i * 16);
-#pragma unroll
-        for (int j = 0; j < (int)sizeof(T); ++j) to[j] = reinterpret_cast<const uint4*>(out)[j];
     }
 }
 
 template <class T>
 cudaError_t dequantize(const uint8_t* q, const uint8_t* sf, const float* s, int block, uint64_t total, int64_t K, int64_t tile_rows,
-                void* y, cudaStream_t stream) {
-    return launch_dependent(dequantize_fp4_kernel<T>, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, 0, stream, q, sf, s, block,
-                            total, (uint32_t)(K / 16), (uint32_t)fp4_pitch(K, block), (uint32_t)tile_rows, static_cast<T*>(y));
+                       void* y, cudaStream_t stream) {
+    const uint64_t per = kBack * kBackUnroll;
+    return launch_dependent(dequantize_fp4_kernel<T>, dim3((unsigned)((total + per - 1) / per)), dim3(kBack), 0, 0, stream, q, sf, s,
+                            block, total, (uint32_t)(K / 32), (uint32_t)fp4_pitch(K, block), (uint32_t)tile_rows,
+                            static_cast<T*>(y), reinterpret_cast<uintptr_t>(y) % 32 == 0);
 }
 
 }  // namespace
@@ -410,7 +472,7 @@ cudaError_t launch_quantize_weight_fp4(const void* w, q8_float_type t, int block
 
 cudaError_t launch_dequantize_fp4(const uint8_t* q, const uint8_t* sf, const float* s, int block, int64_t rows, int64_t K,
                                   int64_t tile_rows, void* y, q8_float_type type, bool e4m3, cudaStream_t stream) {
-    const uint64_t total = (uint64_t)rows * (uint64_t)(K / 16);
+    const uint64_t total = (uint64_t)rows * (uint64_t)(K / 32);
     if (total > 255ull << 31) return cudaErrorNotSupported;
     const cudaError_t e = e4m3             ? dequantize<uint8_t>(q, sf, s, block, total, K, tile_rows, y, stream)
                           : type == Q8_F32  ? dequantize<float>(q, sf, s, block, total, K, tile_rows, y, stream)
