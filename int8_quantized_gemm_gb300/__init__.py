@@ -889,6 +889,14 @@ def _fp4_codes(rows: int, K: int, block: int, q, sf, s, like: torch.Tensor, devi
         raise ValueError("block must be 16 or 32")
     if K % 32:
         raise ValueError("the number of columns must be a multiple of 32")
+    if q is None and sf is None and s is None and stream is None:      # the common call, straight
+        on = like.device
+        q = torch.empty((rows, K >> 1), dtype=torch.uint8, device=on)
+        sf = torch.empty((rows, -(-K // FP4_SPAN) * (FP4_SPAN // block)), dtype=kind, device=on)
+        if block == 32:
+            return q, sf, None, q.data_ptr(), sf.data_ptr(), None
+        s = torch.empty(rows, dtype=torch.float32, device=on)
+        return q, sf, s, q.data_ptr(), sf.data_ptr(), s.data_ptr()
     q, pq = _out(q, (rows, K // 2), torch.uint8, like, device, stream, "q")
     sf, psf = _out(sf, (rows, _fp4_pitch(K, block)), kind, like, device, stream, "sf")
     if block == 32:
@@ -988,7 +996,16 @@ def q8_dequantize_fp4(q: torch.Tensor, sf=None, s=None, out_dtype=torch.bfloat16
         raise TypeError("out_dtype must be torch.float32, torch.bfloat16, torch.float16 or torch.float8_e4m3fn")
     if kind == 3 and (sf is not None or s is not None):
         raise ValueError("float8 holds the codes alone, without scales")
-    lead, N, K, dev = tuple(q.shape[:-2]), q.shape[-2], 2 * q.shape[-1], q.get_device()
+    dev = q.get_device()
+    if sf is None and s is None:                                       # the codes alone
+        shape = (*q.shape[:-1], 2 * q.shape[-1])
+        out, py = _out(out, shape, out_dtype, q, dev, stream, "out")
+        status = (_lib or load()).q8_dequantize_fp4(q.data_ptr(), None, None, 16, q.numel() // max(1, q.shape[-1]), shape[-1], 0, py,
+                                                    kind, _handle(dev, stream))
+        if status:
+            _check(status, "q8_dequantize_fp4")
+        return out
+    lead, N, K = tuple(q.shape[:-2]), q.shape[-2], 2 * q.shape[-1]
     rows, block, tile_rows, psf, ps = (lead[0] * N if lead else N), 16, 0, None, None
     if sf is not None:
         block = _BLOCKS.get(sf.dtype) if isinstance(sf, torch.Tensor) else None
@@ -1009,10 +1026,13 @@ def q8_dequantize_fp4(q: torch.Tensor, sf=None, s=None, out_dtype=torch.bfloat16
 
 def _fp4_operands(qa, sfa, sa, qw, sfw, sw, ndim, out_dtype, out, stream):
     """Addresses and sizes of a product: (device, M, N, K, block, addresses of qa, sfa, sa, qw, sfw, sw and out, type, out)."""
-    for t, name, dims in ((qa, "qa", 2), (qw, "qw", ndim)):
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or not t.is_cuda or t.dim() != dims or not t.is_contiguous():
-            _need(t, torch.uint8, name, dims)
-    block = _BLOCKS.get(sfa.dtype) if isinstance(sfa, torch.Tensor) else None
+    u8 = torch.uint8
+    if not isinstance(qa, torch.Tensor) or qa.dtype is not u8 or not qa.is_cuda or qa.dim() != 2 or not qa.is_contiguous():
+        _need(qa, u8, "qa", 2)
+    if not isinstance(qw, torch.Tensor) or qw.dtype is not u8 or not qw.is_cuda or qw.dim() != ndim or not qw.is_contiguous():
+        _need(qw, u8, "qw", ndim)
+    scales = sfa.dtype if isinstance(sfa, torch.Tensor) else None
+    block = _BLOCKS.get(scales)
     if block is None:
         raise TypeError("sfa must be float8_e4m3fn (blocks of 16) or float8_e8m0fnu (blocks of 32)")
     M, half = qa.shape
@@ -1026,11 +1046,15 @@ def _fp4_operands(qa, sfa, sa, qw, sfw, sw, ndim, out_dtype, out, stream):
     dev = qa.get_device()
     if qw.get_device() != dev:
         raise ValueError(f"qw is on {qw.device}, not on cuda:{dev}")
-    lead, pitch = tuple(shape[:-2]), _fp4_pitch(K, block)
-    psfa = _dense(sfa, sfa.dtype, (M, pitch), dev, "sfa")
-    psfw = _dense(sfw, sfa.dtype, (*lead, -(-N // 128), pitch // 4, 32, 4, 4), dev, "sfw")
+    pitch = -(-K // FP4_SPAN) * (FP4_SPAN // block)
+    psfa = _dense(sfa, scales, (M, pitch), dev, "sfa")
+    if ndim == 2:
+        psfw = _dense(sfw, scales, (-(-N // 128), pitch >> 2, 32, 4, 4), dev, "sfw")
+        psw = None if sw is None else _dense(sw, torch.float32, (N,), dev, "sw")
+    else:
+        psfw = _dense(sfw, scales, (shape[0], -(-N // 128), pitch >> 2, 32, 4, 4), dev, "sfw")
+        psw = None if sw is None else _dense(sw, torch.float32, (shape[0], N), dev, "sw")
     psa = None if sa is None else _dense(sa, torch.float32, (M,), dev, "sa")
-    psw = None if sw is None else _dense(sw, torch.float32, (*lead, N), dev, "sw")
     out, py = _out(out, (M, N), out_dtype, qa, dev, stream, "out")
     return dev, M, N, K, block, qa.data_ptr(), psfa, psa, qw.data_ptr(), psfw, psw, py, kind, out
 
