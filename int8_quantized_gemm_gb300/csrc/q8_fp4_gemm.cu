@@ -948,6 +948,7 @@ cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 //   warps 2, 3 scales of the tile's tokens, every other stage each
 //   warps 4-11 drain: a TMEM lane is a weight row (a column of y); two warps for each quarter of the lanes, 64 tokens each
 constexpr int TWP = 256, TNP = 128;               // weight rows of a tile, token rows at most
+constexpr int kWideEpi = 2048;                    // of a drain warp
 
 template <int kBlock>
 struct WideCfg {
@@ -959,14 +960,14 @@ struct WideCfg {
     static constexpr int kOffSfa = kOffSfw + S::kBytes;
     static constexpr int kStage = kOffSfa + S::kBytes;
     static_assert(kStage % 1024 == 0 && kHalf % kBox == 0, "swizzled tiles start on 1024 bytes");
-    static constexpr int kStages = 6;
+    static constexpr int kStages = 7;
     static constexpr int kBufs = 2;                           // accumulator buffers, beside the scales' columns
     static constexpr uint32_t kId0 = idesc_fp4(TWP, 0, kBlock, 0), kId2 = idesc_fp4(TWP, 0, kBlock, 2);   // N is added
     static constexpr int kScaleCols = 2 * S::kCols;           // weights, then tokens
     static constexpr int kTmemScales = kBufs * TNP;
     static_assert(kTmemScales + 2 * kScaleCols <= 512, "above the tensor memory");
     static constexpr int kOffEpi = kStages * kStage;
-    static constexpr int kOffTok = kOffEpi + kPairDrain * kPairEpi;     // the tokens' row scales
+    static constexpr int kOffTok = kOffEpi + kPairDrain * kWideEpi;     // the tokens' row scales
     static constexpr int kOffBar = kOffTok + TNP * 4;
     static constexpr int kBars = 2 * kStages + 2 * kBufs;
     static constexpr int kSmem = 1024 + kOffBar + 8 * kBars + 32 + 4 * (kMaxExperts + 2);
@@ -974,7 +975,7 @@ struct WideCfg {
 };
 
 // acc[j]: weight row (column of y) col0 + lane, token t0 + j; y's rows are whole 16-byte chunks. 2 KB of tokens x 32 columns at a
-// time are turned round in shared memory (two buffers) and leave by TMA, the last tokens of an expert 16 bytes a lane.
+// time are turned round in shared memory and leave by TMA, the last tokens of an expert 16 bytes a lane.
 template <class T, int NC>
 __device__ __forceinline__ void store_columns(const CUtensorMap* map, T* y, int row, int live, int col0, int N,
                                               const float (&acc)[NC], uint32_t buf, int lane) {
@@ -984,25 +985,21 @@ __device__ __forceinline__ void store_columns(const CUtensorMap* map, T* y, int 
 #pragma unroll
     for (int c = 0; c < NC / kTokens; ++c) {
         if (c * kTokens >= live) break;
-        const uint32_t at = buf + (c & 1) * 2048;
-        if (lane == 0) {   // the buffer has left: of the tile before, or of the step before the last
-            if (c == 0) bulk_wait_read_all();
-            else asm volatile("cp.async.bulk.wait_group.read 1;\n" ::: "memory");
-        }
+        if (lane == 0) bulk_wait_read_all();      // the step before has left the buffer
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kTokens; ++j) {
             const T v = from_float<T>(acc[c * kTokens + j]);
             if constexpr (sizeof(T) == 2)
-                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(at + j * kRow + lane * 2), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 2), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
             else
-                asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(at + j * kRow + lane * 4), "r"(__float_as_uint(acc[c * kTokens + j])) : "memory");
+                asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 4), "r"(__float_as_uint(acc[c * kTokens + j])) : "memory");
         }
         if (live - c * kTokens >= kTokens) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_2d(map, at, col0, row + c * kTokens);
+                tma_store_2d(map, buf, col0, row + c * kTokens);
                 bulk_commit();
             }
         } else {
@@ -1011,7 +1008,7 @@ __device__ __forceinline__ void store_columns(const CUtensorMap* map, T* y, int 
             for (int r = lane / kLanes; r < live - c * kTokens; r += kPass)
                 if (col < N)
                     *reinterpret_cast<uint4*>(y + (int64_t)(row + c * kTokens + r) * N + col) =
-                        lds128(at + r * kRow + lane % kLanes * 16);
+                        lds128(buf + r * kRow + lane % kLanes * 16);
         }
     }
 }
@@ -1165,7 +1162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t tlane = tmem_base + ((uint32_t)(quarter * 32) << 16) + t0;
         const uint32_t free_bar = mapa_shared(bar_accempty, 0);
         float* token_scales = reinterpret_cast<float*>(smem + C::kOffTok) + t0;   // of the four warps of these tokens
-        const uint32_t epi = sbase + C::kOffEpi + (warp - 4) * kPairEpi;
+        const uint32_t epi = sbase + C::kOffEpi + (warp - 4) * kWideEpi;
         const int own = quarter * 32 + lane;           // its token's scale; its weight row in the CTA's half
         uint32_t buf = 0, bphase = 0;
         // A tile's place and this thread's part of its scales. They are fetched while the tile before is written out.
@@ -1285,21 +1282,27 @@ cudaError_t launch(const Fp4Product& p, cudaStream_t stream) {
     const int64_t most = p.offsets ? 4 * per : per;
     if (most <= 16) return launch_swap<8, kBlock>(p, tiles(16), stream);
     if (most <= 32) return launch_swap<16, kBlock>(p, tiles(32), stream);
-    // What a round of tiles takes, in us, as measured: 0.28 a stage and 1.0 for 256 x 128 tiles over 76 pairs, 0.31 and 1.6 for 256 x
-    // 256; a group's last tile is half full on average. Weights that are not in L2 take their time to be read whatever the tile, and the
-    // smaller one waits less for them.
+    // What a round of tiles takes, in us, as measured (a stage, and a fixed part): 0.27 and 0.3 for 128 weight rows x 32 tokens over 152
+    // CTAs, 0.24 (0.20 for up to 64 tokens) and 1.0 for 256 x 128 over 76 pairs, 0.31 and 1.6 for 256 x 256; and once for each kernel
+    // 4.2, 5 and 6. A group's last tile is half full on average. Weights that are not in L2 take their time to be read whatever the
+    // tile, and the pairs with the smaller one wait less for them. Measured, us, in the same order: 128x2048x2048 6.7 / 8.4 / 9.1;
+    // 64x8192x8192 13.1 / 12.1 / 15.0; 256x8192x8192 39 / 13.9 / 16.6; 512x8192x8192 - / 23.3 / 18.3; 2050 rows of 32 experts,
+    // 4096x2048, 55 / 34.6 / 35.7; 8192 rows of 8, 4096x4096, - / 74 / 53.
     int narrow = 0, wide = 0;
     cudaError_t e = wide_clusters<kBlock>(narrow);
     if (e == cudaSuccess) e = pair_clusters<kBlock>(wide);
     if (e != cudaSuccess) return e;
-    auto rounds = [&](int tn, int pairs) {
+    auto rounds = [&](int tn, int weights, int places) {
         const int64_t t = p.offsets ? p.rows / tn + (p.E < p.rows ? p.E : p.rows) / 2 + 1 : (p.rows + tn - 1) / tn;
-        return (double)((t * ((p.N + PN - 1) / PN) + pairs - 1) / pairs);
+        return (double)((t * ((p.N + weights - 1) / weights) + places - 1) / places);
     };
     const double memory = (double)(p.E < p.rows ? p.E : p.rows) * (double)p.N * (double)p.K * (0.5 + 1.0 / kBlock) / 6.5e6;
-    const double small = rounds(TNP, narrow) * (0.28 * (double)KB + 1.0) + 5.0;
-    const double large = rounds(PT, wide) * (0.31 * (double)KB + 1.6) + 6.0;
-    if (small <= (large > memory ? large : memory)) return launch_wide<kBlock>(p, tiles(TNP), stream);
+    auto least = [&](double us) { return us > memory ? us : memory; };
+    const double slim = least(rounds(32, TW, 2 * narrow) * (0.27 * (double)KB + 0.3) + 4.2);
+    const double small = least(rounds(TNP, TWP, narrow) * ((per > 64 ? 0.24 : 0.20) * (double)KB + 1.0) + 5.0);
+    const double large = least(rounds(PT, PN, wide) * (0.31 * (double)KB + 1.6) + 6.0);
+    if (slim < small && slim < large) return launch_swap<16, kBlock>(p, tiles(32), stream);
+    if (small <= large) return launch_wide<kBlock>(p, tiles(TNP), stream);
     return launch_pair<kBlock>(p, tiles(PT), stream);
 }
 
