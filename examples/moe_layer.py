@@ -1,6 +1,7 @@
-"""A layer of routed experts with float8 weights, from one decoded token to a prefill batch.
+"""A layer of routed experts with float8 or 4-bit weights, from one decoded token to a prefill batch.
 
   python examples/moe_layer.py [--experts 64] [--top-k 8] [--hidden 4096] [--inter 2048] [--tokens 1,16,256,4096]
+                               [--format fp8 | fp4-16 | fp4-32]
 
 Router (sigmoid scores, a balance bias), the experts' rows, tokens quantized into them, gate/up product,
 gated activation with quantization, down product, weighted sum back: seven calls of the library, no
@@ -18,11 +19,62 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import int8_quantized_gemm_gb300 as q8  # noqa: E402
 
 
+class Float8:
+    """e4m3 codes, a scale for each block of 128."""
+    name, bits, off = "e4m3", 8, 2.0 ** -4       # half a step of a code, relative
+
+    def weights(self, w):
+        return q8.q8_quantize_weight_fp8(w)
+
+    def tokens(self, x, slots):
+        return q8.q8_quantize_fp8(x, slots=slots)
+
+    def gated(self, h):
+        return q8.q8_swiglu_quantize_fp8(h)
+
+    def product(self, tokens, weights, offsets, dtype):
+        return q8.q8_gemm_fp8_grouped(*tokens, *weights, offsets, out_dtype=dtype)
+
+    def values(self, weights, e):
+        """One expert's weights in 64 bits."""
+        q, s = weights
+        full = s[e].double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+        return q[e].double() * full[:q.shape[1], :q.shape[2]]
+
+
+class Float4:
+    """e2m1 codes, a scale for each block of 16 or 32."""
+    name, off = "e2m1", 2.0 ** -2                # half a step between 1 and 2, the coarsest relative one
+
+    def __init__(self, block):
+        self.block, self.bits = block, 4 + 8 / block
+
+    def weights(self, w):
+        return q8.q8_quantize_weight_fp4(w, block=self.block)
+
+    def tokens(self, x, slots):
+        return q8.q8_quantize_fp4(x, block=self.block, slots=slots)
+
+    def gated(self, h):
+        return q8.q8_swiglu_quantize_fp4(h, block=self.block)
+
+    def product(self, tokens, weights, offsets, dtype):
+        return q8.q8_gemm_fp4_grouped(*tokens, *weights, offsets, out_dtype=dtype)
+
+    def values(self, weights, e):
+        q, sf, s = weights
+        return q8.q8_dequantize_fp4(q[e], sf[e], None if s is None else s[e], out_dtype=torch.float32).double()
+
+
+FORMATS = {"fp8": Float8, "fp4-16": lambda: Float4(16), "fp4-32": lambda: Float4(32)}
+
+
 class MoeLayer:
-    def __init__(self, w13: torch.Tensor, w2: torch.Tensor, bias: torch.Tensor, top_k: int):
-        """w13 [E, 2 I, H] (gate rows, then up rows), w2 [E, H, I], bias fp32 [E]."""
-        self.w13 = q8.q8_quantize_weight_fp8(w13)
-        self.w2 = q8.q8_quantize_weight_fp8(w2)
+    def __init__(self, w13: torch.Tensor, w2: torch.Tensor, bias: torch.Tensor, top_k: int, fmt=None):
+        """w13 [E, 2 I, H] (gate rows, then up rows), w2 [E, H, I], bias fp32 [E]; fmt: one of FORMATS' (default float8)."""
+        self.fmt = fmt or Float8()
+        self.w13 = self.fmt.weights(w13)
+        self.w2 = self.fmt.weights(w2)
         self.bias, self.top_k, self.experts = bias, top_k, w13.shape[0]
 
     def route(self, logits):
@@ -32,10 +84,8 @@ class MoeLayer:
         """x [T, H] bf16 or fp16, logits [T, E] -> [T, H]."""
         idx, weights = self.route(logits)
         offsets, slots = q8.q8_moe_plan(idx, self.experts)
-        qa, sa = q8.q8_quantize_fp8(x, slots=slots)
-        h = q8.q8_gemm_fp8_grouped(qa, sa, *self.w13, offsets, out_dtype=x.dtype)
-        qh, sh = q8.q8_swiglu_quantize_fp8(h)
-        return q8.q8_moe_combine(q8.q8_gemm_fp8_grouped(qh, sh, *self.w2, offsets, out_dtype=x.dtype), slots, weights)
+        h = self.fmt.product(self.fmt.tokens(x, slots), self.w13, offsets, x.dtype)
+        return q8.q8_moe_combine(self.fmt.product(self.fmt.gated(h), self.w2, offsets, x.dtype), slots, weights)
 
     def exact(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """The layer for a few tokens in 64 bits, without the quantization of the activations."""
@@ -44,14 +94,9 @@ class MoeLayer:
         for t in range(x.shape[0]):
             for e, w in zip(idx[t].tolist(), weights[t].double()):
                 if e >= 0:
-                    gate, up = (_values(*self.w13, e) @ x[t].double()).chunk(2)
-                    y[t] += w * (_values(*self.w2, e) @ (gate * torch.sigmoid(gate) * up))
+                    gate, up = (self.fmt.values(self.w13, e) @ x[t].double()).chunk(2)
+                    y[t] += w * (self.fmt.values(self.w2, e) @ (gate * torch.sigmoid(gate) * up))
         return y
-
-
-def _values(q, s, e):
-    full = s[e].double().repeat_interleave(128, 0).repeat_interleave(128, 1)
-    return q[e].double() * full[:q.shape[1], :q.shape[2]]
 
 
 def timed(layer, x, logits, replays=20):
@@ -71,20 +116,22 @@ def timed(layer, x, logits, replays=20):
     return y, start.elapsed_time(end) * 1e3 / replays
 
 
-def main(argv=None):
+def run(argv=None):
+    """(the largest distance from 64 bits, what the format allows it to be)."""
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     p.add_argument("--experts", type=int, default=64)
     p.add_argument("--top-k", type=int, default=8)
     p.add_argument("--hidden", type=int, default=4096)
     p.add_argument("--inter", type=int, default=2048)
     p.add_argument("--tokens", default="1,16,256,4096")
+    p.add_argument("--format", choices=sorted(FORMATS), default="fp8")
     p.add_argument("--hbm-gbs", type=float, default=6781.8, help="copy bandwidth the weights' time is taken at")
     a = p.parse_args(argv)
     g = torch.Generator(device="cuda").manual_seed(0)
     E, H, I = a.experts, a.hidden, a.inter
     w13 = torch.randn((E, 2 * I, H), generator=g, device="cuda", dtype=torch.bfloat16) * H ** -0.5
     w2 = torch.randn((E, H, I), generator=g, device="cuda", dtype=torch.bfloat16) * I ** -0.5
-    layer = MoeLayer(w13, w2, 0.1 * torch.randn(E, generator=g, device="cuda"), a.top_k)
+    layer = MoeLayer(w13, w2, 0.1 * torch.randn(E, generator=g, device="cuda"), a.top_k, FORMATS[a.format]())
     del w13, w2
     worst = 0.0
     for T in (int(v) for v in a.tokens.split(",")):
@@ -96,13 +143,18 @@ def main(argv=None):
         off = float((y[:few].double() - want).norm() / want.norm())
         worst = max(worst, off)
         active = int(torch.unique(layer.route(logits)[0]).numel())
-        floor = active * 3 * H * I / a.hbm_gbs / 1e3
+        floor = active * 3 * H * I * layer.fmt.bits / 8 / a.hbm_gbs / 1e3
         print(f"{T:6d} tokens: {us:9.1f} us a layer, {active} experts' weights {floor:7.1f} us, "
-              f"off from 64 bits {off:.4f} (activations in e4m3)")
+              f"off from 64 bits {off:.4f} (activations in {layer.fmt.name})")
     assert q8.q8_device_error() == 0
-    return worst
+    return worst, layer.fmt.off
+
+
+def main(argv=None):
+    return run(argv)[0]
 
 
 if __name__ == "__main__":
-    # two roundings of activations to e4m3 (2^-4 at most, 2^-5.8 on average, each) and bf16 outputs
-    sys.exit(0 if main() < 2.0 ** -4 else 1)
+    # two roundings of activations (e4m3: 2^-4 at most, 2^-5.8 on average, each; e2m1: 2^-2 and 2^-3.4) and bf16 outputs
+    worst, most = run()
+    sys.exit(0 if worst < most else 1)

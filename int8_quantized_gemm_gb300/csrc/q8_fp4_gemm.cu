@@ -960,7 +960,7 @@ struct WideCfg {
     static constexpr int kOffSfa = kOffSfw + S::kBytes;
     static constexpr int kStage = kOffSfa + S::kBytes;
     static_assert(kStage % 1024 == 0 && kHalf % kBox == 0, "swizzled tiles start on 1024 bytes");
-    static constexpr int kStages = 7;
+    static constexpr int kStages = 6;                         // five or seven: 2 % slower for 128x8192x8192
     static constexpr int kBufs = 2;                           // accumulator buffers, beside the scales' columns
     static constexpr uint32_t kId0 = idesc_fp4(TWP, 0, kBlock, 0), kId2 = idesc_fp4(TWP, 0, kBlock, 2);   // N is added
     static constexpr int kScaleCols = 2 * S::kCols;           // weights, then tokens
