@@ -647,7 +647,8 @@ q8_status q8_gemm_fp8_grouped(const uint8_t* qa, const float* sa, const uint8_t*
  *       written as zeros and not read;
  *   of weights, sfw[E, ceil(N / 128), P / 4, 32, 4, 4]: block b of row n at [n / 128][b / 4][n % 32][n % 128 / 32][b % 4], the
  *       order in which the tensor core takes them; zeros where there is no row n or no block b.
- * All of these arrays are 16-byte aligned. NaN and infinities are passed on, as by the float8 operators.
+ * Block scales have no sign (a product does not look at it). All of these arrays are 16-byte aligned. NaN and infinities are passed
+ * on, as by the float8 operators.
  */
 
 /*

@@ -42,9 +42,9 @@ cudaError_t read_and_clear_gemm_fp4_error(uint32_t* code);
 
 #ifdef __CUDACC__
 // The kernels of these operators may start while the one before them on the stream still runs (programmatic stream
-// serialization): each touches global memory only after depend_wait(), which returns once that kernel has completed and its writes
-// can be seen, and then lets the next one start. What overlaps is the set-up and the launch (128x8192x8192 13.4 -> 12.5 us, 2050 rows
-// of 32 experts 34.3 -> 32.8, called one after another).
+// serialization): each touches global memory only after depend_wait(), which returns once that kernel has completed and its
+// writes can be seen, and then lets the next one start. What overlaps is the set-up and the launch (128x8192x8192 13.4 ->
+// 12.5 us, 2050 rows of 32 experts 34.3 -> 32.8, called one after another).
 __device__ __forceinline__ void depend_wait() {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");

@@ -47,7 +47,8 @@ q8_status gemm_fp4(const q8::Fp4Product& p, int block, q8_stream_t stream) {
     // be a number too (rows of a tile up to 256, and as many again of the tokens; 256 K of a stage).
     if (p.rows > INT32_MAX - 1024 || p.K > INT32_MAX - 2 * q8::kFp4Span) return Q8_ERR_UNSUPPORTED;
     if (!in_range(p.N) || (p.E > 0 && p.N > (INT32_MAX - 1024) / p.E)) return Q8_ERR_UNSUPPORTED;
-    // So are the weights' tiles of scales, as rows of 128 bytes, 16 for each 128 weight rows and 256 K (two weight tiles at a time).
+    // So are the weights' tiles of scales, as rows of 128 bytes, 16 for each 128 weight rows and 256 K (two weight tiles
+    // at a time).
     const int64_t NB = (p.N + 127) / 128, KB = (p.K + q8::kFp4Span - 1) / q8::kFp4Span;
     if (KB > 0 && p.E * NB + 2 > INT32_MAX / (16 * KB)) return Q8_ERR_UNSUPPORTED;
     if (p.rows == 0 || p.N == 0 || p.E == 0) return Q8_OK;

@@ -66,7 +66,9 @@ struct TokenScales {
             }
         }
     }
-    __device__ __forceinline__ static uint32_t word(const uint4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
+    __device__ __forceinline__ static uint32_t word(const uint4& v, int k) {
+        return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+    }
     // `groups`: scales of a row from this stage on; those past the end are not read as numbers (zero codes meet them)
     __device__ __forceinline__ void store(uint32_t dst, int groups, int lane) const {
 #pragma unroll
@@ -81,11 +83,11 @@ struct TokenScales {
     }
 };
 
-// One of two scale warps (which = 0, 1: every other stage, so that each has two stages' time for the way from a free stage to a full
-// one; pairs of stages a warp, which share a sector of the rows' scales, were 15 % slower with 128 tokens): the stages kb0 .. kb1 - 1
-// of one tile. `s`, `phase`: the ring's state at
-// kb0, moved on; `free_bar`: base of the barriers that a stage is free; `put(s)`: address of stage s's tiles; `done(s)`: arrival.
-// Two stages of its own are loaded ahead. False when a wait gave up.
+// One of two scale warps (which = 0, 1: every other stage, so that each has two stages' time for the way from a free stage to
+// a full one; pairs of stages a warp, which share a sector of the rows' scales, were 15 % slower with 128 tokens): the stages
+// kb0 .. kb1 - 1 of one tile. `s`, `phase`: the ring's state at kb0, moved on; `free_bar`: base of the barriers that a stage
+// is free; `put(s)`: address of stage s's tiles; `done(s)`: arrival. Two stages of its own are loaded ahead. False when a
+// wait gave up.
 template <int kBlock, int J, class Put, class Done>
 __device__ __forceinline__ bool feed_scales(const uint8_t* sf, int64_t row0, int n, uint32_t pitch, int groups, int kb0, int kb1,
                                             uint32_t& count, int which, int stages, uint32_t& s, uint32_t& phase,
@@ -130,20 +132,32 @@ __device__ __forceinline__ bool feed_scales(const uint8_t* sf, int64_t row0, int
 //   warp 1     MMA issuer (N = n rounded up to 16), TMEM
 //   warps 2, 3 scales of the stage's tokens, every other stage each
 //   warps 4-11 drain: two warps for each quarter of the TMEM lanes (weight rows), half of the tokens each
-// With few tiles, a cluster of S CTAs splits a tile's stages; each CTA sends the partial sums of the
-// tokens it does not own to the CTA that does (st.async), which adds them in the order of the ranks:
-// the same bits every time, no workspace and no second launch.
+// With few tiles, a cluster of S CTAs splits a tile's stages; each CTA sends the partial sums of the tokens it does not own
+// to the CTA that does (st.async), which adds them in the order of the ranks: the same bits every time, no workspace and no
+// second launch. Measured, called one after another: 16x28672x8192 24.5 us (5.4 TB/s: two CTAs share a tile so that 224 tiles
+// fill three rounds; launch, set-up, the first load and the last exchange are about 4.5 us), 128 rows of 64 experts, 4096 x
+// 4096, blocks of 32, 88.4 us (0.95 of the measured copy bandwidth on the active weights), 1x4096x4096 5.5 us.
 constexpr int kSwapThreads = 384;
 constexpr int kDrainWarps = 8;
 constexpr int kBufs = 2;               // accumulator buffers: the next tile's MMAs run while one is written out
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 8;          // nine: 16x28672x8192 2 % slower, 128 rows of 64 experts too
 constexpr int kTailBytes = 8 * (2 * kMaxStages + 2 * kBufs + 2) + 32 + 4 * (kMaxExperts + 2);
 
-constexpr int kSwapEpi = 2048 + 256;   // of a drain warp: 2 KB of values on their way out, the scales of up to 64 tokens
+// A value as T to shared memory.
+template <class T>
+__device__ __forceinline__ void sts_value(uint32_t addr, float f) {
+    const T v = from_float<T>(f);
+    if constexpr (sizeof(T) == 2)
+        asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
+    else
+        asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(__float_as_uint(f)) : "memory");
+}
 
-// acc[j]: weight row (column of y) col0 + lane, token t0 + j, as store_tokens; y's rows are whole 16-byte chunks. 2 KB of tokens
-// x 32 columns at a time are turned round in shared memory, so that a token's columns leave 16 bytes a lane (2050 rows of 32 experts,
-// 4096 x 2048: 89 -> 35 us with 128 tokens a tile, 57 -> 35 with 64).
+constexpr int kSwapEpi = 2048 + 64;    // of a drain warp: 2 KB of values on their way out, the scales of up to 16 tokens
+
+// acc[j]: weight row (column of y) col0 + lane, token t0 + j, as store_tokens; y's rows are whole 16-byte chunks. 2 KB of
+// tokens x 32 columns at a time are turned round in shared memory, so that a token's columns leave 16 bytes a lane (with
+// tiles of 64 tokens and a word a lane instead, 2050 rows of 32 experts took 57 us for 37).
 template <class T, int CW>
 __device__ __forceinline__ void store_tokens_staged(T* y, int64_t row, int t0, int n, int col0, int N, const float (&acc)[CW],
                                                     uint32_t buf, int split, int rank, int lane) {
@@ -155,11 +169,7 @@ __device__ __forceinline__ void store_tokens_staged(T* y, int64_t row, int t0, i
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kTokens; ++j) {
-            const T v = from_float<T>(acc[c * kTokens + j]);
-            if constexpr (sizeof(T) == 2)
-                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 2), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
-            else
-                asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 4), "r"(__float_as_uint(acc[c * kTokens + j])) : "memory");
+            sts_value<T>(buf + j * kRow + lane * (int)sizeof(T), acc[c * kTokens + j]);
         }
         __syncwarp();
         if (col < N) {
@@ -555,6 +565,16 @@ cudaError_t launch_swap(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
 //   warps 2, 3 scales of the CTA's token rows, every other stage each
 //   warps 4-11 drain: a TMEM lane is a token row; two warps for each quarter of the lanes, 128 columns each
+// The accumulator takes 256 of the 512 TMEM columns and two stages' scales 96, so there is one: the next tile's MMAs wait
+// until the drain warps have read it into registers, and run while they write it out. Measured: 8192x8192x16384 304 us from a
+// cool start (7.2 PFLOP/s, 3.8 times the measured bf16 rate), 355 us back to back, where the power cap holds the SM clock
+// near 1.5 GHz; blocks of 32 287 and 324 us. A stage takes 525 to 540 clocks there against 512 of MMA; without the loads 514,
+// and as many more clocks a second (252 us with neither loads nor stores: wrong results), so it is the power of what is moved
+// that costs. A tile costs some 2500 clocks besides: the hand-over of the accumulator about half, the rest waits for loads
+// behind the burst of stores (8192x8192x4096 95 us, 81 without its stores: wrong results). Tried: stores paced over the tile
+// (no gain), 64-byte boxes (8192x8192x1024 50 us for 47), 32 bytes of a row from each lane without staging (10 %), the first
+// scales' copies ahead of the accumulator's wait (3 %), one wait for both TMEM loads and scales' copies between the MMAs
+// (nothing), the weights' scales multicast to the pair (nothing).
 constexpr int PT = 256, PTH = 128, PN = 256;   // tile: tokens, tokens of a CTA, weight rows
 constexpr int kPairDrain = 8;                    // drain warps
 constexpr int kPairThreads = 128 + 32 * kPairDrain;
@@ -600,8 +620,8 @@ struct PairArgs {
     uint32_t most;   // units there can be
 };
 
-// A drain warp's 32 whole rows x 2 NC columns (one row a lane) to y: 128 bytes of each row at a time are staged in shared memory
-// (128-byte swizzle) and leave by TMA, which cuts off columns past N.
+// A drain warp's 32 whole rows x 2 NC columns (one row a lane) to y: 128 bytes of each row at a time are staged in shared
+// memory (128-byte swizzle) and leave by TMA, which cuts off columns past N.
 template <class T, int NC>
 __device__ __forceinline__ void store_rows_tma(const CUtensorMap* map, int row0, int col0, int N, const uint64_t (&acc)[NC],
                                                uint32_t buf, int lane) {
@@ -947,6 +967,10 @@ cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
 //   warps 2, 3 scales of the tile's tokens, every other stage each
 //   warps 4-11 drain: a TMEM lane is a weight row (a column of y); two warps for each quarter of the lanes, 64 tokens each
+// Bound by the weights' bytes, or by latencies where there is one round of tiles. Measured: 2050 rows of 32 experts, 4096 x
+// 2048, 32.8 us (5.2 TB/s), 2048 rows of 64, 4096 x 4096, 99 us (6.3 TB/s), 64x8192x8192 11.8 us, 256x8192x8192 14.1 us. With
+// 256 tokens a tile it would do the work of the pairs above with less waste in experts' last tiles, but the scales of 256
+// token rows in each CTA take longer than the MMAs (8192x8192x4096 130 us against 95).
 constexpr int TWP = 256, TNP = 128;               // weight rows of a tile, token rows at most
 constexpr int kWideEpi = 2048;                    // of a drain warp
 
@@ -974,8 +998,8 @@ struct WideCfg {
     static_assert(kSmem <= kSmemMax, "above the shared memory of one CTA");
 };
 
-// acc[j]: weight row (column of y) col0 + lane, token t0 + j; y's rows are whole 16-byte chunks. 2 KB of tokens x 32 columns at a
-// time are turned round in shared memory and leave by TMA, the last tokens of an expert 16 bytes a lane.
+// acc[j]: weight row (column of y) col0 + lane, token t0 + j; y's rows are whole 16-byte chunks. 2 KB of tokens x 32 columns
+// at a time are turned round in shared memory and leave by TMA, the last tokens of an expert 16 bytes a lane.
 template <class T, int NC>
 __device__ __forceinline__ void store_columns(const CUtensorMap* map, T* y, int row, int live, int col0, int N,
                                               const float (&acc)[NC], uint32_t buf, int lane) {
@@ -989,11 +1013,7 @@ __device__ __forceinline__ void store_columns(const CUtensorMap* map, T* y, int 
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kTokens; ++j) {
-            const T v = from_float<T>(acc[c * kTokens + j]);
-            if constexpr (sizeof(T) == 2)
-                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 2), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
-            else
-                asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(buf + j * kRow + lane * 4), "r"(__float_as_uint(acc[c * kTokens + j])) : "memory");
+            sts_value<T>(buf + j * kRow + lane * (int)sizeof(T), acc[c * kTokens + j]);
         }
         if (live - c * kTokens >= kTokens) {
             fence_proxy_async_smem();
@@ -1211,8 +1231,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         for (int j = 0; j < 8; ++j) w[j] = reinterpret_cast<const float4*>(token_scales + 32 * h)[j];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
+                        const float4& f = w[j / 4];
                         float x = acc[32 * h + j];
-                        if (p.sa) x = __fmul_rn(x, j % 4 == 0 ? w[j / 4].x : j % 4 == 1 ? w[j / 4].y : j % 4 == 2 ? w[j / 4].z : w[j / 4].w);
+                        if (p.sa) x = __fmul_rn(x, j % 4 == 0 ? f.x : j % 4 == 1 ? f.y : j % 4 == 2 ? f.z : f.w);
                         acc[32 * h + j] = __fmul_rn(x, scale);
                     }
                 }
@@ -1282,12 +1303,13 @@ cudaError_t launch(const Fp4Product& p, cudaStream_t stream) {
     const int64_t most = p.offsets ? 4 * per : per;
     if (most <= 16) return launch_swap<8, kBlock>(p, tiles(16), stream);
     if (most <= 32) return launch_swap<16, kBlock>(p, tiles(32), stream);
-    // What a round of tiles takes, in us, as measured (a stage, and a fixed part): 0.27 and 0.3 for 128 weight rows x 32 tokens over 152
-    // CTAs, 0.24 (0.20 for up to 64 tokens) and 1.0 for 256 x 128 over 76 pairs, 0.31 and 1.6 for 256 x 256; and once for each kernel
-    // 4.2, 5 and 6. A group's last tile is half full on average. Weights that are not in L2 take their time to be read whatever the
-    // tile, and the pairs with the smaller one wait less for them. Measured, us, in the same order: 128x2048x2048 6.7 / 8.4 / 9.1;
-    // 64x8192x8192 13.1 / 12.1 / 15.0; 256x8192x8192 39 / 13.9 / 16.6; 512x8192x8192 - / 23.3 / 18.3; 2050 rows of 32 experts,
-    // 4096x2048, 55 / 34.6 / 35.7; 8192 rows of 8, 4096x4096, - / 74 / 53.
+    // What a round of tiles takes, in us, as measured (a stage, and a fixed part): 0.27 and 0.3 for 128 weight rows x 32
+    // tokens over 152 CTAs, 0.24 (0.20 for up to 64 tokens) and 1.0 for 256 x 128 over 76 pairs, 0.31 and 1.6 for 256 x
+    // 256; and once for each kernel 4.2, 5 and 6. A group's last tile is half full on average. Weights that are not in L2
+    // take their time to be read whatever the tile, and the pairs with the smaller one wait less for them. Measured, us,
+    // in the same order: 128x2048x2048 6.7 / 8.4 / 9.1; 64x8192x8192 13.1 / 12.1 / 15.0; 256x8192x8192 39 / 13.9 / 16.6;
+    // 512x8192x8192 - / 23.3 / 18.3; 2050 rows of 32 experts, 4096x2048, 55 / 34.6 / 35.7; 8192 rows of 8, 4096x4096, - /
+    // 74 / 53.
     int narrow = 0, wide = 0;
     cudaError_t e = wide_clusters<kBlock>(narrow);
     if (e == cudaSuccess) e = pair_clusters<kBlock>(wide);

@@ -3,8 +3,8 @@
 // Blocks of 16 K: every row has an fp32 scale s and every block an e4m3 one. With a the row's and b the block's largest
 // magnitude, A = max(a, 1e-30):
 //   s = A / 2688,  c = e4m3(b * (448 / A)),  q = e2m1(x * ((2688 / A) / c)), 0 where c is 0,
-// so that x is about q c s. Blocks of 32 K: c = 2^e, the smallest power of two with b <= 6 c (e >= -127), q = e2m1(x / c), no s.
-// Every operation is rounded to nearest even in fp32, scales and codes once to their type. A NaN or an infinity makes the
+// so that x is about q c s. Blocks of 32 K: c = 2^e, the smallest power of two with b <= 6 c (e >= -127), q = e2m1(x / c), no
+// s. Every operation is rounded to nearest even in fp32, scales and codes once to their type. A NaN or an infinity makes the
 // row's s NaN (the block's c, for blocks of 32), so that a broken value is not hidden.
 #include "q8_fp4.h"
 #include "q8_internal.h"
@@ -115,12 +115,13 @@ struct Args {
     float* s;
 };
 
-// A row is held by blockDim.x threads, kUnroll vectors of 32 bytes each, all loads first; blockDim.y rows a CTA, some in a warp where
-// they are short. Blocks of 16 need the row's maximum before the first code: rows of up to 512 threads' vectors (32768 elements of 16
-// bits, 16384 of 32) stay in registers, as they were read; longer ones are read a second time, from L2.
-// Bound by memory. On the device, of the measured copy bandwidth: 8192 x 16384 fp32 91 us (0.99), bf16 51.5 (0.98; two vectors
-// a thread 66); 16384 x 4096 bf16 26.8 (0.95); the gated form, 32768 x 2048 bf16, 47.4 (0.95) with CTAs of 64 threads (48.0 with 128,
-// 49.5 with 256) and two vectors a thread (one 58); its fp32 form keeps one (42.6 us for 16384 x 2048, two 47, four 73: registers).
+// A row is held by blockDim.x threads, kUnroll vectors of 32 bytes each, all loads first; blockDim.y rows a CTA, some in a
+// warp where they are short. Blocks of 16 need the row's maximum before the first code: rows of up to 512 threads' vectors
+// (32768 elements of 16 bits, 16384 of 32) stay in registers, as they were read; longer ones are read a second time, from L2.
+// Bound by memory. On the device, of the measured copy bandwidth: 8192 x 16384 fp32 91 us (0.99), bf16 51.5 (0.98; two
+// vectors a thread 66); 16384 x 4096 bf16 26.8 (0.95); the gated form, 32768 x 2048 bf16, 47.4 (0.95) with CTAs of 64 threads
+// (48.0 with 128, 49.5 with 256) and two vectors a thread (one 58); its fp32 form keeps one (42.6 us for 16384 x 2048, two
+// 47, four 73: registers).
 template <class T, int kForm>
 struct Unroll { static constexpr int n = kForm == kGated ? (sizeof(T) == 4 ? 1 : 2) : 4; };
 
@@ -297,7 +298,8 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p,
     } else if constexpr (kForm == kTiles) {
         if (slot_row < p.rows_out)     // the padded rows of all matrices
             for (uint32_t g = (live ? have : 0) + tx; g < p.pitch; g += blockDim.x)
-                p.sf[((size_t)(slot_row >> 7) * (p.pitch / 4) + g / 4) * 512 + (nrow & 31) * 16 + ((nrow >> 5) & 3) * 4 + g % 4] = 0;
+                p.sf[((size_t)(slot_row >> 7) * (p.pitch / 4) + g / 4) * 512 + (nrow & 31) * 16 + ((nrow >> 5) & 3) * 4 +
+                     g % 4] = 0;
         if (kBlock == 16 && live && tx == 0) p.s[row] = s;
     } else if (live) {
         for (uint32_t g = have + tx; g < p.pitch; g += blockDim.x) p.sf[(size_t)row * p.pitch + g] = 0;
@@ -364,8 +366,9 @@ __device__ __forceinline__ void put32(void* y, const uint32_t (&w)[8], bool wide
     }
 }
 
-// 32 codes at a time, two of them a thread with both loads first: one scale of blocks of 32, two of blocks of 16. Bound by memory:
-// DEQ
+// 32 codes at a time, two of them a thread with both loads first: one scale of blocks of 32, two of blocks of 16. Bound by
+// memory: the codes of 8192 x 16384 to e4m3 30.5 us (0.97 of the measured copy bandwidth; 34.9 with 16 at a time), with scales to bf16
+// 53 us (0.96).
 constexpr int kBack = 256, kBackUnroll = 2;
 template <class T>
 __global__ void __launch_bounds__(kBack) dequantize_fp4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
@@ -443,8 +446,8 @@ template <class T>
 cudaError_t dequantize(const uint8_t* q, const uint8_t* sf, const float* s, int block, uint64_t total, int64_t K, int64_t tile_rows,
                        void* y, cudaStream_t stream) {
     const uint64_t per = kBack * kBackUnroll;
-    return launch_dependent(dequantize_fp4_kernel<T>, dim3((unsigned)((total + per - 1) / per)), dim3(kBack), 0, 0, stream, q, sf, s,
-                            block, total, (uint32_t)(K / 32), (uint32_t)fp4_pitch(K, block), (uint32_t)tile_rows,
+    return launch_dependent(dequantize_fp4_kernel<T>, dim3((unsigned)((total + per - 1) / per)), dim3(kBack), 0, 0, stream, q, sf,
+                            s, block, total, (uint32_t)(K / 32), (uint32_t)fp4_pitch(K, block), (uint32_t)tile_rows,
                             static_cast<T*>(y), reinterpret_cast<uintptr_t>(y) % 32 == 0);
 }
 
