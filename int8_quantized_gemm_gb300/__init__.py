@@ -39,6 +39,8 @@ Float8 (e4m3) operands with a scale for each block of 128, and layers of routed 
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -62,6 +64,7 @@ KERNELS = {"auto": 0, "tcgen05": 1, "mma_s8": 2, "skinny": 3, "decode": 4, "deco
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 
 _lib = None
+_calls = None   # the common calls of the 4-bit operators (csrc/q8_calls.cpp); None: the binding makes them itself
 
 
 class Q8Error(RuntimeError):
@@ -141,7 +144,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  "q8_linear", "q8_linear_host", "q8_gemm_pick", "q8_device_error", "q8_selftest_wait_timeout"):
         getattr(lib, name).restype = i32
     _lib = lib
+    _load_calls(lib)
     return lib
+
+
+def _load_calls(lib: ctypes.CDLL):
+    global _calls
+    path = _build.calls_path()
+    if not os.path.exists(path):
+        return
+    loader = importlib.machinery.ExtensionFileLoader("_q8_calls", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_q8_calls", loader))
+    loader.exec_module(module)
+    module.entries(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                     for name in ("q8_quantize_fp4", "q8_swiglu_quantize_fp4", "q8_dequantize_fp4", "q8_gemm_fp4",
+                                  "q8_gemm_fp4_grouped")))
+    _calls = module
 
 
 def status_string(status: int) -> str:
@@ -871,6 +889,8 @@ def q8_moe_combine(h: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, 
 
 # --------------------------------------------------------- 4-bit floating point, scales of 16 or 32 K
 
+# The common calls (new results, the current stream) are made by csrc/q8_calls.cpp where it is built, which leaves everything
+# else, what is wrong among it, to the functions here by returning None.
 FP4_SPAN = 256      # rows of block scales are whole spans of 256 K
 _SCALE_TYPES = {16: torch.float8_e4m3fn, 32: torch.float8_e8m0fnu}
 _BLOCKS = {v: k for k, v in _SCALE_TYPES.items()}
@@ -912,6 +932,10 @@ def q8_quantize_fp4(x: torch.Tensor, block: int = 16, slots=None, rows: int | No
     fp32 scale a row; block 32: powers of two of 32 K. slots int32 [M, k]: row m goes to the rows slots[m] of the result instead
     (skipped where outside), which has `rows` rows (default M * k). Returns (q uint8 [rows, K / 2], two codes a byte, sf
     [rows, 256 / block * ceil(K / 256)] float8_e4m3fn or float8_e8m0fnu, s fp32 [rows] or None)."""
+    if _calls is not None and rows is None and q is None and sf is None and s is None and stream is None:
+        got = _calls.quantize_fp4(x, block, slots)
+        if got is not None:
+            return got
     M, K, ldx, kind = _float_rows(x, "x")
     dev = x.get_device()
     top_k, to = 0, None
@@ -935,6 +959,10 @@ def q8_quantize_fp4(x: torch.Tensor, block: int = 16, slots=None, rows: int | No
 
 def q8_swiglu_quantize_fp4(h: torch.Tensor, block: int = 16, q=None, sf=None, s=None, stream=None):
     """Codes and scales (as q8_quantize_fp4) of silu(h[:, :I]) * h[:, I:], h[M, 2 I] (rows may be strided)."""
+    if _calls is not None and q is None and sf is None and s is None and stream is None:
+        got = _calls.swiglu_quantize_fp4(h, block)
+        if got is not None:
+            return got
     M, cols, ldh, kind = _float_rows(h, "h")
     if cols % 2:
         raise ValueError("h must have an even number of columns")
@@ -986,6 +1014,10 @@ def q8_dequantize_fp4(q: torch.Tensor, sf=None, s=None, out_dtype=torch.bfloat16
     """What codes stand for, [.., K]: q (q8_quantize_fp4's [rows, K / 2] or q8_quantize_weight_fp4's) times its block scales sf (of the
     same kind) times its row scales s; without a scale it counts as 1. out_dtype float32, bfloat16 or float16; without scales
     also float8_e4m3fn, which holds every code."""
+    if _calls is not None and sf is None and s is None and out is None and stream is None:
+        got = _calls.dequantize_fp4(q, out_dtype)
+        if got is not None:
+            return got
     if not isinstance(q, torch.Tensor) or q.dtype is not torch.uint8 or not q.is_cuda or q.dim() not in (2, 3):
         _need(q, torch.uint8, "q")
         raise ValueError("q must be [rows, K / 2] or [E, N, K / 2]")
@@ -1062,6 +1094,10 @@ def _fp4_operands(qa, sfa, sa, qw, sfw, sw, ndim, out_dtype, out, stream):
 def q8_gemm_fp4(qa, sfa, sa, qw, sfw, sw, out_dtype=torch.bfloat16, out=None, stream=None):
     """y[m, n] = sa[m] sw[n] sum over blocks b of sfa[m, b] sfw[n, b] (qa . qw over block b), as out_dtype [M, N]. The operands are
     those of q8_quantize_fp4 and q8_quantize_weight_fp4, with the same block; sa or sw None stands for ones."""
+    if _calls is not None and out is None and stream is None:
+        got = _calls.gemm_fp4(qa, sfa, sa, qw, sfw, sw, None, out_dtype)
+        if got is not None:
+            return got
     dev, M, N, K, block, pa, psfa, psa, pw, psfw, psw, py, kind, out = _fp4_operands(qa, sfa, sa, qw, sfw, sw, 2, out_dtype, out,
                                                                                      stream)
     status = (_lib or load()).q8_gemm_fp4(pa, psfa, psa, pw, psfw, psw, block, M, N, K, py, kind, _handle(dev, stream))
@@ -1073,6 +1109,10 @@ def q8_gemm_fp4(qa, sfa, sa, qw, sfw, sw, out_dtype=torch.bfloat16, out=None, st
 def q8_gemm_fp4_grouped(qa, sfa, sa, qw, sfw, sw, offsets, out_dtype=torch.bfloat16, out=None, stream=None):
     """The product of q8_gemm_fp4 with qw[e], sfw[e], sw[e] (of qw[E, N, K / 2]) for the rows offsets[e] .. offsets[e + 1] - 1 of each
     expert; offsets int32 [E + 1] stay on the device. Rows of no expert are not written."""
+    if _calls is not None and offsets is not None and out is None and stream is None:
+        got = _calls.gemm_fp4(qa, sfa, sa, qw, sfw, sw, offsets, out_dtype)
+        if got is not None:
+            return got
     dev, M, N, K, block, pa, psfa, psa, pw, psfw, psw, py, kind, out = _fp4_operands(qa, sfa, sa, qw, sfw, sw, 3, out_dtype, out,
                                                                                      stream)
     E = qw.shape[0]

@@ -1,15 +1,20 @@
 """Build the CUDA library libq8.so in-tree for sm_103a.
 
 Each .cu file is compiled separately (in parallel) and linked into one shared
-library with the C ABI of include/q8.h. Run `python -m int8_quantized_gemm_gb300.build`.
+library with the C ABI of include/q8.h. Beside it, one small module of the host compiler against the
+installed PyTorch: the common calls of the 4-bit operators (csrc/q8_calls.cpp), without which the binding
+makes them itself. Run `python -m int8_quantized_gemm_gb300.build`.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +24,7 @@ LIB = os.path.join(OUT_DIR, "libq8.so")
 SOURCES = ["q8_api.cu", "q8_quant.cu", "q8_gemm_mma.cu", "q8_gemm_tc.cu", "q8_gemv_tc.cu", "q8_gemv_mma.cu", "q8_gemm_tc2.cu",
            "q8_host.cu", "q8_fp8_api.cu", "q8_fp8_quant.cu", "q8_fp8_gemm.cu", "q8_moe.cu",
            "q8_fp4_api.cu", "q8_fp4_quant.cu", "q8_fp4_gemm.cu"]
+CALLS_SOURCE = "q8_calls.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -27,6 +33,32 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libq8.so")
+
+
+def calls_path() -> str:
+    """The module of the common calls, for this interpreter and PyTorch."""
+    tag = f"{sys.implementation.cache_tag}_torch_{importlib.metadata.version('torch')}"
+    return os.path.join(OUT_DIR, "_q8_calls_" + "".join(c if c.isalnum() else "_" for c in tag) + ".so")
+
+
+def _build_calls() -> str:
+    """Compiles it. Returns why it could not be compiled (the binding works without it), or an empty string."""
+    out = calls_path()
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cc = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cc:
+        return "no host compiler"
+    cmd = [cc, "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           os.path.join(CSRC, CALLS_SOURCE), "-o", out + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        return r.stderr[-2000:]
+    os.replace(out + ".tmp", out)
+    return ""
 
 
 def _flags(verbose: bool):
@@ -38,12 +70,13 @@ def _flags(verbose: bool):
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    made = [p for p in (calls_path(), calls_path() + ".none") if os.path.exists(p)]   # .none: it could not be compiled here
+    if not os.path.exists(LIB) or not made:
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), max(os.path.getmtime(p) for p in made))
     headers = ["q8_internal.h", "q8_tc_ptx.cuh", "q8_fp8.h", "q8_fp8_ptx.cuh", "q8_tiles.cuh", "q8_silu.cuh", "q8_fp4.h",
                "q8_fp4_ptx.cuh"]
-    deps = [os.path.join(CSRC, s) for s in SOURCES + headers] + [os.path.join(ROOT, "include", "q8.h"), os.path.abspath(__file__)]
+    deps = [os.path.join(CSRC, s) for s in SOURCES + headers + [CALLS_SOURCE]] + [os.path.join(ROOT, "include", "q8.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -62,11 +95,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls)
         for obj, log in ex.map(compile_one, SOURCES):
             objs.append(obj)
             if verbose and log:
                 sys.stderr.write(log)
+        why = calls.result()
+    if why:
+        open(calls_path() + ".none", "w").close()
+        sys.stderr.write(f"{CALLS_SOURCE} was not built, the binding makes these calls itself: {why}\n")
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
            "-Xlinker", "-rpath,/usr/local/cuda/lib64"]

@@ -230,6 +230,50 @@ def test_two_graphs_replayed_at_once(q8):
         assert all(torch.equal(y, want) for _, _, y, want, *_ in pairs)
 
 
+# ------------------------------------------------------------------------------------------ the two ways a call is made
+
+@pytest.mark.parametrize("block", BLOCKS)
+def test_the_binding_makes_the_same_calls_itself(q8, block, monkeypatch):
+    """Results of the compiled calls against those of the binding's own: types, shapes, bits, and the stream that is current."""
+    assert q8._calls is not None
+    x = ref.tokens(70, 544, seed=1).to(torch.bfloat16).cuda()
+    slots = torch.randperm(140, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(70, 2).cuda()
+    w = q8.q8_quantize_weight_fp4(ref.tokens(2 * 264, 544, seed=2).view(2, 264, 544).cuda(), block=block)
+    off = torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda")
+    h = ref.tokens(9, 320, seed=3).cuda()
+
+    def calls():
+        a = q8.q8_quantize_fp4(x, block=block)
+        yield from a
+        yield from q8.q8_quantize_fp4(x[::2, 32:320], block=block)
+        yield from q8.q8_quantize_fp4(x, block=block, slots=slots)
+        yield from q8.q8_quantize_fp4(x[:0], block=block)
+        yield from q8.q8_swiglu_quantize_fp4(h, block=block)
+        for t in (torch.float8_e4m3fn, torch.float16):
+            yield q8.q8_dequantize_fp4(a[0], out_dtype=t)
+        for t in (torch.float32, torch.bfloat16):
+            yield q8.q8_gemm_fp4(*a, *(None if t is None else t[0] for t in w), out_dtype=t)
+            yield q8.q8_gemm_fp4(*a[:2], None, *(None if t is None else t[1] for t in w[:2]), None, out_dtype=t)
+            yield q8.q8_gemm_fp4_grouped(*a, *w, off, out_dtype=t)
+
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        compiled = list(calls())
+        side.synchronize()
+    assert {pool_stream(t) for t in compiled if t is not None and t.numel()} == {side.cuda_stream}
+    monkeypatch.setattr(q8, "_calls", None)
+    own = list(calls())
+    torch.cuda.synchronize()
+    assert len(own) == len(compiled)
+    for a, b in zip(compiled, own):
+        if a is None or b is None:
+            assert a is b
+            continue
+        assert (a.dtype, a.shape, a.device, a.stride()) == (b.dtype, b.shape, b.device, b.stride())
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 # ------------------------------------------------------------------------------------------ refusals
 
 def test_operands_that_do_not_fit_one_another(q8):
