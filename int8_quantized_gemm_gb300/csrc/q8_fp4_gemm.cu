@@ -7,7 +7,8 @@
 // tile's sum over all K stays in its fp32 accumulator; the rows' scales are applied as it is written out. A stage is 256 K: 128
 // bytes of codes a row (128-byte swizzle) and the scales in tiles of 128 rows x 4 (512 bytes, tcgen05.cp). The weights'
 // scales are stored in such tiles (TMA); the tokens', which may begin at any row of an expert, as rows: a warp turns
-// them into tiles on the way to shared memory.
+// them into tiles on the way to shared memory. In tensor memory every stage has columns of its own for its scales: they are copied
+// again only after the stage's barriers have seen the MMAs that read them.
 #include <cuda.h>
 
 #include <type_traits>
@@ -211,8 +212,8 @@ struct SwapCfg {
     static constexpr uint32_t kId0 = idesc_fp4(TW, 0, kBlock, 0), kId2 = idesc_fp4(TW, 0, kBlock, 2);   // N is added
     static constexpr int kScaleCols = 2 * S::kCols;             // of a stage: weights, then tokens
     static constexpr int kTmemScales = kBufs * TN;
-    static constexpr int kTmemUsed = kTmemScales + 2 * kScaleCols;
-    static constexpr int kTmem = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+    static constexpr int kTmem = 512;
+    static_assert(kTmemScales + kMaxStages * kScaleCols <= kTmem, "above the tensor memory");
     // receive buffer: the groups of four tokens that a CTA owns, from each other CTA
     static int reduce_bytes(int split) { return (split - 1) * ((TN / 4 + split - 1) / split) * TW * 16; }
 };
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------------------- MMA
-        uint32_t s = 0, phase = 0, buf = 0, bphase = 1, c = 0;
+        uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
         bool ok = true;
         for (uint32_t u = first; u < units && ok; u += step) {
             int e, row, n;
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
             const uint32_t id0 = C::kId0 + width, id2 = C::kId2 + width;
             if (!warp_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc)) break;
             const uint32_t d = tmem_base + buf * TN;
-            for (int kb = kb0; kb < kb1; ++kb, ++c) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!warp_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull)) {
                     ok = false;
                     break;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                 const uint32_t at = sbase + s * C::kStage;
                 const uint64_t w = smem_desc_sw128(at), a = smem_desc_sw128(at + C::kOffTokens);
                 const uint64_t sfw = smem_desc_scales(at + C::kOffSfw), sfa = smem_desc_scales(at + C::kOffSfa);
-                const uint32_t tw = tmem_base + C::kTmemScales + (c & 1) * C::kScaleCols, ta = tw + S::kCols;
+                const uint32_t tw = tmem_base + C::kTmemScales + s * C::kScaleCols, ta = tw + S::kCols;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < S::kAtoms; ++k) {
@@ -565,7 +566,7 @@ cudaError_t launch_swap(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
 //   warps 2, 3 scales of the CTA's token rows, every other stage each
 //   warps 4-11 drain: a TMEM lane is a token row; two warps for each quarter of the lanes, 128 columns each
-// The accumulator takes 256 of the 512 TMEM columns and two stages' scales 96, so there is one: the next tile's MMAs wait
+// The accumulator takes 256 of the 512 TMEM columns and five stages' scales 240, so there is one: the next tile's MMAs wait
 // until the drain warps have read it into registers, and run while they write it out. Measured: 8192x8192x16384 304 us from a
 // cool start (7.2 PFLOP/s, 3.8 times the measured bf16 rate), 355 us back to back, where the power cap holds the SM clock
 // near 1.5 GHz; blocks of 32 287 and 324 us. A stage takes 525 to 540 clocks there against 512 of MMA; without the loads 514,
@@ -598,7 +599,7 @@ struct PairCfg {
     static constexpr uint32_t kId0 = idesc_fp4(PT, PN, kBlock, 0), kId2 = idesc_fp4(PT, PN, kBlock, 2);
     static constexpr int kScaleCols = S::kCols + PN / TW * S::kCols;    // tokens, then weights
     static constexpr int kTmemScales = kBufs * PN;
-    static_assert(kTmemScales + 2 * kScaleCols <= 512, "above the tensor memory");
+    static_assert(kTmemScales + kStages * kScaleCols <= 512, "above the tensor memory");
     static constexpr int kOffEpi = kStages * kStage;
     static constexpr int kOffCol = kOffEpi + kPairDrain * kPairEpi;     // the tile's column scales
     static constexpr int kOffBar = kOffCol + PN * 4;
@@ -762,12 +763,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------------------------ MMA
             constexpr uint32_t id0 = C::kId0, id2 = C::kId2;
-            uint32_t s = 0, phase = 0, buf = 0, bphase = 1, c = 0;
+            uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
             bool ok = true;
             for (uint32_t u = first; u < units && ok; u += step) {
                 if (!warp_wait_cluster(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc)) break;
                 const uint32_t d = tmem_base + buf * PN;
-                for (int kb = 0; kb < KB; ++kb, ++c) {
+                for (int kb = 0; kb < KB; ++kb) {
                     if (!warp_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull)) {
                         ok = false;
                         break;
@@ -776,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t at = sbase + s * C::kStage;
                     const uint64_t a = smem_desc_sw128(at), w = smem_desc_sw128(at + C::kOffW);
                     const uint64_t sfa = smem_desc_scales(at + C::kOffSfa), sfw = smem_desc_scales(at + C::kOffSfw);
-                    const uint32_t ta = tmem_base + C::kTmemScales + (c & 1) * C::kScaleCols, tw = ta + S::kCols;
+                    const uint32_t ta = tmem_base + C::kTmemScales + s * C::kScaleCols, tw = ta + S::kCols;
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < S::kAtoms; ++k) {
@@ -989,7 +990,7 @@ struct WideCfg {
     static constexpr uint32_t kId0 = idesc_fp4(TWP, 0, kBlock, 0), kId2 = idesc_fp4(TWP, 0, kBlock, 2);   // N is added
     static constexpr int kScaleCols = 2 * S::kCols;           // weights, then tokens
     static constexpr int kTmemScales = kBufs * TNP;
-    static_assert(kTmemScales + 2 * kScaleCols <= 512, "above the tensor memory");
+    static_assert(kTmemScales + kStages * kScaleCols <= 512, "above the tensor memory");
     static constexpr int kOffEpi = kStages * kStage;
     static constexpr int kOffTok = kOffEpi + kPairDrain * kWideEpi;     // the tokens' row scales
     static constexpr int kOffBar = kOffTok + TNP * 4;
@@ -1120,7 +1121,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------------------------ MMA
-            uint32_t s = 0, phase = 0, buf = 0, bphase = 1, c = 0;
+            uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
             bool ok = true;
             for (uint32_t u = first; u < units && ok; u += step) {
                 int t, nt, e, row, n;
@@ -1130,7 +1131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint32_t id0 = C::kId0 + width, id2 = C::kId2 + width;
                 if (!warp_wait_cluster(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc)) break;
                 const uint32_t d = tmem_base + buf * TNP;
-                for (int kb = 0; kb < KB; ++kb, ++c) {
+                for (int kb = 0; kb < KB; ++kb) {
                     if (!warp_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull)) {
                         ok = false;
                         break;
@@ -1139,7 +1140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t at = sbase + s * C::kStage;
                     const uint64_t w = smem_desc_sw128(at), a = smem_desc_sw128(at + C::kOffTokens);
                     const uint64_t sfw = smem_desc_scales(at + C::kOffSfw), sfa = smem_desc_scales(at + C::kOffSfa);
-                    const uint32_t tw = tmem_base + C::kTmemScales + (c & 1) * C::kScaleCols, ta = tw + S::kCols;
+                    const uint32_t tw = tmem_base + C::kTmemScales + s * C::kScaleCols, ta = tw + S::kCols;
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < S::kAtoms; ++k) {
