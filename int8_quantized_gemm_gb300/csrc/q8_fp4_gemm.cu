@@ -282,53 +282,53 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------------------- TMA
-        uint32_t s = 0, phase = 1;
-        bool ok = true;
-        for (uint32_t u = first; u < units && ok; u += step) {
-            int e, row, n;
-            groups.tile((int)(u / (uint32_t)NT), e, row, n);
-            const int nt = (int)(u % (uint32_t)NT), wrow = e * p.N + nt * TW, boxes = (n + C::kBox - 1) / C::kBox;
-            const int sfrow = (e * NT + nt) * KB * (S::kAtoms * 4);     // tiles of scales as rows of 128 bytes
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!warp_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = sbase + s * C::kStage, bar = bar_full + 8 * s;
-                if (elect_one()) {
+        if (elect_one()) {   // one lane for all of it, as of the MMAs: 16x8192x8192 8.5 us, 8.9 with the warp at each stage
+            uint32_t s = 0, phase = 1;
+            bool ok = true;
+            for (uint32_t u = first; u < units && ok; u += step) {
+                int e, row, n;
+                groups.tile((int)(u / (uint32_t)NT), e, row, n);
+                const int nt = (int)(u % (uint32_t)NT), wrow = e * p.N + nt * TW, boxes = (n + C::kBox - 1) / C::kBox;
+                const int sfrow = (e * NT + nt) * KB * (S::kAtoms * 4);     // tiles of scales as rows of 128 bytes
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp4_error)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + s * C::kStage, bar = bar_full + 8 * s;
                     mbar_expect_tx(bar, C::kOffTokens + S::kBytes + boxes * C::kBox * kRowBytes);
                     tma_load_2d(dst, &tmap_w, kb * kRowBytes, wrow, bar);
                     tma_load_2d(dst + C::kOffSfw, &tmap_sf, 0, sfrow + kb * (S::kAtoms * 4), bar);
                     for (int b = 0; b < boxes; ++b)
                         tma_load_2d(dst + C::kOffTokens + b * C::kBox * kRowBytes, &tmap_a, kb * kRowBytes, row + b * C::kBox,
                                     bar);
+                    if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
                 }
-                __syncwarp();
-                if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------------------- MMA
-        uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
-        bool ok = true;
-        for (uint32_t u = first; u < units && ok; u += step) {
-            int e, row, n;
-            groups.tile((int)(u / (uint32_t)NT), e, row, n);
-            const uint32_t width = (uint32_t)((n + 15) >> 4) << 18;   // N = n rounded up to 16
-            const uint32_t id0 = C::kId0 + width, id2 = C::kId2 + width;
-            if (!warp_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc)) break;
-            const uint32_t d = tmem_base + buf * TN;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!warp_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t at = sbase + s * C::kStage;
-                const uint64_t w = smem_desc_sw128(at), a = smem_desc_sw128(at + C::kOffTokens);
-                const uint64_t sfw = smem_desc_scales(at + C::kOffSfw), sfa = smem_desc_scales(at + C::kOffSfa);
-                const uint32_t tw = tmem_base + C::kTmemScales + s * C::kScaleCols, ta = tw + S::kCols;
-                if (elect_one()) {
+        if (elect_one()) {
+            uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
+            bool ok = true;
+            for (uint32_t u = first; u < units && ok; u += step) {
+                int e, row, n;
+                groups.tile((int)(u / (uint32_t)NT), e, row, n);
+                const uint32_t width = (uint32_t)((n + 15) >> 4) << 18;   // N = n rounded up to 16
+                const uint32_t id0 = C::kId0 + width, id2 = C::kId2 + width;
+                if (!mbar_wait(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc, &g_fp4_error)) break;
+                const uint32_t d = tmem_base + buf * TN;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp4_error)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = sbase + s * C::kStage;
+                    const uint64_t w = smem_desc_sw128(at), a = smem_desc_sw128(at + C::kOffTokens);
+                    const uint64_t sfw = smem_desc_scales(at + C::kOffSfw), sfa = smem_desc_scales(at + C::kOffSfa);
+                    const uint32_t tw = tmem_base + C::kTmemScales + s * C::kScaleCols, ta = tw + S::kCols;
 #pragma unroll
                     for (int k = 0; k < S::kAtoms; ++k) {
                         copy_scales<1>(tw + 4 * k, sfw + 32 * k);
@@ -342,12 +342,12 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                     }
                     mma_commit(bar_empty + 8 * s);
                     if (kb == kb1 - 1) mma_commit(bar_accfull + 8 * buf);
+                    if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
                 }
-                __syncwarp();
-                if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
+                if (++buf == kBufs) { buf = 0; bphase ^= 1; }
             }
-            if (++buf == kBufs) { buf = 0; bphase ^= 1; }
         }
+        __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------------------------------- scales
         uint32_t s = 0, phase = 1, count = 0;
@@ -969,7 +969,7 @@ cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 //   warps 2, 3 scales of the tile's tokens, every other stage each
 //   warps 4-11 drain: a TMEM lane is a weight row (a column of y); two warps for each quarter of the lanes, 64 tokens each
 // Bound by the weights' bytes, or by latencies where there is one round of tiles. Measured: 2050 rows of 32 experts, 4096 x
-// 2048, 32.8 us (5.2 TB/s), 2048 rows of 64, 4096 x 4096, 99 us (6.3 TB/s), 64x8192x8192 11.8 us, 256x8192x8192 14.1 us. With
+// 2048, 32.3 us (5.3 TB/s), 2048 rows of 64, 4096 x 4096, 99 us (6.3 TB/s), 64x8192x8192 10.9 us, 256x8192x8192 14.2 us. With
 // 256 tokens a tile it would do the work of the pairs above with less waste in experts' last tiles, but the scales of 256
 // token rows in each CTA take longer than the MMAs (8192x8192x4096 130 us against 95).
 constexpr int TWP = 256, TNP = 128;               // weight rows of a tile, token rows at most
@@ -1088,60 +1088,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPairRegsLow));
         if (warp == 0) {
             // ------------------------------------------------------------------------ TMA
-            const uint32_t full0 = mapa_shared(bar_full, 0);
-            uint32_t s = 0, phase = 1;
-            bool ok = true;
-            for (uint32_t u = first; u < units && ok; u += step) {
-                int t, nt, e, row, n;
-                pair_unit(u, tiles, NT, t, nt);
-                groups.tile(t, e, row, n);
-                const int half = ((n + 15) >> 4) << 3, boxes = (half + C::kBox - 1) / C::kBox;   // tokens of a CTA
-                const int arow = row + rank * half;
-                // A half without a weight row is loaded from past the end of the tensor: zeros
-                const int wrow = nt * TWP + rank * TW < p.N ? e * p.N + nt * TWP + rank * TW : p.E * p.N;
-                const int sfrow = (e * NB + nt * 2 + rank) * KB * (S::kAtoms * 4);
-                const uint32_t bytes = 2 * (C::kOffTokens + S::kBytes + boxes * C::kBox * kRowBytes);
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!warp_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t dst = sbase + s * C::kStage;
-                    if (elect_one()) {
+            if (elect_one()) {   // one lane for all of it, as of the MMAs: 64x8192x8192 10.9 us, 11.8 with the warp at each stage
+                const uint32_t full0 = mapa_shared(bar_full, 0);
+                uint32_t s = 0, phase = 1;
+                bool ok = true;
+                for (uint32_t u = first; u < units && ok; u += step) {
+                    int t, nt, e, row, n;
+                    pair_unit(u, tiles, NT, t, nt);
+                    groups.tile(t, e, row, n);
+                    const int half = ((n + 15) >> 4) << 3, boxes = (half + C::kBox - 1) / C::kBox;   // tokens of a CTA
+                    const int arow = row + rank * half;
+                    // A half without a weight row is loaded from past the end of the tensor: zeros
+                    const int wrow = nt * TWP + rank * TW < p.N ? e * p.N + nt * TWP + rank * TW : p.E * p.N;
+                    const int sfrow = (e * NB + nt * 2 + rank) * KB * (S::kAtoms * 4);
+                    const uint32_t bytes = 2 * (C::kOffTokens + S::kBytes + boxes * C::kBox * kRowBytes);
+                    for (int kb = 0; kb < KB; ++kb) {
+                        if (!mbar_wait(bar_done + 8 * s, phase, abort_flag, kErrProducer, &g_fp4_error)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t dst = sbase + s * C::kStage;
                         if (rank == 0) mbar_expect_tx(bar_full + 8 * s, bytes);
                         tma_load_2d_pair(dst, &tmap_w, kb * kRowBytes, wrow, full0 + 8 * s);
                         tma_load_2d_pair(dst + C::kOffSfw, &tmap_sf, 0, sfrow + kb * (S::kAtoms * 4), full0 + 8 * s);
                         for (int b = 0; b < boxes; ++b)
                             tma_load_2d_pair(dst + C::kOffTokens + b * C::kBox * kRowBytes, &tmap_a, kb * kRowBytes,
                                              arow + b * C::kBox, full0 + 8 * s);
+                        if (++s == kStages) { s = 0; phase ^= 1; }
                     }
-                    __syncwarp();
-                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
             }
+            __syncwarp();
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------------------------------ MMA
-            uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
-            bool ok = true;
-            for (uint32_t u = first; u < units && ok; u += step) {
-                int t, nt, e, row, n;
-                pair_unit(u, tiles, NT, t, nt);
-                groups.tile(t, e, row, n);
-                const uint32_t width = (uint32_t)((n + 15) >> 4) << 18;   // N = n rounded up to 16
-                const uint32_t id0 = C::kId0 + width, id2 = C::kId2 + width;
-                if (!warp_wait_cluster(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc)) break;
-                const uint32_t d = tmem_base + buf * TNP;
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!warp_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t at = sbase + s * C::kStage;
-                    const uint64_t w = smem_desc_sw128(at), a = smem_desc_sw128(at + C::kOffTokens);
-                    const uint64_t sfw = smem_desc_scales(at + C::kOffSfw), sfa = smem_desc_scales(at + C::kOffSfa);
-                    const uint32_t tw = tmem_base + C::kTmemScales + s * C::kScaleCols, ta = tw + S::kCols;
-                    if (elect_one()) {
+            if (elect_one()) {
+                uint32_t s = 0, phase = 0, buf = 0, bphase = 1;
+                bool ok = true;
+                for (uint32_t u = first; u < units && ok; u += step) {
+                    int t, nt, e, row, n;
+                    pair_unit(u, tiles, NT, t, nt);
+                    groups.tile(t, e, row, n);
+                    const uint32_t width = (uint32_t)((n + 15) >> 4) << 18;   // N = n rounded up to 16
+                    const uint32_t id0 = C::kId0 + width, id2 = C::kId2 + width;
+                    if (!mbar_wait_cluster(bar_accempty + 8 * buf, bphase, abort_flag, kErrMmaAcc, &g_fp4_error)) break;
+                    const uint32_t d = tmem_base + buf * TNP;
+                    for (int kb = 0; kb < KB; ++kb) {
+                        if (!mbar_wait_cluster(bar_full + 8 * s, phase, abort_flag, kErrMmaFull, &g_fp4_error)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t at = sbase + s * C::kStage;
+                        const uint64_t w = smem_desc_sw128(at), a = smem_desc_sw128(at + C::kOffTokens);
+                        const uint64_t sfw = smem_desc_scales(at + C::kOffSfw), sfa = smem_desc_scales(at + C::kOffSfa);
+                        const uint32_t tw = tmem_base + C::kTmemScales + s * C::kScaleCols, ta = tw + S::kCols;
 #pragma unroll
                         for (int k = 0; k < S::kAtoms; ++k) {
                             copy_scales<2>(tw + 4 * k, sfw + 32 * k);
@@ -1155,12 +1155,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         }
                         mma_commit_pair(bar_done + 8 * s, 3);
                         if (kb == KB - 1) mma_commit_pair(bar_accfull + 8 * buf, 3);
+                        if (++s == kStages) { s = 0; phase ^= 1; }
                     }
-                    __syncwarp();
-                    if (++s == kStages) { s = 0; phase ^= 1; }
+                    if (++buf == kBufs) { buf = 0; bphase ^= 1; }
                 }
-                if (++buf == kBufs) { buf = 0; bphase ^= 1; }
             }
+            __syncwarp();
         } else if (warp >= 2) {
             // --------------------------------------------------------------------- scales
             const uint32_t full0 = mapa_shared(bar_full, 0);
@@ -1308,7 +1308,7 @@ cudaError_t launch(const Fp4Product& p, cudaStream_t stream) {
     // tokens over 152 CTAs, 0.24 (0.20 for up to 64 tokens) and 1.0 for 256 x 128 over 76 pairs, 0.31 and 1.6 for 256 x
     // 256; and once for each kernel 4.2, 5 and 6. A group's last tile is half full on average. Weights that are not in L2
     // take their time to be read whatever the tile, and the pairs with the smaller one wait less for them. Measured, us,
-    // in the same order: 128x2048x2048 6.7 / 8.4 / 9.1; 64x8192x8192 13.1 / 12.1 / 15.0; 256x8192x8192 39 / 13.9 / 16.6;
+    // in the same order: 128x2048x2048 6.7 / 8.4 / 9.1; 64x8192x8192 12.9 / 10.9 / 14.1; 256x8192x8192 39 / 13.9 / 16.6;
     // 512x8192x8192 - / 23.3 / 18.3; 2050 rows of 32 experts, 4096x2048, 55 / 34.6 / 35.7; 8192 rows of 8, 4096x4096, - /
     // 74 / 53.
     int narrow = 0, wide = 0;
