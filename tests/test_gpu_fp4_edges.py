@@ -230,6 +230,41 @@ def test_two_graphs_replayed_at_once(q8):
         assert all(torch.equal(y, want) for _, _, y, want, *_ in pairs)
 
 
+def test_graph_with_branches(q8):
+    """A capture that forks to another stream after the quantizer and joins again: replayed with other tokens."""
+    w = [q8.q8_quantize_weight_fp4(ref.tokens(520, 1056, seed=i).cuda()) for i in range(2)]
+    x = ref.tokens(40, 1056, seed=3).cuda()
+    side = torch.cuda.Stream()
+
+    def work():
+        a = q8.q8_quantize_fp4(x)
+        fork, join = torch.cuda.Event(), torch.cuda.Event()
+        fork.record()
+        with torch.cuda.stream(side):
+            side.wait_event(fork)
+            y1 = q8.q8_gemm_fp4(*a, *w[1], out_dtype=torch.float32)
+            b = q8.q8_quantize_fp4(y1[:, :512])
+            join.record()
+        y0 = q8.q8_gemm_fp4(*a, *w[0], out_dtype=torch.float32)
+        torch.cuda.current_stream().wait_event(join)
+        return q8.q8_quantize_fp4(y0[:, :512] + y1[:, :512]), b, y0, y1
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both, b, y0, y1 = work()
+    for turn in range(4):
+        x.copy_(ref.tokens(40, 1056, seed=10 + turn))
+        graph.replay()
+        torch.cuda.synchronize()
+        a = q8.q8_quantize_fp4(x)
+        want = [q8.q8_gemm_fp4(*a, *v, out_dtype=torch.float32) for v in w]
+        assert torch.equal(y0, want[0]) and torch.equal(y1, want[1])
+        for got, t in ((both, want[0][:, :512] + want[1][:, :512]), (b, want[1][:, :512])):
+            assert all(torch.equal(g.view(torch.uint8), v.view(torch.uint8)) for g, v in zip(got, q8.q8_quantize_fp4(t)))
+
+
 # ------------------------------------------------------------------------------------------ the two ways a call is made
 
 @pytest.mark.parametrize("block", BLOCKS)
