@@ -8,13 +8,14 @@ makes them itself. Run `python -m int8_quantized_gemm_gb300.build`.
 from __future__ import annotations
 
 import concurrent.futures as cf
-import importlib.metadata
-import importlib.util
+import glob
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -37,14 +38,15 @@ def nvcc() -> str:
 
 def calls_path() -> str:
     """The module of the common calls, for this interpreter and PyTorch."""
-    tag = f"{sys.implementation.cache_tag}_torch_{importlib.metadata.version('torch')}"
+    tag = f"{sys.implementation.cache_tag}_torch_{torch.__version__}"
     return os.path.join(OUT_DIR, "_q8_calls_" + "".join(c if c.isalnum() else "_" for c in tag) + ".so")
 
 
 def _build_calls() -> str:
-    """Compiles it. Returns why it could not be compiled (the binding works without it), or an empty string."""
+    """Compiles it to calls_path() + ".tmp". Returns why it could not be compiled (the binding works without it), or an empty
+    string."""
     out = calls_path()
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     cc = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
@@ -54,11 +56,25 @@ def _build_calls() -> str:
            "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
            os.path.join(CSRC, CALLS_SOURCE), "-o", out + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            f"-Wl,-rpath,{lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        return r.stderr[-2000:]
-    os.replace(out + ".tmp", out)
-    return ""
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return str(e)
+    return "" if r.returncode == 0 else r.stderr[-2000:] or f"{cc}: status {r.returncode}"
+
+
+def _install(lib: str, why: str):
+    """Puts a new library in place, and its module of the common calls where that could be compiled (`why` is empty). A module calls
+    the C ABI that it was compiled against, so those of the library before, for other interpreters too, go first."""
+    for old in glob.glob(os.path.join(glob.escape(OUT_DIR), "_q8_calls_*.so")) + [calls_path() + ".none"]:
+        if os.path.exists(old):
+            os.remove(old)
+    os.replace(lib, LIB)
+    if why:
+        open(calls_path() + ".none", "w").close()
+        sys.stderr.write(f"{CALLS_SOURCE} was not built, the binding makes these calls itself: {why}\n")
+    else:
+        os.replace(calls_path() + ".tmp", calls_path())
 
 
 def _flags(verbose: bool):
@@ -102,16 +118,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose and log:
                 sys.stderr.write(log)
         why = calls.result()
-    if why:
-        open(calls_path() + ".none", "w").close()
-        sys.stderr.write(f"{CALLS_SOURCE} was not built, the binding makes these calls itself: {why}\n")
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
            "-Xlinker", "-rpath,/usr/local/cuda/lib64"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    _install(tmp, why)
     for o in objs:
         os.remove(o)
     return LIB
