@@ -42,6 +42,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -149,16 +150,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
 
 
 def _load_calls(lib: ctypes.CDLL):
+    """The module of the common calls, where it is built. One that does not load (built against another PyTorch, say) is reported
+    and not used: the binding makes the same calls."""
     global _calls
     path = _build.calls_path()
     if not os.path.exists(path):
         return
-    loader = importlib.machinery.ExtensionFileLoader("_q8_calls", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_q8_calls", loader))
-    loader.exec_module(module)
-    module.entries(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                     for name in ("q8_quantize_fp4", "q8_swiglu_quantize_fp4", "q8_dequantize_fp4", "q8_gemm_fp4",
-                                  "q8_gemm_fp4_grouped")))
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_q8_calls", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_q8_calls", loader))
+        loader.exec_module(module)
+        module.entries(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                         for name in ("q8_quantize_fp4", "q8_swiglu_quantize_fp4", "q8_dequantize_fp4", "q8_gemm_fp4",
+                                      "q8_gemm_fp4_grouped")))
+    except Exception as e:      # whatever it is, no call depends on this module
+        warnings.warn(f"{path} does not load, the binding makes its calls itself: {e}", RuntimeWarning, stacklevel=3)
+        return
     _calls = module
 
 
