@@ -90,7 +90,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB) or not made:
         return True
     t = min(os.path.getmtime(LIB), max(os.path.getmtime(p) for p in made))
-    headers = ["q8_internal.h", "q8_tc_ptx.cuh", "q8_fp8.h", "q8_fp8_ptx.cuh", "q8_tiles.cuh", "q8_silu.cuh", "q8_fp4.h",
+    headers = ["q8_internal.h", "q8_tc_ptx.cuh", "q8_fp8.h", "q8_fp8_ptx.cuh", "q8_tiles.cuh", "q8_loads.cuh", "q8_silu.cuh", "q8_fp4.h",
                "q8_fp4_ptx.cuh"]
     deps = [os.path.join(CSRC, s) for s in SOURCES + headers + [CALLS_SOURCE]] + [os.path.join(ROOT, "include", "q8.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)

@@ -44,7 +44,8 @@ cudaError_t read_and_clear_gemm_fp4_error(uint32_t* code);
 // The kernels of these operators may start while the one before them on the stream still runs (programmatic stream
 // serialization): each touches global memory only after depend_wait(), which returns once that kernel has completed and its
 // writes can be seen, and then lets the next one start. What overlaps is the set-up and the launch (128x8192x8192 13.4 ->
-// 12.5 us, 2050 rows of 32 experts 34.3 -> 32.8, called one after another).
+// 12.5 us, 2050 rows of 32 experts 34.3 -> 32.8, called one after another). What they read may have been written while they
+// were already there, so it is read by the loads of q8_loads.cuh.
 __device__ __forceinline__ void depend_wait() {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");

@@ -16,6 +16,7 @@
 #include "q8_fp4.h"
 #include "q8_fp4_ptx.cuh"
 #include "q8_internal.h"
+#include "q8_loads.cuh"
 #include "q8_tiles.cuh"
 
 namespace q8 {
@@ -58,9 +59,9 @@ struct TokenScales {
             a[j] = make_uint4(0, 0, 0, 0);
             if (have && lane + 32 * j < n) {
                 if constexpr (kBlock == 16) {
-                    a[j] = __ldg(reinterpret_cast<const uint4*>(p));
+                    a[j] = load128(p);
                 } else {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+                    const uint2 v = load64(p);
                     a[j].x = v.x;
                     a[j].y = v.y;
                 }
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
     const uint32_t first = blockIdx.x / p.split, step = gridDim.x / p.split;
     const int kb0 = KB / p.split * rank + min(rank, KB % p.split);   // this CTA's share of the stages
     const int kb1 = kb0 + KB / p.split + (rank < KB % p.split ? 1 : 0);
-    const Groups groups{p.offsets, cum, p.rows, p.E, TN};
+    const EarlyGroups groups{p.offsets, cum, p.rows, p.E, TN};
 
     if (warp == 0) {
         if (lane == 0) {
@@ -371,12 +372,12 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
             int e, row, n;
             groups.tile((int)(u / (uint32_t)NT), e, row, n);
             const int col = (int)(u % (uint32_t)NT) * TW + quarter * 32 + lane;   // this thread's weight row
-            const float scale = p.sw && col < p.N ? __ldg(p.sw + (int64_t)e * p.N + col) : 1.0f;
+            const float scale = p.sw && col < p.N ? load_float(p.sw + (int64_t)e * p.N + col) : 1.0f;
             if (p.sa) {
 #pragma unroll
                 for (int i = 0; i < (CW + 31) / 32; ++i) {
                     const int j = 32 * i + lane;
-                    if (j < CW) token_scales[j] = t0 + j < n ? __ldg(p.sa + row + t0 + j) : 0.0f;
+                    if (j < CW) token_scales[j] = t0 + j < n ? load_float(p.sa + row + t0 + j) : 0.0f;
                 }
                 __syncwarp();
             }
@@ -712,7 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_sf)) : "memory");
     }
-    const Groups groups{p.offsets, cum, p.rows, p.E, PT};
+    const EarlyGroups groups{p.offsets, cum, p.rows, p.E, PT};
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
     depend_wait();
     if (warp == 2) groups.scan(cum, lane);
@@ -839,9 +840,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             next.row = row + r0;
             next.live = min(32, n - r0);
             next.col0 = nt * PN + part;
-            next.f = p.sa && lane < next.live ? __ldg(p.sa + next.row + lane) : 1.0f;
+            next.f = p.sa && lane < next.live ? load_float(p.sa + next.row + lane) : 1.0f;
             if (p.sw)
-                next.w = own < C::kHalf && next.col0 + own < p.N ? __ldg(p.sw + (int64_t)e * p.N + next.col0 + own) : 0.0f;
+                next.w = own < C::kHalf && next.col0 + own < p.N ? load_float(p.sw + (int64_t)e * p.N + next.col0 + own) : 0.0f;
         };
         if (first < units) fetch(first);
         for (uint32_t u = first; u < units; u += step) {
@@ -1070,7 +1071,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&tmap_sf)) : "memory");
     }
-    const Groups groups{p.offsets, cum, p.rows, p.E, TNP};
+    const EarlyGroups groups{p.offsets, cum, p.rows, p.E, TNP};
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
     depend_wait();
     if (warp == 2) groups.scan(cum, lane);
@@ -1199,8 +1200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             next.live = min(C::kHalf, n - t0);
             next.col0 = nt * TWP + rank * TW + quarter * 32;
             const int col = next.col0 + lane;
-            next.w = p.sw && col < p.N ? __ldg(p.sw + (int64_t)e * p.N + col) : 1.0f;
-            if (p.sa) next.f = own < next.live ? __ldg(p.sa + next.row + own) : 0.0f;
+            next.w = p.sw && col < p.N ? load_float(p.sw + (int64_t)e * p.N + col) : 1.0f;
+            if (p.sa) next.f = own < next.live ? load_float(p.sa + next.row + own) : 0.0f;
         };
         if (first < units) fetch(first);
         for (uint32_t u = first; u < units; u += step) {

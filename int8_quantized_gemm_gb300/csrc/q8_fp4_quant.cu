@@ -8,6 +8,7 @@
 // row's s NaN (the block's c, for blocks of 32), so that a broken value is not hidden.
 #include "q8_fp4.h"
 #include "q8_internal.h"
+#include "q8_loads.cuh"
 #include "q8_silu.cuh"
 
 namespace q8 {
@@ -27,9 +28,10 @@ struct Vec32 {
         if (wide) {
             asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                         : "l"(p));
+                         : "l"(p)
+                         : "memory");
         } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+            const uint4 a = load128(p), b = load128(reinterpret_cast<const uint4*>(p) + 1);
             w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
             w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
         }
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_fp4_kernel(const Args p,
 
     int to = -1;           // kSlots: lane j has the row's slot j
     if constexpr (kForm == kSlots) {
-        if (live && (int)lane < p.top_k) to = __ldg(p.slots + row * p.top_k + lane);
+        if (live && (int)lane < p.top_k) to = load_int(p.slots + row * p.top_k + lane);
         if (to >= p.rows_out) to = -1;
     }
     const bool once = kBlock == 16 && p.vecs <= chunk;
@@ -371,16 +373,15 @@ __device__ __forceinline__ void put32(void* y, const uint32_t (&w)[8], bool wide
 // 53 us (0.96).
 constexpr int kBack = 256, kBackUnroll = 2;
 template <class T>
-__global__ void __launch_bounds__(kBack) dequantize_fp4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
-                                                               const float* __restrict__ s, int block, uint64_t total,
-                                                               uint32_t per_row, uint32_t pitch, uint32_t tile_rows,
-                                                               T* __restrict__ y, bool wide) {
+__global__ void __launch_bounds__(kBack) dequantize_fp4_kernel(const uint8_t* q, const uint8_t* sf, const float* s, int block,
+                                                               uint64_t total, uint32_t per_row, uint32_t pitch,
+                                                               uint32_t tile_rows, T* y, bool wide) {
     depend_wait();
     const uint64_t first = (uint64_t)blockIdx.x * (kBack * kBackUnroll) + threadIdx.x;
     uint4 c[kBackUnroll];
 #pragma unroll
     for (int r = 0; r < kBackUnroll; ++r)
-        c[r] = first + r * kBack < total ? __ldg(reinterpret_cast<const uint4*>(q) + first + r * kBack) : make_uint4(0, 0, 0, 0);
+        c[r] = first + r * kBack < total ? load128(reinterpret_cast<const uint4*>(q) + first + r * kBack) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int r = 0; r < kBackUnroll; ++r) {
         const uint64_t i = first + r * kBack;
@@ -410,13 +411,13 @@ __global__ void __launch_bounds__(kBack) dequantize_fp4_kernel(const uint8_t* __
                             at = ((e * ((tile_rows + 127) / 128) + n / 128) * (pitch / 4) + b / 4) * 512 + (n % 32) * 16 +
                                  n % 128 / 32 * 4 + b % 4;
                         }
-                        const uint32_t v = __ldg(sf + at);
+                        const uint32_t v = load8(sf + at);
                         // 2^-127 is subnormal: its bit is below the exponent's
                         scale[h] = block == 16 ? of_e4m3(v) : v == 255u ? __uint_as_float(0x7fffffffu)
                                                                          : __uint_as_float(v ? v << 23 : 0x400000u);
                     }
                 }
-                if (s) by = __ldg(s + row);
+                if (s) by = load_float(s + row);
             }
             constexpr int kPer = 32 / sizeof(T);       // values of a store
             uint32_t out[8];

@@ -3,6 +3,7 @@
 
 #include "q8_fp8.h"
 #include "q8_fp8_ptx.cuh"
+#include "q8_loads.cuh"
 
 namespace q8 {
 namespace tc {
@@ -11,7 +12,9 @@ namespace tc {
 // [0, rows], so that no offset, whatever its value, leads outside of qa and y. Offsets that fall make ranges overlap, and
 // up to E times the tiles that disjoint ranges have: `units` cuts the work to what those can have, which the host has
 // checked to be below 2^31 (so that no unit's number wraps and no kernel runs for the sum of all overlaps).
-struct Groups {
+// kEarly: the kernel may have started before the one that wrote the offsets was done.
+template <bool kEarly>
+struct GroupsOf {
     const int32_t* offsets;
     const int* cum;   // shared: tiles before group e
     int rows, E, tn;
@@ -20,9 +23,13 @@ struct Groups {
             lo = 0;
             hi = rows;
         } else {
-            lo = min(max(__ldg(offsets + e), 0), rows);
-            hi = min(max(__ldg(offsets + e + 1), lo), rows);
+            lo = min(max(at(e), 0), rows);
+            hi = min(max(at(e + 1), lo), rows);
         }
+    }
+    __device__ __forceinline__ int at(int e) const {
+        if constexpr (kEarly) return load_int(offsets + e);
+        else return __ldg(offsets + e);
     }
     // token tile t -> its group, first row and rows
     __device__ __forceinline__ void tile(int t, int& e, int& row, int& n) const {
@@ -65,6 +72,8 @@ struct Groups {
         if (lane == 0) out[E] = run;
     }
 };
+using Groups = GroupsOf<false>;
+using EarlyGroups = GroupsOf<true>;
 
 __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
     const uint4 u = lds128(addr);
