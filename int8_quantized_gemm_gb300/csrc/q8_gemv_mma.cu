@@ -99,7 +99,7 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[
 // Programmatic dependent launch: the decode kernels are launched so that they may start while
 // the kernel before them on the stream is still running. Nothing they read is touched before
 // griddep_wait(), which returns once the preceding kernel has completed and its writes are
-// visible (at once when there is none), with one exception: when the launch follows the
+// visible (at once when there is none), and then by the loads of q8_loads.cuh, with one exception: when the launch follows the
 // library's own activation quantizer of the same layer (Epilogue::pdl_early_weights, set only by
 // q8_linear and the host-buffer layer, which launch the two back to back and check that the
 // quantizer's outputs do not overlap the weight operands), the first ring of weight (and scale)
@@ -265,12 +265,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int eza0 = 0, eza1 = 0, ecs = 0;
         if (!ep.out_i32) {
             if (em < M) {
-                esa0 = __ldg(ep.s_a + (ep.a_per_row ? em : 0));
-                if (ep.z_a) eza0 = __ldg(ep.z_a + (ep.a_per_row ? em : 0));
+                esa0 = load_float(ep.s_a + (ep.a_per_row ? em : 0));
+                if (ep.z_a) eza0 = load_int(ep.z_a + (ep.a_per_row ? em : 0));
             }
             if (em + 8 < M) {
-                esa1 = __ldg(ep.s_a + (ep.a_per_row ? em + 8 : 0));
-                if (ep.z_a) eza1 = __ldg(ep.z_a + (ep.a_per_row ? em + 8 : 0));
+                esa1 = load_float(ep.s_a + (ep.a_per_row ? em + 8 : 0));
+                if (ep.z_a) eza1 = load_int(ep.z_a + (ep.a_per_row ? em + 8 : 0));
             }
         }
         int tot[8][4];
@@ -395,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rb[i1] = 0;
                 const int n = ((int)blockIdx.x + ti * (int)gridDim.x) * RW + er;
                 if (n < N && !ep.out_i32) {
-                    esw = __ldg(ep.s_w + (ep.w_per_row ? n : 0));
-                    if (ep.z_a) ecs = __ldg(ep.colsum + n);
+                    esw = load_float(ep.s_w + (ep.w_per_row ? n : 0));
+                    if (ep.z_a) ecs = load_int(ep.colsum + n);
                 }
                 if (n < N) {
                     if (ep.out_i32) {
@@ -405,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         if (em < M)
                             epi_store(ep, (int64_t)em * N + n,
-                                      epi_bias(ep, __fmul_rn(__int2float_rn(v0 - eza0 * ecs), __fmul_rn(esa0, esw)), n));
+                                      epi_bias<true>(ep, __fmul_rn(__int2float_rn(v0 - eza0 * ecs), __fmul_rn(esa0, esw)), n));
                         if (em + 8 < M)
                             epi_store(ep, (int64_t)(em + 8) * N + n,
-                                      epi_bias(ep, __fmul_rn(__int2float_rn(v1 - eza1 * ecs), __fmul_rn(esa1, esw)), n));
+                                      epi_bias<true>(ep, __fmul_rn(__int2float_rn(v1 - eza1 * ecs), __fmul_rn(esa1, esw)), n));
                     }
                 }
             }
@@ -554,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int em = ct / RW, er = ct % RW;   // epilogue outputs: tokens em, em + 8 of row er
         float esa0 = 0.0f, esa1 = 0.0f;
         griddep_wait();   // the token scales come from the quantizer
-        if (em < M) esa0 = __ldg(ep.s_a + (ep.a_per_row ? em : 0));
-        if (em + 8 < M) esa1 = __ldg(ep.s_a + (ep.a_per_row ? em + 8 : 0));
+        if (em < M) esa0 = load_float(ep.s_a + (ep.a_per_row ? em : 0));
+        if (em + 8 < M) esa1 = load_float(ep.s_a + (ep.a_per_row ? em + 8 : 0));
         float part[8][4];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -629,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int n = ((int)blockIdx.x + ti * (int)gridDim.x) * RW + er;
                 if (n < N) {
-                    if (em < M) epi_store(ep, (int64_t)em * N + n, epi_bias(ep, __fmul_rn(T0, esa0), n));
-                    if (em + 8 < M) epi_store(ep, (int64_t)(em + 8) * N + n, epi_bias(ep, __fmul_rn(T1, esa1), n));
+                    if (em < M) epi_store(ep, (int64_t)em * N + n, epi_bias<true>(ep, __fmul_rn(T0, esa0), n));
+                    if (em + 8 < M) epi_store(ep, (int64_t)(em + 8) * N + n, epi_bias<true>(ep, __fmul_rn(T1, esa1), n));
                 }
                 named_barrier(1, 32 * kComputeWarps);   // the slots are free for the next tile
             }

@@ -5,6 +5,8 @@
 #include <stdint.h>
 #ifdef __CUDACC__
 #include <cuda_bf16.h>
+
+#include "q8_loads.cuh"
 #endif
 
 #include "../../include/q8.h"
@@ -94,8 +96,11 @@ struct Epilogue {
 };
 
 #ifdef __CUDACC__
+// kEarly: in a kernel that may have started before the one that wrote the bias was done.
+template <bool kEarly = false>
 __device__ __forceinline__ float epi_bias(const Epilogue& ep, float v, int64_t n) {
-    return ep.bias ? __fadd_rn(v, __ldg(ep.bias + n)) : v;
+    if constexpr (kEarly) return ep.bias ? __fadd_rn(v, load_float(ep.bias + n)) : v;
+    else return ep.bias ? __fadd_rn(v, __ldg(ep.bias + n)) : v;
 }
 
 __device__ __forceinline__ void epi_store(const Epilogue& ep, int64_t idx, float v) {
