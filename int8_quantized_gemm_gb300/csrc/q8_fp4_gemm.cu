@@ -128,8 +128,8 @@ __device__ __forceinline__ bool feed_scales(const uint8_t* sf, int64_t row0, int
 }
 
 // ------------------------------------------------------------------------ weights on the MMA's M side
-// For few tokens a matrix: a tile is 128 weight rows x up to TN = 16, 32, 64 or 128 token rows, so that a weight
-// matrix is read once whatever the tokens. Bound by the weights' bytes.
+// For few tokens a matrix: a tile is 128 weight rows x up to TN = 16 or 32 token rows, so that a weight matrix is read from
+// memory once (a group of more tokens than a tile reads it again from L2). Bound by the weights' bytes.
 //   warp 0     TMA: weights [128 x 256 codes] with their scales and tokens [n x 256 codes] of each stage
 //   warp 1     MMA issuer (N = n rounded up to 16), TMEM
 //   warps 2, 3 scales of the stage's tokens, every other stage each
@@ -155,7 +155,8 @@ __device__ __forceinline__ void sts_value(uint32_t addr, float f) {
         asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(__float_as_uint(f)) : "memory");
 }
 
-constexpr int kSwapEpi = 2048 + 64;    // of a drain warp: 2 KB of values on their way out, the scales of up to 16 tokens
+constexpr int kSwapTokens = 16;        // of a drain warp, at most
+constexpr int kSwapEpi = 2048 + 4 * kSwapTokens;   // of a drain warp: 2 KB of values on their way out, its tokens' scales
 
 // acc[j]: weight row (column of y) col0 + lane, token t0 + j, as store_tokens; y's rows are whole 16-byte chunks. 2 KB of
 // tokens x 32 columns at a time are turned round in shared memory, so that a token's columns leave 16 bytes a lane (with
@@ -203,8 +204,9 @@ struct SwapArgs {
 template <int CW, int kBlock>   // tokens of a drain warp; TN = 2 CW
 struct SwapCfg {
     using S = Scales<kBlock>;
+    static_assert(CW <= kSwapTokens, "above the room for a drain warp's token scales");
     static constexpr int TN = 2 * CW;
-    static constexpr int kBox = TN < 32 ? TN : 32;              // token rows of a TMA box
+    static constexpr int kBox = TN;                             // token rows of the TMA box
     static constexpr int kOffTokens = TW * kRowBytes;
     static constexpr int kOffSfw = kOffTokens + TN * kRowBytes;
     static constexpr int kOffSfa = kOffSfw + S::kBytes;
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
             for (uint32_t u = first; u < units && ok; u += step) {
                 int e, row, n;
                 groups.tile((int)(u / (uint32_t)NT), e, row, n);
-                const int nt = (int)(u % (uint32_t)NT), wrow = e * p.N + nt * TW, boxes = (n + C::kBox - 1) / C::kBox;
+                const int nt = (int)(u % (uint32_t)NT), wrow = e * p.N + nt * TW;
                 const int sfrow = (e * NT + nt) * KB * (S::kAtoms * 4);     // tiles of scales as rows of 128 bytes
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(bar_empty + 8 * s, phase, abort_flag, kErrProducer, &g_fp4_error)) {
@@ -297,12 +299,10 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
                         break;
                     }
                     const uint32_t dst = sbase + s * C::kStage, bar = bar_full + 8 * s;
-                    mbar_expect_tx(bar, C::kOffTokens + S::kBytes + boxes * C::kBox * kRowBytes);
+                    mbar_expect_tx(bar, C::kOffTokens + S::kBytes + C::kBox * kRowBytes);
                     tma_load_2d(dst, &tmap_w, kb * kRowBytes, wrow, bar);
                     tma_load_2d(dst + C::kOffSfw, &tmap_sf, 0, sfrow + kb * (S::kAtoms * 4), bar);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(dst + C::kOffTokens + b * C::kBox * kRowBytes, &tmap_a, kb * kRowBytes, row + b * C::kBox,
-                                    bar);
+                    tma_load_2d(dst + C::kOffTokens, &tmap_a, kb * kRowBytes, row, bar);
                     if (++s == (uint32_t)p.stages) { s = 0; phase ^= 1; }
                 }
             }
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
         for (uint32_t u = first; u < units && ok; u += step) {
             int e, row, n;
             groups.tile((int)(u / (uint32_t)NT), e, row, n);
-            ok = feed_scales<kBlock, (TN + 31) / 32>(
+            ok = feed_scales<kBlock, 1>(
                 p.sfa, row, n, p.pitch, p.K / kBlock, kb0, kb1, count, warp - 2, p.stages, s, phase, bar_empty, abort_flag, lane,
                 [&](uint32_t st) { return sbase + st * C::kStage + C::kOffSfa; },
                 [&](uint32_t st) { mbar_arrive(bar_full + 8 * st); });
@@ -374,11 +374,7 @@ __global__ void __launch_bounds__(kSwapThreads, 1)
             const int col = (int)(u % (uint32_t)NT) * TW + quarter * 32 + lane;   // this thread's weight row
             const float scale = p.sw && col < p.N ? load_float(p.sw + (int64_t)e * p.N + col) : 1.0f;
             if (p.sa) {
-#pragma unroll
-                for (int i = 0; i < (CW + 31) / 32; ++i) {
-                    const int j = 32 * i + lane;
-                    if (j < CW) token_scales[j] = t0 + j < n ? load_float(p.sa + row + t0 + j) : 0.0f;
-                }
+                if (lane < CW) token_scales[lane] = t0 + lane < n ? load_float(p.sa + row + t0 + lane) : 0.0f;
                 __syncwarp();
             }
             if (!warp_wait(bar_accfull + 8 * buf, bphase, abort_flag, kErrDrain)) break;

@@ -120,6 +120,8 @@ struct Args {
 // A row is held by blockDim.x threads, kUnroll vectors of 32 bytes each, all loads first; blockDim.y rows a CTA, some in a
 // warp where they are short. Blocks of 16 need the row's maximum before the first code: rows of up to 512 threads' vectors
 // (32768 elements of 16 bits, 16384 of 32) stay in registers, as they were read; longer ones are read a second time, from L2.
+// The gated form holds the activation instead, of rows of up to 16384 elements for 16-bit h and 4096 for fp32; longer ones are
+// read and activated twice.
 // Bound by memory. On the device, of the measured copy bandwidth: 8192 x 16384 fp32 91 us (0.99), bf16 51.5 (0.98; two
 // vectors a thread 66); 16384 x 4096 bf16 26.8 (0.95); the gated form, 32768 x 2048 bf16, 47.4 (0.95) with CTAs of 64 threads
 // (48.0 with 128, 49.5 with 256) and two vectors a thread (one 58); its fp32 form keeps one (42.6 us for 16384 x 2048, two

@@ -413,11 +413,11 @@ bool make_tma_map_i8_sw64(CUtensorMap* map, const int8_t* base, int64_t rows, in
 // Output map for TMA stores of a row-major [rows, cols] matrix of fp32, int32, bf16 or int8:
 // box [32 rows, 128 bytes of columns] with the 128-byte swizzle. False unless the row pitch
 // is a multiple of 16 bytes and the base is 16-byte aligned.
+enum { kMapF32 = 0, kMapI32 = 1, kMapBF16 = 2, kMapI8 = 3 };
+bool make_tma_map_out(CUtensorMap* map, void* base, int kind, int64_t rows, int64_t cols);
 // Output map for TMA stores of a row-major [rows, cols] matrix of elements of 2 or 4 bytes: box [box_rows, box_cols], rows side by
 // side in shared memory. False unless the row pitch is a multiple of 16 bytes and the base is 16-byte aligned.
 bool make_tma_map_box(CUtensorMap* map, void* base, int size, int64_t rows, int64_t cols, int box_cols, int box_rows);
-enum { kMapF32 = 0, kMapI32 = 1, kMapBF16 = 2, kMapI8 = 3 };
-bool make_tma_map_out(CUtensorMap* map, void* base, int kind, int64_t rows, int64_t cols);
 int device_sm_count();
 
 }  // namespace q8
