@@ -136,9 +136,10 @@ __device__ __forceinline__ bool feed_scales(const uint8_t* sf, int64_t row0, int
 //   warps 4-11 drain: two warps for each quarter of the TMEM lanes (weight rows), half of the tokens each
 // With few tiles, a cluster of S CTAs splits a tile's stages; each CTA sends the partial sums of the tokens it does not own
 // to the CTA that does (st.async), which adds them in the order of the ranks: the same bits every time, no workspace and no
-// second launch. Measured, called one after another: 16x28672x8192 24.5 us (5.4 TB/s: two CTAs share a tile so that 224 tiles
-// fill three rounds; launch, set-up, the first load and the last exchange are about 4.5 us), 128 rows of 64 experts, 4096 x
-// 4096, blocks of 32, 88.4 us (0.95 of the measured copy bandwidth on the active weights), 1x4096x4096 5.5 us.
+// second launch. Measured, called one after another from Python with three sets of operands in turn (in brackets in a graph
+// with two): 16x28672x8192 25.3 to 25.6 us (24.5), 5.2 TB/s, 0.77 of the measured copy bandwidth (two CTAs share a tile so that
+// 224 tiles fill three rounds; launch, set-up, the first load and the last exchange are about 4.5 us); 128 rows of 64 experts,
+// 4096 x 4096, blocks of 32, 86.6 to 87.7 us (0.96 on the active weights); 1x4096x4096 6.1 us (5.6).
 constexpr int kSwapThreads = 384;
 constexpr int kDrainWarps = 8;
 constexpr int kBufs = 2;               // accumulator buffers: the next tile's MMAs run while one is written out
@@ -564,9 +565,9 @@ cudaError_t launch_swap(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 //   warps 2, 3 scales of the CTA's token rows, every other stage each
 //   warps 4-11 drain: a TMEM lane is a token row; two warps for each quarter of the lanes, 128 columns each
 // The accumulator takes 256 of the 512 TMEM columns and five stages' scales 240, so there is one: the next tile's MMAs wait
-// until the drain warps have read it into registers, and run while they write it out. Measured: 8192x8192x16384 304 us from a
-// cool start (7.2 PFLOP/s, 3.8 times the measured bf16 rate), 355 us back to back, where the power cap holds the SM clock
-// near 1.5 GHz; blocks of 32 287 and 324 us. A stage takes 525 to 540 clocks there against 512 of MMA; without the loads 514,
+// until the drain warps have read it into registers, and run while they write it out. Measured: 8192x8192x16384 306 us from a
+// cool start (7.2 PFLOP/s, 3.8 times the measured bf16 rate), 348 to 357 us back to back, where the power cap holds the SM clock
+// near 1.5 GHz; blocks of 32 294 and 317 to 322 us. A stage takes 525 to 540 clocks there against 512 of MMA; without the loads 514,
 // and as many more clocks a second (252 us with neither loads nor stores: wrong results), so it is the power of what is moved
 // that costs. A tile costs some 2500 clocks besides: the hand-over of the accumulator about half, the rest waits for loads
 // behind the burst of stores (8192x8192x4096 95 us, 81 without its stores: wrong results). Tried: stores paced over the tile
@@ -965,8 +966,10 @@ cudaError_t launch_pair(const Fp4Product& g, int64_t tiles, cudaStream_t stream)
 //   warp 1     even CTA: pair MMA issuer; TMEM in both
 //   warps 2, 3 scales of the tile's tokens, every other stage each
 //   warps 4-11 drain: a TMEM lane is a weight row (a column of y); two warps for each quarter of the lanes, 64 tokens each
-// Bound by the weights' bytes, or by latencies where there is one round of tiles. Measured: 2050 rows of 32 experts, 4096 x
-// 2048, 32.3 us (5.3 TB/s), 2048 rows of 64, 4096 x 4096, 99 us (6.3 TB/s), 64x8192x8192 10.9 us, 256x8192x8192 14.2 us. With
+// Bound by the weights' bytes, or by latencies where there is one round of tiles. Measured, called one after another from Python
+// with three sets of operands in turn (in a graph with two in brackets): 2050 rows of 32 experts, 4096 x 2048, 32.9 to 33.3 us
+// (32.5), 5.2 TB/s, 2048 rows of 64, 4096 x 4096, 97 us (99), 6.4 TB/s, 64x8192x8192 12.9 us (11.0: L2 holds two sets), 256x8192x8192
+// 15.3 to 15.5 us (14.0). With
 // 256 tokens a tile it would do the work of the pairs above with less waste in experts' last tiles, but the scales of 256
 // token rows in each CTA take longer than the MMAs (8192x8192x4096 130 us against 95).
 constexpr int TWP = 256, TNP = 128;               // weight rows of a tile, token rows at most
@@ -1305,7 +1308,8 @@ cudaError_t launch(const Fp4Product& p, cudaStream_t stream) {
     // tokens over 152 CTAs, 0.24 (0.20 for up to 64 tokens) and 1.0 for 256 x 128 over 76 pairs, 0.31 and 1.6 for 256 x
     // 256; and once for each kernel 4.2, 5 and 6. A group's last tile is half full on average. Weights that are not in L2
     // take their time to be read whatever the tile, and the pairs with the smaller one wait less for them. Measured, us,
-    // in the same order: 128x2048x2048 6.7 / 8.4 / 9.1; 64x8192x8192 12.9 / 10.9 / 14.1; 256x8192x8192 39 / 13.9 / 16.6;
+    // in the same order, in a graph with two sets of operands in turn, which L2 holds: 128x2048x2048 6.7 / 8.4 / 9.1;
+    // 64x8192x8192 11.4 / 11.0 / 14.1; 128x8192x8192 19.1 / 12.8 / 14.8; 256x8192x8192 39 / 14.0 / 16.6;
     // 512x8192x8192 - / 23.3 / 18.3; 2050 rows of 32 experts, 4096x2048, 55 / 34.6 / 35.7; 8192 rows of 8, 4096x4096, - /
     // 74 / 53.
     int narrow = 0, wide = 0;
