@@ -1300,7 +1300,10 @@ cudaError_t launch(const Fp4Product& p, cudaStream_t stream) {
     auto tiles = [&](int tn) { return p.offsets ? p.rows / tn + (p.E < p.rows ? p.E : p.rows) : (p.rows + tn - 1) / tn; };
     // The kernels count tiles in 32 bits, whatever the offsets are (each group at most all rows).
     if (tiles(16) * NT >= (1LL << 31) - 1024 || (p.rows / 16 + 1) * p.E >= (1LL << 31)) return cudaErrorNotSupported;
-    // Groups of unequal size: a tile four times the average leaves few of them more than one.
+    // Groups of unequal size: a tile four times the average leaves few of them more than one. The host does not see the offsets, so
+    // a group far above the average reads its weights again from L2 for each of its tiles. Measured, us, for tiles of 16 and 32
+    // tokens and the pairs' 128: 512 rows of 128 experts, 4096x4096, evenly 179 / 180 / 181; the largest with 94 rows 176 / 173 / 173,
+    // with 300 191 / 183 / 181, with all 35 / 23 / 12; 2048x2048, evenly 50.9 / 51.3 / 53.4, 300 rows 54.0 / 52.4 / 52.7.
     const int64_t most = p.offsets ? 4 * per : per;
     if (most <= 16) return launch_swap<8, kBlock>(p, tiles(16), stream);
     if (most <= 32) return launch_swap<16, kBlock>(p, tiles(32), stream);
